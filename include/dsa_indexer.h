@@ -104,7 +104,8 @@ typedef enum {
   DSA_ERR_CUDA = 4,
   DSA_ERR_TIMEOUT = 5,
   DSA_ERR_BAD_PAGE = 6,
-  DSA_ERR_BAD_SEQLEN = 7
+  DSA_ERR_BAD_SEQLEN = 7,
+  DSA_ERR_BAD_POSITION = 8
 } dsa_status_t;
 
 /*
@@ -294,6 +295,140 @@ int dsa_indexer_topk_decode_static(const void* q, const float* w, const void* kc
 int dsa_kcache_store(const void* k, const int* slot_mapping, int n, void* kcache,
                      long long page_stride_bytes, int num_pages, int kv_dtype,
                      int D, int page_size, int* dev_status, void* stream);
+
+/*
+ * ---- Around the sparse attention: norm + rotation, latent cache, attention --
+ *
+ * The common rules above hold (device pointers, no allocation, no
+ * synchronisation, programmatic dependent launch, host errors by return
+ * value before any launch, data errors by atomicMax into *dev_status).
+ * Strides are in elements of the array they belong to.  A rope_table is fp32
+ * [max_pos, rot] contiguous: row t holds rot/2 cosines, then rot/2 sines, of
+ * the angles of position t.  A rotation turns the pair (a, b) into
+ * (a cos - b sin, b cos + a sin); pair i is (x[i], x[i + rot/2]), or
+ * (x[2i], x[2i + 1]) when `interleaved` is not 0.
+ */
+typedef enum { DSA_BF16 = 0, DSA_FP16 = 1, DSA_FP32 = 2 } dsa_dtype_t;
+typedef enum { DSA_NORM_NONE = 0, DSA_NORM_RMS = 1, DSA_NORM_LAYER = 2 } dsa_norm_t;
+
+/*
+ * Per-head norm of queries and keys, with the position rotation in the same
+ * pass.  Row (t, h) of q starts at q + t * q_token_stride + h *
+ * q_head_stride and holds D contiguous values (k alike); the results go to
+ * q_out and k_out, which may be q and k themselves (same strides) but must
+ * not overlap them in any other way.  Per row, every step in fp32 with one
+ * rounding at the end:
+ *   DSA_NORM_RMS    y = x * rsqrt(mean(x^2) + eps) * weight + bias
+ *   DSA_NORM_LAYER  y = (x - mean) * rsqrt(var + eps) * weight + bias
+ *   DSA_NORM_NONE   y = x (weights and biases unused)
+ * then values [rot_offset, rot_offset + rot_dims) are rotated by
+ * positions[t].  weight, bias: fp32 [D] per side, nullable (1 and 0).
+ * positions NULL: no rotation.  Hq or Hk may be 0 (that side's pointers are
+ * not used).  8 <= D <= 256, a multiple of 8; rot_dims a multiple of 16
+ * (interleaved: of 8), rot_offset of 8 (DSA_ERR_UNSUPPORTED).  Arrays and
+ * rows 16-byte aligned, rope_table too (DSA_ERR_MISALIGNED).  A position
+ * outside [0, max_pos) is a data error: that token's rows are NaN, status
+ * DSA_ERR_BAD_POSITION.
+ */
+int dsa_qk_norm_rope(const void* q, long long q_token_stride, long long q_head_stride, int Hq,
+                     const void* k, long long k_token_stride, long long k_head_stride, int Hk,
+                     int T, int D, int dtype, int norm, const float* q_weight,
+                     const float* k_weight, const float* q_bias, const float* k_bias, float eps,
+                     const int* positions, const float* rope_table, int max_pos, int rot_dims,
+                     int rot_offset, int interleaved, void* q_out, long long qo_token_stride,
+                     long long qo_head_stride, void* k_out, long long ko_token_stride,
+                     long long ko_head_stride, int* dev_status, void* stream);
+
+/*
+ * The latent cache: per token one latent vector (latent_dim = 512 values)
+ * and one rotated part (rope_dim = 64 values) that all heads share, in pages
+ * of 64 tokens.
+ *   DSA_KV_BF16      token s of a page: 576 bf16 values at page + s * 1152
+ *                    (page_stride_bytes >= 73,728).
+ *   DSA_KV_FP8_E4M3  512 e4m3 codes at page + s * 512, the rotated part as 64
+ *                    bf16 at page + 32768 + s * 128, four fp32 scales at page
+ *                    + 40960 + s * 16, one per 128 latent values
+ *                    (page_stride_bytes >= 41,984).  Value = code * scale.
+ *
+ * Store: n new tokens into their slots (slot_mapping as for
+ * dsa_kcache_store: page * 64 + slot, negative = skip, past the pool =
+ * skipped with DSA_ERR_BAD_PAGE, equal slots race).  latent: bf16, row i at
+ * latent + i * latent_stride; rope alike.  norm_weight (fp32 [512],
+ * nullable): the latent is first normalised, c * rsqrt(mean(c^2) + eps) *
+ * norm_weight.  positions (nullable): the rotated part is turned by
+ * positions[i] (rope_table's rot = 64).  Every step is fp32.  The fp8 scale
+ * of a group is 2^e with the smallest e for which its largest finite
+ * magnitude is at most 448 * 2^e (e >= -126; 1 for a group of zeros), the codes
+ * round to nearest even, infinities become +-448 and NaN stays NaN; a power
+ * of two keeps code * scale exact in bf16.  A bad position makes the rotated
+ * part NaN, status DSA_ERR_BAD_POSITION.
+ */
+int dsa_latent_store(const void* latent, long long latent_stride, const void* rope,
+                     long long rope_stride, int n, int latent_dim, int rope_dim,
+                     const float* norm_weight, float eps, const int* positions,
+                     const float* rope_table, int max_pos, int interleaved,
+                     const int* slot_mapping, void* cache, long long page_stride_bytes,
+                     int num_pages, int kv_dtype, int page_size, int* dev_status, void* stream);
+
+/*
+ * Load: ranges of tokens back as packed bf16 rows of 576 values (latent,
+ * then rotated part).  Output row i (out + i * out_stride) belongs to the
+ * request r with cu_rows[r] <= i < cu_rows[r + 1] and holds its position
+ * starts[r] + i - cu_rows[r] (starts NULL: 0), read through block-table row
+ * r.  cu_rows: DEVICE int32 [n_req + 1], non-decreasing.  Rows i < n of no
+ * request are zeros.  An fp8 value is code * scale rounded to bf16 (exact
+ * for the scales that the store writes).  A position outside [0, W * 64)
+ * gives a NaN row and DSA_ERR_BAD_SEQLEN, a page outside the pool a NaN row
+ * and DSA_ERR_BAD_PAGE.
+ */
+int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_pages, int kv_dtype,
+                    int page_size, const int* block_table, long long bt_stride, int W,
+                    const int* starts, const int* cu_rows, int n_req, int n, int latent_dim,
+                    int rope_dim, void* out, long long out_stride, int* dev_status, void* stream);
+
+/*
+ * Attention over the latent cache in the absorbed form.  For row r (a decode
+ * request, or a prefill query token) and head h < H:
+ *     s[t] = scale * (q_latent[r, h] . c[t] + q_rope[r, h] . k[t])
+ *     out[r, h, :] = sum_t softmax(s)[t] c[t],   lse[r, h] = log sum_t exp(s[t])
+ * with c[t] the 512 latent values and k[t] the rotated part of position t of
+ * the row's block-table row.  The visible positions are t < seqlens[r]
+ * (idx NULL), or those of the row's selection list: entries idx[r * idx_stride
+ * + j], j < min(k, seqlens[r]), that are not negative and below seqlens[r]
+ * (the lists that the top-k calls write: valid entries first, then -1; an
+ * entry that is repeated counts as often).  A row without a visible position
+ * gives zeros and lse = -inf.
+ *   q_latent  bf16 [rows, H, 512], q_rope bf16 [rows, H, 64] through their
+ *             row and head strides, values contiguous; 1 <= H <= 128.
+ *   out       bf16 [rows, H, 512] through its strides; lse fp32 [rows, H]
+ *             contiguous, nullable.
+ *   block_table, bt_stride, seqlens  as for the indexer calls (bt_stride = 0:
+ *             all rows share row 0).
+ *   workspace fp32, at least dsa_latent_attention_workspace() floats for the
+ *             current device, 16-byte aligned; calls that may overlap need
+ *             one each.
+ * The softmax and all sums are fp32; the weights of the value product are
+ * rounded to bf16.  The launch shape depends on H alone, so a captured call
+ * may be replayed with other lengths, lists and tables.  Two kernel launches.
+ * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
+ * visible position without a page in the pool a NaN row and
+ * DSA_ERR_BAD_PAGE; a wait that runs out DSA_ERR_TIMEOUT and NaN rows.
+ * rows * max(W, ceil(k / 64)) must be below 2^31 (DSA_ERR_UNSUPPORTED).
+ */
+int dsa_latent_attention(const void* q_latent, long long ql_row_stride, long long ql_head_stride,
+                         const void* q_rope, long long qr_row_stride, long long qr_head_stride,
+                         int rows, int H, int latent_dim, int rope_dim, float scale,
+                         const void* cache, long long page_stride_bytes, int num_pages,
+                         int kv_dtype, int page_size, const int* block_table, long long bt_stride,
+                         int W, const int* seqlens, const int* idx, long long idx_stride, int k,
+                         void* out, long long out_row_stride, long long out_head_stride,
+                         float* lse, float* workspace, long long workspace_floats,
+                         int* dev_status, void* stream);
+
+/* Floats of workspace that dsa_latent_attention needs on the current device
+ * (two partial rows of 64 heads and a split record per SM); -1 when there is
+ * no device. */
+long long dsa_latent_attention_workspace(void);
 
 /* A static, human-readable name for a status code. */
 const char* dsa_status_string(int status);

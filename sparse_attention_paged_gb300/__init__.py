@@ -25,7 +25,7 @@ PAGE = 64
 STATUS = {
     0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED",
     3: "DSA_ERR_MISALIGNED", 4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT",
-    6: "DSA_ERR_BAD_PAGE", 7: "DSA_ERR_BAD_SEQLEN",
+    6: "DSA_ERR_BAD_PAGE", 7: "DSA_ERR_BAD_SEQLEN", 8: "DSA_ERR_BAD_POSITION",
 }
 
 
@@ -169,4 +169,279 @@ def indexer_logits(kind: str, q, w, kcache, kscale, page_stride_bytes, num_pages
             bt_stride, seqlens, rows, H, D, PAGE, W, out, out.stride(0), dev_status, stream)
     if st != 0:
         raise DsaError(st)
+    return out
+
+
+# ---- around the sparse attention: norm + rotation, latent cache, attention ----
+
+BF16 = 0
+FP16 = 1
+FP32 = 2
+NORM_NONE = 0
+NORM_RMS = 1
+NORM_LAYER = 2
+LATENT = 512
+ROPE = 64
+LATENT_PAGE_BYTES = {KV_FP8_E4M3: 41984, KV_BF16: 73728}
+
+
+def dsa_qk_norm_rope(q, q_token_stride, q_head_stride, Hq, k, k_token_stride, k_head_stride, Hk,
+                     T, D, dtype, norm, q_weight, k_weight, q_bias, k_bias, eps, positions,
+                     rope_table, max_pos, rot_dims, rot_offset, interleaved, q_out,
+                     qo_token_stride, qo_head_stride, k_out, ko_token_stride, ko_head_stride,
+                     dev_status=None, stream=None) -> int:
+    """C ``dsa_qk_norm_rope``; returns its status code."""
+    return _native.load().dsa_qk_norm_rope(
+        _p(q), q_token_stride, q_head_stride, Hq, _p(k), k_token_stride, k_head_stride, Hk, T, D,
+        dtype, norm, _p(q_weight), _p(k_weight), _p(q_bias), _p(k_bias), eps, _p(positions),
+        _p(rope_table), max_pos, rot_dims, rot_offset, int(interleaved), _p(q_out),
+        qo_token_stride, qo_head_stride, _p(k_out), ko_token_stride, ko_head_stride,
+        _p(dev_status), _stream(stream))
+
+
+def dsa_latent_store(latent, latent_stride, rope, rope_stride, n, latent_dim, rope_dim,
+                     norm_weight, eps, positions, rope_table, max_pos, interleaved, slot_mapping,
+                     cache, page_stride_bytes, num_pages, kv_dtype, page_size, dev_status=None,
+                     stream=None) -> int:
+    """C ``dsa_latent_store``; returns its status code."""
+    return _native.load().dsa_latent_store(
+        _p(latent), latent_stride, _p(rope), rope_stride, n, latent_dim, rope_dim,
+        _p(norm_weight), eps, _p(positions), _p(rope_table), max_pos, int(interleaved),
+        _p(slot_mapping), _p(cache), page_stride_bytes, num_pages, kv_dtype, page_size,
+        _p(dev_status), _stream(stream))
+
+
+def dsa_latent_load(cache, page_stride_bytes, num_pages, kv_dtype, page_size, block_table,
+                    bt_stride, W, starts, cu_rows, n_req, n, latent_dim, rope_dim, out,
+                    out_stride, dev_status=None, stream=None) -> int:
+    """C ``dsa_latent_load``; returns its status code."""
+    return _native.load().dsa_latent_load(
+        _p(cache), page_stride_bytes, num_pages, kv_dtype, page_size, _p(block_table), bt_stride,
+        W, _p(starts), _p(cu_rows), n_req, n, latent_dim, rope_dim, _p(out), out_stride,
+        _p(dev_status), _stream(stream))
+
+
+def dsa_latent_attention(q_latent, ql_row_stride, ql_head_stride, q_rope, qr_row_stride,
+                         qr_head_stride, rows, H, latent_dim, rope_dim, scale, cache,
+                         page_stride_bytes, num_pages, kv_dtype, page_size, block_table,
+                         bt_stride, W, seqlens, idx, idx_stride, k, out, out_row_stride,
+                         out_head_stride, lse, workspace, workspace_floats, dev_status=None,
+                         stream=None) -> int:
+    """C ``dsa_latent_attention``; returns its status code."""
+    return _native.load().dsa_latent_attention(
+        _p(q_latent), ql_row_stride, ql_head_stride, _p(q_rope), qr_row_stride, qr_head_stride,
+        rows, H, latent_dim, rope_dim, scale, _p(cache), page_stride_bytes, num_pages, kv_dtype,
+        page_size, _p(block_table), bt_stride, W, _p(seqlens), _p(idx), idx_stride, k, _p(out),
+        out_row_stride, out_head_stride, _p(lse), _p(workspace), workspace_floats,
+        _p(dev_status), _stream(stream))
+
+
+def dsa_latent_attention_workspace() -> int:
+    """C ``dsa_latent_attention_workspace``: floats for the current device, -1 without one."""
+    return int(_native.load().dsa_latent_attention_workspace())
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _ints(x, name, shape=None):
+    import torch
+    _need(x.dtype is torch.int32 and x.is_contiguous(), f"{name}: contiguous int32 expected")
+    _need(shape is None or tuple(x.shape) == shape, f"{name}: shape {shape} expected")
+    return x
+
+
+def _floats(x, name, shape):
+    import torch
+    if x is not None:
+        _need(x.dtype is torch.float32 and x.is_contiguous() and tuple(x.shape) == shape,
+              f"{name}: contiguous float32 of shape {shape} expected")
+    return x
+
+
+def _pool(cache, kv_dtype):
+    """(page stride in bytes, pages) of a pool: uint8 [pages, page bytes], rows contiguous."""
+    import torch
+    _need(cache.dtype is torch.uint8 and cache.dim() == 2 and cache.stride(1) == 1,
+          "cache: uint8 [pages, page bytes] expected")
+    _need(kv_dtype in LATENT_PAGE_BYTES, "kv_dtype: KV_FP8_E4M3 or KV_BF16")
+    _need(cache.shape[1] >= LATENT_PAGE_BYTES[kv_dtype], "cache: rows shorter than a page")
+    return (cache.stride(0) if cache.shape[0] > 1 else cache.shape[1]), cache.shape[0]
+
+
+def _table_rows(block_table, rows, name="block_table"):
+    """(stride, W) of an int32 [rows, W] table, or of one shared row [W] or [1, W]."""
+    import torch
+    _need(block_table.dtype is torch.int32 and block_table.dim() in (1, 2)
+          and block_table.stride(-1) == 1, f"{name}: int32 [rows, W] expected")
+    W = block_table.shape[-1]
+    if block_table.dim() == 1 or block_table.shape[0] == 1:
+        return 0, W
+    _need(block_table.shape[0] == rows, f"{name}: one row, or one per request")
+    return block_table.stride(0), W
+
+
+def _check(status):
+    if status != 0:
+        raise DsaError(status)
+
+
+_DTYPES = None
+
+
+def _dtype(t):
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+    code = _DTYPES.get(t.dtype)
+    _need(code is not None, f"{t.dtype}: bfloat16, float16 or float32 expected")
+    return code
+
+
+def rope_table(max_pos, rot_dims, base=10000.0, device="cuda"):
+    """The fp32 [max_pos, rot_dims] table of the rotations: per position rot_dims/2 cosines, then
+    the sines, of position * base^(-2i/rot_dims); the angles are taken in 64 bits."""
+    import torch
+    freq = float(base) ** (-torch.arange(0, rot_dims, 2, dtype=torch.float64, device=device) / rot_dims)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], dim=1).float()
+
+
+def qk_norm_rope(q, k, positions=None, table=None, *, rot_dims=None, rot_offset=0,
+                 interleaved=False, norm=NORM_RMS, q_weight=None, k_weight=None, q_bias=None,
+                 k_bias=None, eps=1e-6, q_out=None, k_out=None, dev_status=None, stream=None):
+    """Norm and rotate queries [T, Hq, D] and keys [T, Hk, D] per head, in one kernel.
+
+    The last dimension is contiguous, the others may be strided; ``k`` may be None.  ``table``
+    as ``rope_table`` makes it.  Outputs are allocated unless given (in place: pass q and k).
+    Returns (q_out, k_out).  Raises DsaError on a host-side error.
+    """
+    import torch
+    T, Hq, D = q.shape
+    dtype = _dtype(q)
+    _need(q.stride(2) == 1 or D == 1, "q: the last dimension must be contiguous")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.stride(2) == 1,
+          "q_out: like q")
+    Hk, ks, kos = 0, (0, 0), (0, 0)
+    if k is not None:
+        _need(k.dim() == 3 and k.shape[0] == T and k.shape[2] == D and k.dtype == q.dtype
+              and k.stride(2) == 1, "k: [T, Hk, D] of q's type")
+        Hk = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=k.dtype, device=k.device)
+        _need(k_out.shape == k.shape and k_out.dtype == k.dtype and k_out.stride(2) == 1,
+              "k_out: like k")
+        ks, kos = k.stride(), k_out.stride()
+    max_pos = rot = 0
+    if positions is not None:
+        _ints(positions, "positions", (T,))
+        _need(table is not None, "positions need a table")
+        max_pos, rot = table.shape
+        _need(rot_dims is None or rot_dims == rot, "rot_dims: the table's width")
+        _floats(table, "table", (max_pos, rot))
+    for name, x in (("q_weight", q_weight), ("k_weight", k_weight), ("q_bias", q_bias),
+                    ("k_bias", k_bias)):
+        _floats(x, name, (D,))
+    qs, qos = q.stride(), q_out.stride()
+    _check(dsa_qk_norm_rope(q, qs[0], qs[1], Hq, k, ks[0], ks[1], Hk, T, D, dtype, norm, q_weight,
+                            k_weight, q_bias, k_bias, eps, positions, table, max_pos, rot,
+                            rot_offset, interleaved, q_out, qos[0], qos[1], k_out, kos[0], kos[1],
+                            dev_status, stream))
+    return q_out, k_out
+
+
+def latent_store(latent, rope, slot_mapping, cache, kv_dtype, *, norm_weight=None, eps=1e-6,
+                 positions=None, rope_table=None, interleaved=False, dev_status=None, stream=None):
+    """Write n tokens (latent [n, 512], rope [n, 64], bf16) into their slots of ``cache``.
+
+    Optionally normalises the latent and rotates the other part on the way.  ``cache``: uint8
+    [pages, LATENT_PAGE_BYTES[kv_dtype]].  Raises DsaError on a host-side error.
+    """
+    import torch
+    n = latent.shape[0]
+    _need(latent.dtype is torch.bfloat16 and tuple(latent.shape) == (n, LATENT)
+          and latent.stride(1) == 1, "latent: bfloat16 [n, 512], rows contiguous")
+    _need(rope.dtype is torch.bfloat16 and tuple(rope.shape) == (n, ROPE) and rope.stride(1) == 1,
+          "rope: bfloat16 [n, 64], rows contiguous")
+    _ints(slot_mapping, "slot_mapping", (n,))
+    _floats(norm_weight, "norm_weight", (LATENT,))
+    max_pos = 0
+    if positions is not None:
+        _ints(positions, "positions", (n,))
+        _need(rope_table is not None, "positions need a rope_table")
+        max_pos = rope_table.shape[0]
+        _floats(rope_table, "rope_table", (max_pos, ROPE))
+    stride, pages = _pool(cache, kv_dtype)
+    _check(dsa_latent_store(latent, latent.stride(0), rope, rope.stride(0), n, LATENT, ROPE,
+                            norm_weight, eps, positions, rope_table, max_pos, interleaved,
+                            slot_mapping, cache, stride, pages, kv_dtype, PAGE, dev_status, stream))
+    return cache
+
+
+def latent_load(cache, kv_dtype, block_table, cu_rows, n, *, starts=None, out=None,
+                dev_status=None, stream=None):
+    """Read ranges of cached tokens back as bf16 [n, 576] (latent, then rotated part).
+
+    ``cu_rows`` int32 [requests + 1] on the device: request r's rows of the output.  Raises
+    DsaError on a host-side error.
+    """
+    import torch
+    n_req = cu_rows.shape[0] - 1
+    _ints(cu_rows, "cu_rows")
+    if starts is not None:
+        _ints(starts, "starts", (n_req,))
+    if out is None:
+        out = torch.empty((n, LATENT + ROPE), dtype=torch.bfloat16, device=cache.device)
+    _need(out.dtype is torch.bfloat16 and tuple(out.shape) == (n, LATENT + ROPE)
+          and out.stride(1) == 1, "out: bfloat16 [n, 576], rows contiguous")
+    stride, pages = _pool(cache, kv_dtype)
+    bt_stride, W = _table_rows(block_table, n_req)
+    _check(dsa_latent_load(cache, stride, pages, kv_dtype, PAGE, block_table, bt_stride, W, starts,
+                           cu_rows, n_req, n, LATENT, ROPE, out, out.stride(0), dev_status, stream))
+    return out
+
+
+def latent_attention(q_latent, q_rope, cache, kv_dtype, block_table, seqlens, scale, *, idx=None,
+                     out=None, lse=None, workspace=None, dev_status=None, stream=None):
+    """Attention of [rows, H] query heads over the latent cache, in the absorbed form.
+
+    Over every position below ``seqlens``, or over the selection lists ``idx`` (int32 [rows, k],
+    as the top-k calls write them).  Returns out, bf16 [rows, H, 512]; ``lse`` (fp32 [rows, H])
+    is written when given.  Raises DsaError on a host-side error.
+    """
+    import torch
+    rows, H, _ = q_latent.shape
+    _need(q_latent.dtype is torch.bfloat16 and q_latent.shape[2] == LATENT
+          and q_latent.stride(2) == 1, "q_latent: bfloat16 [rows, H, 512]")
+    _need(q_rope.dtype is torch.bfloat16 and tuple(q_rope.shape) == (rows, H, ROPE)
+          and q_rope.stride(2) == 1, "q_rope: bfloat16 [rows, H, 64]")
+    _ints(seqlens, "seqlens", (rows,))
+    idx_stride = k = 0
+    if idx is not None:
+        _need(idx.dtype is torch.int32 and idx.dim() == 2 and idx.shape[0] == rows
+              and idx.stride(1) == 1, "idx: int32 [rows, k]")
+        k = idx.shape[1]
+        idx_stride = idx.stride(0) if rows > 1 else k
+    if out is None:
+        out = torch.empty((rows, H, LATENT), dtype=torch.bfloat16, device=q_latent.device)
+    _need(out.dtype is torch.bfloat16 and tuple(out.shape) == (rows, H, LATENT)
+          and out.stride(2) == 1, "out: bfloat16 [rows, H, 512]")
+    _floats(lse, "lse", (rows, H))
+    if workspace is None:
+        workspace = torch.empty(dsa_latent_attention_workspace(), dtype=torch.float32,
+                                device=q_latent.device)
+    _need(workspace.dtype is torch.float32 and workspace.is_contiguous(),
+          "workspace: contiguous float32")
+    stride, pages = _pool(cache, kv_dtype)
+    bt_stride, W = _table_rows(block_table, rows)
+    _check(dsa_latent_attention(q_latent, q_latent.stride(0), q_latent.stride(1), q_rope,
+                                q_rope.stride(0), q_rope.stride(1), rows, H, LATENT, ROPE, scale,
+                                cache, stride, pages, kv_dtype, PAGE, block_table, bt_stride, W,
+                                seqlens, idx, idx_stride, k, out, out.stride(0), out.stride(1),
+                                lse, workspace, workspace.numel(), dev_status, stream))
     return out

@@ -29,6 +29,8 @@ EXPORTS = ("dsa_indexer_logits_decode", "dsa_indexer_logits_prefill",
            "dsa_indexer_logits_prefill_varlen", "dsa_indexer_topk_decode",
            "dsa_indexer_topk_decode_form",
            "dsa_indexer_topk_decode_static", "dsa_kcache_store",
+           "dsa_qk_norm_rope", "dsa_latent_store", "dsa_latent_load",
+           "dsa_latent_attention", "dsa_latent_attention_workspace",
            "dsa_status_string", "dsa_indexer_abi_version")
 
 _lib = None
@@ -116,6 +118,23 @@ def load() -> ctypes.CDLL:
                                                        ci, ci, ci, ci, ci, vp, vp, ll, vp, vp]
         lib.dsa_kcache_store.restype = ci
         lib.dsa_kcache_store.argtypes = [vp, vp, ci, vp, ll, ci, ci, ci, ci, vp, vp]
+        cf = ctypes.c_float
+        lib.dsa_qk_norm_rope.restype = ci
+        lib.dsa_qk_norm_rope.argtypes = [vp, ll, ll, ci, vp, ll, ll, ci, ci, ci, ci, ci, vp, vp, vp,
+                                         vp, cf, vp, vp, ci, ci, ci, ci, vp, ll, ll, vp, ll, ll, vp,
+                                         vp]
+        lib.dsa_latent_store.restype = ci
+        lib.dsa_latent_store.argtypes = [vp, ll, vp, ll, ci, ci, ci, vp, cf, vp, vp, ci, ci, vp, vp,
+                                         ll, ci, ci, ci, vp, vp]
+        lib.dsa_latent_load.restype = ci
+        lib.dsa_latent_load.argtypes = [vp, ll, ci, ci, ci, vp, ll, ci, vp, vp, ci, ci, ci, ci, vp,
+                                        ll, vp, vp]
+        lib.dsa_latent_attention.restype = ci
+        lib.dsa_latent_attention.argtypes = [vp, ll, ll, vp, ll, ll, ci, ci, ci, ci, cf, vp, ll, ci,
+                                             ci, ci, vp, ll, ci, vp, vp, ll, ci, vp, ll, ll, vp, vp,
+                                             ll, vp, vp]
+        lib.dsa_latent_attention_workspace.restype = ll
+        lib.dsa_latent_attention_workspace.argtypes = []
         lib.dsa_status_string.restype = ctypes.c_char_p
         lib.dsa_status_string.argtypes = [ci]
         lib.dsa_indexer_abi_version.restype = ci

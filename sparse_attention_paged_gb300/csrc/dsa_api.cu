@@ -301,6 +301,7 @@ const char* dsa_status_string(int status) {
     case DSA_ERR_TIMEOUT: return "DSA_ERR_TIMEOUT: a device wait exceeded its bound";
     case DSA_ERR_BAD_PAGE: return "DSA_ERR_BAD_PAGE: block-table entry outside the pool";
     case DSA_ERR_BAD_SEQLEN: return "DSA_ERR_BAD_SEQLEN: length exceeds the block table";
+    case DSA_ERR_BAD_POSITION: return "DSA_ERR_BAD_POSITION: position outside the rotation table";
     default: return "unknown dsa status";
   }
 }
