@@ -413,7 +413,8 @@ int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_page
  * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
  * visible position without a page in the pool a NaN row and
  * DSA_ERR_BAD_PAGE; a wait that runs out DSA_ERR_TIMEOUT and NaN rows.
- * rows * max(W, ceil(k / 64)) must be below 2^31 (DSA_ERR_UNSUPPORTED).
+ * rows * (idx ? ceil(k / 64) : W), W * 64 and num_pages * 64 must be below
+ * 2^31 (DSA_ERR_UNSUPPORTED).
  */
 int dsa_latent_attention(const void* q_latent, long long ql_row_stride, long long ql_head_stride,
                          const void* q_rope, long long qr_row_stride, long long qr_head_stride,

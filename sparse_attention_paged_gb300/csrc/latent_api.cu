@@ -176,7 +176,8 @@ int dsa_latent_attention(const void* q_latent, long long ql_row_stride, long lon
   if (rows > 0 && (!q_latent || !q_rope || !block_table || !seqlens || !out || !workspace))
     return DSA_ERR_INVALID_ARG;
   const long long tiles = idx ? (k + 63LL) / 64 : W;
-  if ((long long)rows * tiles >= (1LL << 31) || (long long)W * dsa::kPage >= (1LL << 31))
+  if ((long long)rows * tiles >= (1LL << 31) || (long long)W * dsa::kPage >= (1LL << 31) ||
+      (long long)num_pages * dsa::kPage >= (1LL << 31))
     return DSA_ERR_UNSUPPORTED;
   if (!aligned(q_latent, 16) || !aligned(q_rope, 16) || ql_row_stride % 8 || ql_head_stride % 8 ||
       qr_row_stride % 8 || qr_head_stride % 8 || !aligned(out, 16) || out_row_stride % 8 ||

@@ -5,36 +5,58 @@
 //   p[h, :] = softmax(s[h, :]) over the row's visible tokens
 //   out[h]  = sum_t p[h, t] c[t],   lse[h] = log sum_t exp(s[h, t])
 //
-// One token serves as key and value of every head, so a tile of 64 tokens is
-// brought into shared memory once (bf16, nine blocks of 64 values, 128-byte
+// One token serves as key and value of every head, so a tile of 128 tokens is
+// brought into shared memory once (16-bit, nine blocks of 64 values, 128-byte
 // swizzle) and feeds both products as it lies there:
 //
-//   S^T [64 tokens x 64 heads]  = tile [64 x 576] (A, K-major) * Q^T (B, K-major)
+//   S^T [128 tokens x 64 heads] = tile [128 x 576] (A, K-major) * Q^T (B, K-major)
 //   O^T [512 values x 64 heads] += tile^T (A, MN-major) * P^T (B, MN-major)
 //
-// Keeping the heads on the N side leaves O^T at 4 x 64 TMEM columns, beside
-// two S^T buffers, and a token's mask is a whole row of S^T.  The softmax
-// warps read S^T, keep a maximum per head that is raised only when a score
-// passes it by 2^8 (then O^T is rescaled in TMEM; the sums are fp32, so the
-// reference point does not change their relative precision), and write P as
-// bf16, rounded to nearest: its rounding is independent from token to token
-// and below that of the bf16 result.
+// Keeping the heads on the N side leaves O^T at 4 x 64 TMEM columns, gives
+// every softmax thread one token, and makes a token's mask a whole row.  The
+// softmax warps keep a reference per head that is raised only when a weight
+// passes it by 2^8 (fp8: 2^9), and then O^T is rescaled in TMEM; the sums are
+// fp32, so the reference does not change their relative precision.
 //
-// Persistent: the call's tiles (per head group of 64) are cut into equal
-// slices, one per CTA, rows in order.  A row that a slice cuts leaves
+// bf16 cache: tile, queries and weights are bf16.  The weights' rounding
+// (nearest, 2^-8) is independent from token to token and below that of the
+// bf16 result.
+//
+// fp8 cache: tile, latent queries and weights are fp16, which holds e4m3
+// exactly and takes one conversion where bf16 takes four instructions.  With
+// s(t) the largest of token t's four scales, the tile holds code * s_g / s(t)
+// (exact for scales that are powers of two and lie within 2^15; what is
+// rounded below is under 2^-25 of s(t)), the scores are multiplied by s(t) and
+// the weights written as w * s(t).  A head's queries are scaled by a power of
+// two to bring their largest below 2^15, so that any bf16 range fits; the
+// rotated part stays bf16 in an accumulator of its own.  The reference is
+// kept on w * s(t): the largest lie between 2^6 and 2^15, and what is 2^-20 of
+// them is still a normal number.
+//
+// Shared memory holds one tile (144 KB) and the row's queries (72 KB); the
+// tile is refilled part by part: the value product takes the latent parts of
+// 128 values in order and gives each back as soon as it is used, the score
+// product of the next tile takes them in the same order as they arrive.  P
+// lies where the rotated part was, which only the score product reads.
+//
+// Persistent: the call's 64-token units (per head group of 64) are cut into
+// equal slices, one per CTA, rows in order.  A row that a slice cuts leaves
 // unnormalised partial sums in the workspace, and a second kernel joins
 // them, so one long row or a few short ones spread over every SM, and a
 // batch of any lengths is balanced.
 //
-// Warps: 0-3 softmax and output, 4 MMA issue, 5-12 loaders in two groups of
-// four, one per tile buffer.  A selected token is 1,152 contiguous bytes (fp8:
-// 512 + 128 + 16), gathered with 16-byte loads per token through the block
-// table; masked tokens are not read, their rows are zeros.
+// Warps: 0-7 softmax and output, 8 MMA issue, 9-11 token lookup, 12-19
+// loaders.  The lookup warps go through selection list and block table up to
+// three tiles ahead and ask L2 for the tokens' bytes, which keeps HBM busy
+// whatever the tile buffer does.  The loaders copy (bf16) or convert (fp8) 16
+// bytes at a time; masked tokens are not read, their rows are zeros.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "latent_common.cuh"
@@ -50,40 +72,70 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = 64;                       // tokens per tile
-constexpr int kBlocks = (kLatent + kRope) / 64; // 64-value blocks of a token
-constexpr int kBlockBytes = kTile * 128;        // one block of a tile (or of Q)
-constexpr int kTileBytes = kBlocks * kBlockBytes;
-constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp0 = 5, kLoadWarps = 8;
+constexpr int kUnit = 64;                       // tokens per unit of the split
+constexpr int kTile = 128;                      // tokens per tile
+constexpr int kParts = 4;                       // latent parts of 128 values; the rotated part follows
+constexpr int kBlockBytes = kTile * 128;        // 64 values of a tile's tokens
+constexpr int kPartBytes = 2 * kBlockBytes;
+constexpr int kRopeBlock = 8;                   // index of the rotated part's block
+constexpr int kQBlockBytes = kAttnHeads * 128;  // 64 values of the queries
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLookWarp0 = 9, kLookWarps = 3, kLoadWarp0 = 12, kLoadWarps = 8;
 constexpr int kAttnThreads = (kLoadWarp0 + kLoadWarps) * 32;
-constexpr int kGroupThreads = kLoadWarps / 2 * 32;
-constexpr int kKeysPerWarp = kTile / (kLoadWarps / 2);  // 16
-constexpr float kSlack = 8.f;                   // log2 of how far a score may pass the kept maximum
+// Tiles of looked-up tokens: one slot per lookup warp, so that no warp can be
+// two phases of a slot's barrier ahead of another.
+constexpr int kRing = kLookWarps;
+constexpr int kKeysPerWarp = kTile / kLoadWarps;  // 16
+// Registers per thread: at launch (65,536 / 640 in steps of 8), then per role.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsMisc = 64, kRegsLoad = 104;
+static_assert(kSoftmaxWarps * kRegsSoftmax + 4 * kRegsMisc + kLoadWarps * kRegsLoad <=
+                  kAttnThreads / 32 * kRegsLaunch,
+              "the roles' registers are those of the launch");
+// The reference (log2 units): a new one is set ref_below under the largest
+// weight, and holds until a weight is ref_limit above it.
+constexpr float ref_below(int kv) { return kv == DSA_KV_BF16 ? 0.f : 6.f; }
+constexpr float ref_limit(int kv) { return kv == DSA_KV_BF16 ? 8.f : 15.f; }
+constexpr uint32_t kUnset = 0x80000000u;        // bits of -reference (-0) before the first visible token
+constexpr float kSmallestScale = 7.8886090522101181e-31f;  // 2^-100: keeps 1 / s and the sums in range
 
 // Shared memory, from a 1,024-byte boundary.
-constexpr int kOffQ = 2 * kTileBytes;
-constexpr int kOffP = kOffQ + kTileBytes;
-constexpr int kOffMisc = kOffP + kBlockBytes;
+constexpr int kOffQ = 9 * kBlockBytes;
+constexpr int kOffMisc = kOffQ + 9 * kQBlockBytes;
+constexpr int kOffP = kRopeBlock * kBlockBytes;
 struct Misc {
-  uint64_t full[2], empty[2], sfull[2], pfull, qfree, ofull, ofree, done;
+  uint64_t full[kParts + 1];   // a part of the tile is in place (rotated part last; part 0: the queries too)
+  uint64_t empty[kParts];      // the value product is done with the part; the last: with the tile
+  uint64_t sfull;              // S^T is there
+  uint64_t pfull;              // P is there
+  uint64_t ofree;              // O^T has been read
+  uint64_t look_full[kRing], look_empty[kRing], scale_full[kRing];
+  uint64_t done;
   uint32_t tmem;
-  int abort;
-  int start_row, start_tile, total;
-  int nzero;
-  uint32_t keymask[2][4];   // per tile buffer and loader warp: 16 valid bits, bad data in bit 16
-  int scan[16];
-  float red[4][kAttnHeads]; // per softmax warp and head
-  float fac[kAttnHeads];
-  int zero[64];
+  int start_row, start_unit, nzero;
+  int begin, total, ctas;      // the slice's first unit, the call's units, the CTAs that have one
+  int scan[kAttnThreads / 32];
+  alignas(16) uint2 ratio[kRing][kTile];  // fp8: each part's scale over s(t), fp16
+  int token[kRing][kTile];     // page * 64 + slot, -1 when masked
+  float key_scale[kRing][kTile];  // fp8: s(t)
+  uint32_t mask[kRing][4];     // valid tokens
+  uint32_t bad[kRing];         // a visible token has no page
+  alignas(16) float red[4][kAttnHeads];  // per quarter of the tokens and head
+  float nref[kAttnHeads];      // -reference, in log2 units; nref, mul, fac are read as float4
+  float mul[2][kAttnHeads];    // fp8: from a head's score sums to log2 units, this row's and the next one's
+  float fac[kAttnHeads], keep[kAttnHeads];
 };
-constexpr int kSmemBytes = kOffMisc + 2048 + 1024;
-static_assert(sizeof(Misc) <= 2048, "misc");
+constexpr int kMiscBytes = 9 * 1024;
+constexpr int kSmemBytes = kOffMisc + kMiscBytes + 1024;
+static_assert(sizeof(Misc) <= kMiscBytes, "misc");
 static_assert(kSmemBytes <= 232448, "227 KB");
+static_assert(offsetof(Misc, nref) % 16 == 0 && offsetof(Misc, mul) % 16 == 0 && offsetof(Misc, fac) % 16 == 0 &&
+                  offsetof(Misc, ratio) % 8 == 0 && kOffMisc % 16 == 0,
+              "vector reads");
 
-// TMEM columns: O^T 4 x 64, S^T 2 x 64.
-constexpr uint32_t kTmemS = 256, kTmemCols = 512;
+// TMEM columns: O^T 4 x 64, S^T 64, the rotated part's S^T (fp8) 64.
+constexpr uint32_t kTmemS = 256, kTmemR = 320, kTmemCols = 512;
 
-constexpr long long kWaitLimit = DSA_WAIT_LIMIT_CYCLES;
+// at most about a second: the clock's low 32 bits are compared
+constexpr uint32_t kWaitLimit = DSA_WAIT_LIMIT_CYCLES < 2000000000ll ? DSA_WAIT_LIMIT_CYCLES : 2000000000ll;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -95,7 +147,35 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but the last N groups of this thread.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Every copy of this thread, committed to a group or not.
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// 16 bytes that are read once: not kept in L1
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Ask L2 for a line / for `bytes` (a multiple of 16, 16-byte aligned).  The
+// bulk form takes a page at a time; per token it would hold up its queue.
+__device__ __forceinline__ void l2_prefetch(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
+__device__ __forceinline__ void l2_prefetch_bulk(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -114,41 +194,60 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
   return r != 0;
 }
 
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 32 lanes x 8 columns of TMEM, and the waits for them
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&a)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// tcgen05.wait::ld tied to a 32-register destination
-__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&a)[32]) {
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
-        "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]),
-        "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]),
-        "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]),
-        "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
-      :
-      : "memory");
-}
 
 // Descriptor of an MN-major operand in the 128-byte swizzle: 64 M/N values of
 // one K index are a 128-byte row, eight K rows an atom; `k_bytes` from one
@@ -160,8 +259,13 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
   return d;
 }
 
-constexpr uint32_t kIdescS = instr_desc(1, 1, kTile, kAttnHeads);
-constexpr uint32_t kIdescO = instr_desc(1, 1, 128, kAttnHeads) | (1u << 15) | (1u << 16);  // A, B MN-major
+// Instruction descriptors: formats 0 = fp16, 1 = bf16; O^T with A and B MN-major.
+constexpr uint32_t format(int kv) { return kv == DSA_KV_BF16 ? 1u : 0u; }
+constexpr uint32_t idesc_s(int kv) { return instr_desc(format(kv), format(kv), kTile, kAttnHeads); }
+constexpr uint32_t idesc_o(int kv) {
+  return instr_desc(format(kv), format(kv), 128, kAttnHeads) | (1u << 15) | (1u << 16);
+}
+constexpr uint32_t kIdescRope = instr_desc(1, 1, kTile, kAttnHeads);
 
 // A row's visible entries: its length, or the part of its selection list that
 // is read.  A length past the block table is an error: no entries.
@@ -172,124 +276,143 @@ __device__ __forceinline__ int row_entries(const LatentAttnParams& p, int row, i
   return p.idx ? min(L, p.k) : L;
 }
 
-// Walks the tiles of a CTA's slice, row by row; rows without tiles are passed.
+__device__ __forceinline__ int row_units(const LatentAttnParams& p, int row) {
+  int len;
+  return (row_entries(p, row, &len) + kUnit - 1) / kUnit;
+}
+
+// Walks the tiles of a CTA's slice, row by row; rows without units are passed.
+// A tile is up to two units of one row.
 struct TileWalk {
-  int row, t, n, len, left, piece;
+  int row, u, n, len, left, piece;
   bool first;
-  __device__ __forceinline__ int tiles() const { return (n + kTile - 1) / kTile; }
-  __device__ __forceinline__ bool last() const { return left == 1 || t + 1 == tiles(); }
-  __device__ __forceinline__ void start(const LatentAttnParams& p, int row0, int tile0, int count) {
-    row = row0, t = tile0, left = count, piece = 0, first = true, n = 0, len = 0;
+  __device__ __forceinline__ int units() const { return (n + kUnit - 1) / kUnit; }
+  __device__ __forceinline__ int count() const { return min(2, min(left, units() - u)); }
+  __device__ __forceinline__ int tokens() const { return min(n - u * kUnit, count() * kUnit); }
+  __device__ __forceinline__ bool last() const { return left == count() || u + count() == units(); }
+  __device__ __forceinline__ void start(const LatentAttnParams& p, int row0, int unit0, int units) {
+    row = row0, u = unit0, left = units, piece = 0, first = true, n = 0, len = 0;
     if (left > 0) n = row_entries(p, row, &len);
   }
   __device__ __forceinline__ void step(const LatentAttnParams& p) {
-    if (--left <= 0) return;
-    if (++t < tiles()) {
-      first = false;
-      return;
-    }
+    const int c = count();
+    left -= c;
+    if (left <= 0) return;
+    u += c;
+    first = false;
+    if (u < units()) return;
     do {
       n = row_entries(p, ++row, &len);
     } while (n == 0 && row + 1 < p.rows);
-    t = 0, first = true, ++piece;
+    u = 0, first = true, ++piece;
   }
 };
 
+// Waits, by a whole warp together (every lane gets the same answer) or by one
+// lane.  After one that ran out the rest return at once.  Short, because it is
+// inlined everywhere: the loops of five roles share the instruction caches.
+template <bool WARP>
 struct Waiter {
-  Misc* m;
   int* status;
   bool ok;
-  // Wait for phase `parity` of `bar`; after a wait that ran out (here or in
-  // another warp) every wait returns at once.
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
     if (!ok) return false;
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t i = 1;; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if ((i & 15u) == 0) {
-        if (*reinterpret_cast<volatile int*>(&m->abort)) break;
-        if (clock64() - t0 > kWaitLimit) {
-          *reinterpret_cast<volatile int*>(&m->abort) = 1;
-          raise_status(status, DSA_ERR_TIMEOUT);
-          break;
-        }
-      }
-    }
-    ok = false;
+    const uint32_t t0 = (uint32_t)clock();
+#pragma unroll 1
+    do {
+      const bool r = mbar_try_wait(bar, parity);
+      if (WARP ? __all_sync(0xffffffffu, r) : r) return true;
+      const bool late = (uint32_t)clock() - t0 > kWaitLimit;
+      ok = WARP ? !__any_sync(0xffffffffu, late) : !late;
+    } while (ok);
+    raise_status(status, DSA_ERR_TIMEOUT);
     return false;
   }
 };
 
-// The byte offset in the cache of entry j of a tile's row, -1 when it is
-// masked; *bad when a valid entry has no page.
-__device__ __forceinline__ long long token_offset(const LatentAttnParams& p, const TileWalk& w, int j,
-                                                  int kv_token_bytes, bool* bad, int* slot) {
-  *bad = false;
-  *slot = 0;
-  if (j >= w.n) return -1;
-  int pos = j;
-  if (p.idx) {
-    pos = __ldg(p.idx + w.row * p.idx_stride + j);
-    if (pos < 0 || pos >= w.len) return -1;
-  }
-  const int page = __ldg(p.block_table + w.row * p.bt_stride + pos / kPage);
-  if (page < 0 || page >= p.num_pages) {
-    *bad = true;
-    return -1;
-  }
-  *slot = pos % kPage;
-  return (long long)page * p.page_stride + (long long)(pos % kPage) * kv_token_bytes;
+// Every lane's writes to shared memory, made visible to the MMA, before one
+// lane arrives for the warp.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
-// Bytes `chunk` (16 bytes each, 8 per block) of row r of a tile in the swizzled layout.
-__device__ __forceinline__ uint32_t swz(int r, int chunk) {
-  return (uint32_t)((chunk >> 3) * kBlockBytes + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
+// Eight e4m3 codes times `f` (a factor twice, fp16), 16 bytes of fp16.
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, uint32_t f) {
+  const uint32_t u[2] = {lo, hi};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&r), *reinterpret_cast<const __half2*>(&f));
+    o[j] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 16 e4m3 codes times their scale as bf16, 32 bytes.
-__device__ __forceinline__ void dequant16(const uint4& c, float s, uint4& a, uint4& b) {
-  const uint32_t u[4] = {c.x, c.y, c.z, c.w};
-  uint32_t o[8];
+// Eight bf16 values (16 bytes) as floats.
+__device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8]) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+// The largest value of a warp's lanes; NaN does not count.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Sums 32 values per lane over the warp's lanes: lane l gets sum l.
+__device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[j] >> (16 * h)), __NV_E4M3);
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-      const __nv_bfloat162 r = __floats2bfloat162_rn(v.x * s, v.y * s);
-      o[2 * j + h] = *reinterpret_cast<const uint32_t*>(&r);
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const bool up = lane & o;
+      const float give = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
-  a = make_uint4(o[0], o[1], o[2], o[3]);
-  b = make_uint4(o[4], o[5], o[6], o[7]);
+  return v[0];
 }
+
+// What a masked token's codes are read from.
+__device__ const uint4 g_zeros[kLatent / 16] = {};
 
 template <int KV>
 __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const LatentAttnParams p) {
+  constexpr bool kFp8 = KV != DSA_KV_BF16;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // an offset, not a rounded address: the compiler keeps seeing shared memory
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc* m = reinterpret_cast<Misc*>(smem + kOffMisc);
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int cta = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
   const int head0 = grp * kAttnHeads, heads = min(kAttnHeads, p.H - head0);
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&m->full[i], kGroupThreads);
-      mbar_init(&m->empty[i], 1);
-      mbar_init(&m->sfull[i], 1);
+    for (int i = 0; i <= kParts; ++i) mbar_init(&m->full[i], kLoadWarps);
+    for (int i = 0; i < kParts; ++i) mbar_init(&m->empty[i], 1);
+    mbar_init(&m->sfull, 1);
+    mbar_init(&m->pfull, kSoftmaxWarps);
+    mbar_init(&m->ofree, kSoftmaxWarps);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&m->look_full[i], 1);
+      mbar_init(&m->scale_full[i], 1);
+      mbar_init(&m->look_empty[i], kLoadWarps + kSoftmaxWarps);
     }
-    mbar_init(&m->pfull, kSoftmaxWarps * 32);
-    mbar_init(&m->qfree, 1);
-    mbar_init(&m->ofull, 1);
-    mbar_init(&m->ofree, kSoftmaxWarps * 32);
     mbar_init(&m->done, 1);
     fence_barrier_init();
-    m->abort = 0;
-    m->start_row = m->start_tile = m->total = 0;
-    m->nzero = 0;
+    m->start_row = m->start_unit = m->nzero = 0;
   }
+  if (tid < kAttnHeads) m->nref[tid] = __uint_as_float(kUnset);
   if (warp == kMmaWarp) {
     tmem_alloc(&m->tmem, kTmemCols);
     tmem_relinquish();
@@ -298,232 +421,439 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
   griddep_launch_dependents();
 
   // ---- the slice -----------------------------------------------------------
-  // thread i owns a run of rows; an exclusive scan of the runs' tile counts
+  // thread i owns a run of rows; an exclusive scan of the runs' unit counts
   // finds the row in which this CTA's slice begins
-  const int per = (p.rows + kAttnThreads - 1) / kAttnThreads;
-  const int r0 = min(p.rows, tid * per), r1 = min(p.rows, r0 + per);
-  int mine = 0, len;
-  for (int r = r0; r < r1; ++r) mine += (row_entries(p, r, &len) + kTile - 1) / kTile;
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) m->scan[warp] = incl;
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = m->tmem;
-  int base = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kAttnThreads / 32; ++w) {
-    if (w < warp) base += m->scan[w];
-    total += m->scan[w];
-  }
-  const int ctas = min(p.ctas, total);            // every slice has a tile
-  int begin = 0, end = 0;
-  if (cta < ctas) {
-    begin = (int)((long long)cta * total / ctas);
-    end = (int)((long long)(cta + 1) * total / ctas);
-  }
+  TileWalk walk;
   {
+    const int per = (p.rows + kAttnThreads - 1) / kAttnThreads;
+    const int r0 = min(p.rows, tid * per), r1 = min(p.rows, r0 + per);
+    int mine = 0;
+    bool zero = false;
+    for (int r = r0; r < r1; ++r) {
+      const int t = row_units(p, r);
+      mine += t;
+      zero |= t == 0 && r % p.ctas == cta;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) m->scan[warp] = incl;
+    const bool zeros = __syncthreads_or(zero);
+    int base = 0, total = 0;
+#pragma unroll 4
+    for (int w = 0; w < kAttnThreads / 32; ++w) {
+      const int v = m->scan[w];
+      if (w < warp) base += v;
+      total += v;
+    }
+    const int ctas = min(p.ctas, total);            // every slice has a unit
+    int begin = 0, end = 0;
+    if (cta < ctas) {
+      if (total < (1 << 22)) {                      // p.ctas < 512
+        begin = (int)((unsigned)(cta * total) / (unsigned)ctas);
+        end = (int)((unsigned)((cta + 1) * total) / (unsigned)ctas);
+      } else {
+        begin = (int)((long long)cta * total / ctas);
+        end = (int)((long long)(cta + 1) * total / ctas);
+      }
+    }
     int at = base + incl - mine;
     if (end > begin && at <= begin && begin < at + mine) {
       int r = r0;
       for (;; ++r) {
-        const int t = (row_entries(p, r, &len) + kTile - 1) / kTile;
+        const int t = row_units(p, r);
         if (begin < at + t) break;
         at += t;
       }
       m->start_row = r;
-      m->start_tile = begin - at;
+      m->start_unit = begin - at;
     }
-  }
-  // rows without a visible token: zeros (a length past the table: NaN)
-  for (long long r = cta; r - cta < p.rows; r += (long long)p.ctas * 64) {
+    if (tid == 0) m->begin = begin, m->total = total, m->ctas = ctas;
     __syncthreads();
-    if (tid == 0) m->nzero = 0;
-    __syncthreads();
-    if (tid < 64) {
-      const long long row = r + (long long)tid * p.ctas;
-      if (row < p.rows && row_entries(p, (int)row, &len) == 0) m->zero[atomicAdd(&m->nzero, 1)] = (int)row;
-    }
-    __syncthreads();
-    for (int i = 0; i < m->nzero; ++i) {
-      const int row = m->zero[i];
-      const bool bad = __ldg(p.seqlens + row) > 0 && (p.idx == nullptr || p.k > 0);
-      if (bad && tid == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
-      const uint32_t v = bad ? 0x7fff7fffu : 0u;
-      for (int j = tid; j < heads * (kLatent / 8); j += kAttnThreads) {
-        const int h = head0 + j / (kLatent / 8);
-        *reinterpret_cast<uint4*>(p.out + row * p.out_row + h * p.out_head + (j % (kLatent / 8)) * 8) =
-            make_uint4(v, v, v, v);
+    if (zeros) {
+      // rows without a visible token: zeros (a length past the table: NaN); the
+      // list lies where the tile will
+      int* list = reinterpret_cast<int*>(smem);
+      for (int i = 0; i < per; ++i) {
+        if (r0 + i < r1 && (r0 + i) % p.ctas == cta && row_units(p, r0 + i) == 0)
+          list[atomicAdd(&m->nzero, 1)] = r0 + i;
+        __syncthreads();
+        const int n = m->nzero;
+        __syncthreads();
+        if (tid == 0) m->nzero = 0;
+        for (int z = 0; z < n; ++z) {
+          const int row = list[z];
+          const bool bad = __ldg(p.seqlens + row) > 0;
+          if (bad && tid == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
+          const uint32_t v = bad ? 0x7fff7fffu : 0u;
+          for (int j = tid; j < heads * (kLatent / 8); j += kAttnThreads) {
+            const int h = head0 + j / (kLatent / 8);
+            *reinterpret_cast<uint4*>(p.out + row * p.out_row + h * p.out_head + (j % (kLatent / 8)) * 8) =
+                make_uint4(v, v, v, v);
+          }
+          if (p.lse && tid < heads)
+            p.lse[(long long)row * p.H + head0 + tid] = bad ? CUDART_NAN_F : -CUDART_INF_F;
+        }
+        __syncthreads();
       }
-      if (p.lse && tid < heads) p.lse[(long long)row * p.H + head0 + tid] = bad ? CUDART_NAN_F : -CUDART_INF_F;
     }
+    walk.start(p, m->start_row, m->start_unit, end - begin);
   }
-  __syncthreads();
-
-  TileWalk walk;
-  walk.start(p, m->start_row, m->start_tile, end - begin);
-  Waiter wait{m, p.status, true};
+  tc_fence_after();
+  const uint32_t tmem = m->tmem;
+  Waiter<true> wait{p.status, true};
 
   if (warp >= kLoadWarp0) {
     // ---- loaders -------------------------------------------------------------
-    const int g = (warp - kLoadWarp0) / 4, w = (warp - kLoadWarp0) % 4;
-    const uint32_t tile = sbase + g * kTileBytes;
-    const int token_bytes = KV == DSA_KV_BF16 ? kTokenBytesBf16 : kLatent;
-    if (g == 1) walk.step(p);
-    for (int it = g; walk.left > 0; it += 2) {
-      bool bad;
-      int slot;
-      const long long off =
-          token_offset(p, walk, walk.t * kTile + w * kKeysPerWarp + (lane & 15), token_bytes, &bad, &slot);
-      const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
-      const uint32_t badmask = __ballot_sync(0xffffffffu, bad);
-      if (KV == DSA_KV_BF16) {
-        if (it >= 2) wait(&m->empty[g], ((it >> 1) - 1) & 1);
-        if (wait.ok) {
+    more_registers<kRegsLoad>();
+    // warp w brings tokens 16w .. 16w+15 of every tile
+    const int w = warp - kLoadWarp0;
+    const int sub = lane >> 3, col = lane & 7;     // rotated part and fp8: 4 tokens x 8 lanes
+    auto token_at = [&](int slot, int j) { return m->token[slot][w * kKeysPerWarp + j]; };
+    auto page_of = [&](int t) { return p.cache + (long long)(t >> 6) * p.page_stride; };
+
+    // fp8: tokens 4i + sub of the tile, and the codes of its first three parts,
+    // already in registers when the buffer falls free (the fourth part's
+    // follow into the first one's place)
+    uint4 codes[kParts - 1][4];
+    int tok[4];
+    auto code_row = [&](int t) {
+      return (t >= 0 ? page_of(t) + (t & 63) * kLatent : reinterpret_cast<const uint8_t*>(g_zeros)) + col * 16;
+    };
+    auto fetch = [&](int it) {
+      const int slot = it % kRing;
+      wait(&m->look_full[slot], (it / kRing) & 1);
 #pragma unroll
-          for (int k = 0; k < kKeysPerWarp; ++k) {
-            const long long o = __shfl_sync(0xffffffffu, off, k);
-            const uint8_t* src = p.cache + (o < 0 ? 0 : o) + lane * 16;
-            const int r = w * kKeysPerWarp + k;
-            cp_async16(tile + swz(r, lane), src, o < 0 ? 0u : 16u);
-            cp_async16(tile + swz(r, lane + 32), src + 512, o < 0 ? 0u : 16u);
-          }
+      for (int i = 0; i < 4; ++i) {
+        tok[i] = wait.ok ? token_at(slot, 4 * i + sub) : -1;
+        const uint8_t* row = code_row(tok[i]);
 #pragma unroll
-          for (int k4 = 0; k4 < kKeysPerWarp; k4 += 4) {
-            const int k = k4 + lane / 8;
-            const long long o = __shfl_sync(0xffffffffu, off, k);
-            cp_async16(tile + swz(w * kKeysPerWarp + k, 64 + lane % 8),
-                       p.cache + (o < 0 ? 0 : o) + kLatent * 2 + (lane % 8) * 16, o < 0 ? 0u : 16u);
-          }
-        }
-      } else {
-        // codes and scales into registers before the buffer is free
-        uint4 codes[kKeysPerWarp];
-        float scale[kKeysPerWarp];
-        const int my_slot = slot;
-#pragma unroll
-        for (int k = 0; k < kKeysPerWarp; ++k) {
-          const long long o = __shfl_sync(0xffffffffu, off, k);
-          const int sl = __shfl_sync(0xffffffffu, my_slot, k);
-          codes[k] = make_uint4(0u, 0u, 0u, 0u);
-          scale[k] = 0.f;
-          if (o >= 0) {
-            codes[k] = __ldg(reinterpret_cast<const uint4*>(p.cache + o) + lane);
-            // the page's start is o - slot * 512
-            scale[k] = __ldg(reinterpret_cast<const float*>(p.cache + o - sl * kLatent + kScaleOffsetFp8) +
-                             sl * kLatentGroups + lane / 8);
-          }
-        }
-        if (it >= 2) wait(&m->empty[g], ((it >> 1) - 1) & 1);
-        if (wait.ok) {
-#pragma unroll
-          for (int k4 = 0; k4 < kKeysPerWarp; k4 += 4) {
-            const int k = k4 + lane / 8;
-            const long long o = __shfl_sync(0xffffffffu, off, k);
-            const int sl = __shfl_sync(0xffffffffu, my_slot, k);
-            const uint8_t* src = p.cache + (o < 0 ? 0 : o - sl * kLatent + kRopeOffsetFp8 + sl * (kRope * 2));
-            cp_async16(tile + swz(w * kKeysPerWarp + k, 64 + lane % 8), src + (lane % 8) * 16, o < 0 ? 0u : 16u);
-          }
-#pragma unroll
-          for (int k = 0; k < kKeysPerWarp; ++k) {
-            uint4 a, b;
-            dequant16(codes[k], scale[k], a, b);
-            const int r = w * kKeysPerWarp + k;
-            // lanes 4-7 of each eight write their halves in the other order:
-            // no two lanes of a store meet in a bank
-            const int flip = (lane >> 2) & 1;
-            st_shared_v4(tile + swz(r, 2 * lane + flip), flip ? b : a);
-            st_shared_v4(tile + swz(r, 2 * lane + 1 - flip), flip ? a : b);
-          }
-        }
+        for (int part = 0; part < kParts - 1; ++part) codes[part][i] = ld_stream(row + part * 128);
       }
-      if (wait.ok) {
-        if (lane == 0) m->keymask[g][w] = mask | (badmask ? 0x10000u : 0u);
-        if (badmask && lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
-        if (walk.first) {
-          // this row's queries, by the group that brings the row's first tile
-          if (walk.piece > 0) wait(&m->qfree, (walk.piece - 1) & 1);
-          if (wait.ok) {
-            for (int h = w * 16; h < w * 16 + 16; ++h) {
-              const bool in = h < heads;
-              const uint32_t n = in ? 16u : 0u;
-              const long long hh = in ? head0 + h : head0;
-              const uint16_t* ql = p.ql + walk.row * p.ql_row + hh * p.ql_head;
-              const uint16_t* qr = p.qr + walk.row * p.qr_row + hh * p.qr_head;
-              cp_async16(sbase + kOffQ + swz(h, lane), ql + lane * 8, n);
-              cp_async16(sbase + kOffQ + swz(h, lane + 32), ql + 256 + lane * 8, n);
-              if (lane < 8) cp_async16(sbase + kOffQ + swz(h, 64 + lane), qr + lane * 8, n);
-            }
-          }
-        }
-      }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
+    };
+    if (kFp8 && walk.left > 0) fetch(0);
+
+    for (int it = 0; walk.left > 0; ++it) {
 #ifdef DSA_TEST_SKIP_FIRST_TILE
       // test builds only: never deliver the first tile, so that the waits for
       // it run out
-      if (it == 0) {
-        walk.step(p);
-        if (walk.left > 0) walk.step(p);
-        continue;
-      }
+      const bool deliver = it != 0;
+#else
+      constexpr bool deliver = true;
 #endif
-      if (wait.ok) mbar_arrive(&m->full[g]);
+      const bool mine_used = w * kKeysPerWarp < walk.tokens();  // else no product reads these rows
+      const int slot = it % kRing;
+      const uint32_t prev = (it - 1) & 1;
+      if (walk.first) {
+        // the row's queries; their place is free once the last scores are done
+        if (it > 0) wait(&m->sfull, prev);
+        if (wait.ok && !kFp8) {
+#pragma unroll 2
+          for (int h = w * 8; h < w * 8 + 8; ++h) {
+            const uint32_t n = h < heads ? 16u : 0u;
+            const long long hh = h < heads ? head0 + h : head0;
+            const uint16_t* ql = p.ql + walk.row * p.ql_row + hh * p.ql_head + lane * 8;
+            const uint32_t dst = sbase + kOffQ + sub * kQBlockBytes + h * 128 + ((col ^ (h & 7)) << 4);
+            cp_async16(dst, ql, n);
+            cp_async16(dst + 4 * kQBlockBytes, ql + 256, n);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int h = w * 8 + i * 4 + sub;
+            const long long hh = h < heads ? head0 + h : head0;
+            cp_async16(sbase + kOffQ + kRopeBlock * kQBlockBytes + h * 128 + ((col ^ (h & 7)) << 4),
+                       p.qr + walk.row * p.qr_row + hh * p.qr_head + col * 8, h < heads ? 16u : 0u);
+          }
+        } else if (wait.ok) {
+#pragma unroll 1
+          for (int h = w * 8; h < w * 8 + 8; ++h) {
+            uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a, r = a;
+            if (h < heads) {
+              const uint4* ql = reinterpret_cast<const uint4*>(p.ql + walk.row * p.ql_row + (head0 + h) * p.ql_head);
+              a = __ldg(ql + lane);
+              b = __ldg(ql + 32 + lane);
+              if (lane < 8)
+                r = __ldg(reinterpret_cast<const uint4*>(p.qr + walk.row * p.qr_row + (head0 + h) * p.qr_head) + lane);
+            }
+            float x[8], y[8];
+            unpack8(a, x);
+            unpack8(b, y);
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
+            top = warp_max(top);
+            // 2^n that brings the largest into [2^14, 2^15)
+            const int n = top > 0.f ? min(max(127 + 14 - (int)(__float_as_uint(top) >> 23), -100), 100) : 0;
+            const float f = __uint_as_float((uint32_t)(n + 127) << 23);
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 u = __floats2half2_rn(x[2 * j] * f, x[2 * j + 1] * f);
+              const __half2 v = __floats2half2_rn(y[2 * j] * f, y[2 * j + 1] * f);
+              o[j] = *reinterpret_cast<const uint32_t*>(&u);
+              o[4 + j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            const uint32_t dst = sbase + kOffQ + h * 128 + ((col ^ (h & 7)) << 4);
+            st_shared_v4(dst + sub * kQBlockBytes, make_uint4(o[0], o[1], o[2], o[3]));
+            st_shared_v4(dst + (4 + sub) * kQBlockBytes, make_uint4(o[4], o[5], o[6], o[7]));
+            if (lane < 8) {
+              unpack8(r, x);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 u = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
+                o[j] = *reinterpret_cast<const uint32_t*>(&u);
+              }
+              st_shared_v4(dst + kRopeBlock * kQBlockBytes, make_uint4(o[0], o[1], o[2], o[3]));
+            }
+            if (lane == 0) m->mul[walk.piece & 1][h] = p.scale_log2 * __uint_as_float((uint32_t)(127 - n) << 23);
+          }
+        }
+      }
+      if (!kFp8) {
+        // every address before the first part falls free
+        wait(&m->look_full[slot], (it / kRing) & 1);
+        const uint8_t* src[8];
+        const uint8_t* rsrc[4];
+        uint32_t valid = 0, rvalid = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = wait.ok ? token_at(slot, 2 * i + (lane >> 4)) : -1;
+          valid |= (t >= 0 ? 1u : 0u) << i;
+          src[i] = page_of(max(t, 0)) + (max(t, 0) & 63) * kTokenBytesBf16 + (lane & 15) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = wait.ok ? token_at(slot, 4 * i + sub) : -1;
+          rvalid |= (t >= 0 ? 1u : 0u) << i;
+          rsrc[i] = page_of(max(t, 0)) + (max(t, 0) & 63) * kTokenBytesBf16 + kLatent * 2 + col * 16;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->look_empty[slot]);
+        const uint32_t dst = sbase + ((lane >> 3) & 1) * kBlockBytes + (w * kKeysPerWarp + (lane >> 4)) * 128;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          if (it > 0) wait(&m->empty[part], prev);
+          if (wait.ok && mine_used) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              cp_async16(dst + part * kPartBytes + i * 256 + ((col ^ ((2 * i + (lane >> 4)) & 7)) << 4),
+                         src[i] + part * 256, (valid >> i) & 1 ? 16u : 0u);
+          }
+          cp_async_commit();
+        }
+        if (wait.ok && mine_used) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            cp_async16(sbase + kOffP + (w * kKeysPerWarp + 4 * i + sub) * 128 + ((col ^ ((4 * i + sub) & 7)) << 4),
+                       rsrc[i], (rvalid >> i) & 1 ? 16u : 0u);
+        }
+        cp_async_commit();
+        cp_async_wait<4>();
+        if (wait.ok && deliver) warp_arrive(&m->full[0], lane);
+        cp_async_wait<3>();
+        if (wait.ok && deliver) warp_arrive(&m->full[1], lane);
+        cp_async_wait<2>();
+        if (wait.ok && deliver) warp_arrive(&m->full[2], lane);
+        cp_async_wait<1>();
+        if (wait.ok && deliver) warp_arrive(&m->full[3], lane);
+        cp_async_wait<0>();
+        if (wait.ok && deliver) warp_arrive(&m->full[kParts], lane);
+        walk.step(p);
+      } else {
+        uint2 ratio[4];
+        wait(&m->scale_full[slot], (it / kRing) & 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ratio[i] = m->ratio[slot][w * kKeysPerWarp + 4 * i + sub];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->look_empty[slot]);
+        // lanes 4-7 of eight take their halves in the other order: no two
+        // lanes of a store meet in a bank
+        const int flip = col >> 2, c = (col & 3) * 2;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          if (it > 0) wait(&m->empty[part], prev);
+          if (wait.ok && mine_used) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t two = part < 2 ? ratio[i].x : ratio[i].y;
+              const uint32_t f = __byte_perm(two, two, part & 1 ? 0x3232 : 0x1010);
+              const uint4 c4 = codes[part % (kParts - 1)][i];
+              const uint4 a = widen8(flip ? c4.z : c4.x, flip ? c4.w : c4.y, f);
+              const uint4 b = widen8(flip ? c4.x : c4.z, flip ? c4.y : c4.w, f);
+              const int r = w * kKeysPerWarp + 4 * i + sub;
+              const uint32_t row = sbase + part * kPartBytes + flip * kBlockBytes + r * 128;
+              st_shared_v4(row + (((c + flip) ^ (r & 7)) << 4), a);
+              st_shared_v4(row + (((c + 1 - flip) ^ (r & 7)) << 4), b);
+            }
+          }
+          if (part == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) codes[0][i] = ld_stream(code_row(tok[i]) + (kParts - 1) * 128);
+          }
+          if (part == kParts - 1 && wait.ok && mine_used) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = max(tok[i], 0);
+              cp_async16(sbase + kOffP + (w * kKeysPerWarp + 4 * i + sub) * 128 + ((col ^ ((4 * i + sub) & 7)) << 4),
+                         page_of(t) + kRopeOffsetFp8 + (t & 63) * (kRope * 2) + col * 16, tok[i] < 0 ? 0u : 16u);
+            }
+          }
+          if (wait.ok && deliver) warp_arrive(&m->full[part], lane);
+        }
+        cp_async_wait_all();
+        if (wait.ok && deliver) warp_arrive(&m->full[kParts], lane);
+        walk.step(p);
+        if (walk.left > 0) fetch(it + 1);
+      }
+    }
+  } else if (warp >= kLookWarp0) {
+    // ---- token lookup ----------------------------------------------------------
+    fewer_registers<kRegsMisc>();
+    // tile i by warp i % 3: list and block table to token, and L2 asked for it
+    const int slot = warp - kLookWarp0;
+    for (int it = 0; walk.left > 0; ++it) {
+      if (it % kLookWarps == slot) {
+        const int n = walk.tokens();
+        int tok[4];
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = i * 32 + lane;
+          tok[i] = -1;                             // first the position
+          if (j < n) {
+            const int e = walk.u * kUnit + j;
+            tok[i] = p.idx ? __ldg(p.idx + walk.row * p.idx_stride + e) : e;
+          }
+          if (tok[i] >= walk.len) tok[i] = -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (tok[i] < 0) {
+            tok[i] = -1;
+            continue;
+          }
+          const int page = __ldg(p.block_table + walk.row * p.bt_stride + tok[i] / kPage);
+          const bool in = page >= 0 && page < p.num_pages;
+          tok[i] = in ? page * kPage + tok[i] % kPage : -1;
+          bad |= !in;
+        }
+        if (it >= kRing) wait(&m->look_empty[slot], (it / kRing - 1) & 1);
+        const bool any_bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = __ballot_sync(0xffffffffu, tok[i] >= 0);
+          if (wait.ok) {
+            m->token[slot][i * 32 + lane] = tok[i];
+            if (lane == 0) m->mask[slot][i] = v;
+          }
+        }
+        if (wait.ok && lane == 0) m->bad[slot] = any_bad;
+        if (any_bad && lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
+        __syncwarp();
+        if (wait.ok && lane == 0) mbar_arrive(&m->look_full[slot]);
+        if (kFp8) {
+          float4 sc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = max(tok[i], 0);
+            sc[i] = __ldg(reinterpret_cast<const float4*>(p.cache + (long long)(t >> 6) * p.page_stride +
+                                                          kScaleOffsetFp8) + (t & 63));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float most = fmaxf(fmaxf(fmaxf(sc[i].x, sc[i].y), fmaxf(sc[i].z, sc[i].w)), kSmallestScale);
+            const float inv = __frcp_rn(most);
+            const __half2 a = __floats2half2_rn(sc[i].x * inv, sc[i].y * inv);
+            const __half2 b = __floats2half2_rn(sc[i].z * inv, sc[i].w * inv);
+            const bool in = tok[i] >= 0;           // a masked token: zeros times zero
+            if (wait.ok) {
+              m->ratio[slot][i * 32 + lane] = make_uint2(in ? *reinterpret_cast<const uint32_t*>(&a) : 0u,
+                                                         in ? *reinterpret_cast<const uint32_t*>(&b) : 0u);
+              m->key_scale[slot][i * 32 + lane] = in ? most : 1.f;
+            }
+          }
+          __syncwarp();
+          if (wait.ok && lane == 0) mbar_arrive(&m->scale_full[slot]);
+        }
+        if (it > 0) {
+          // the first tile is loaded at once; the later ones wait for its place
+          if (p.idx == nullptr) {
+            // whole pages: the two units' first tokens
+            const int t0 = __shfl_sync(0xffffffffu, tok[0], 0), t1 = __shfl_sync(0xffffffffu, tok[2], 0);
+            const int t = lane == 0 ? t0 : lane == 1 ? t1 : -1;
+            if (t >= 0)
+              l2_prefetch_bulk(p.cache + (long long)(t >> 6) * p.page_stride,
+                               (uint32_t)(kFp8 ? kPageBytesFp8 : kPageBytesBf16));
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              const int t = i == 0 ? tok[0] : i == 1 ? tok[1] : i == 2 ? tok[2] : tok[3];
+              if (t < 0) continue;
+              const uint8_t* pg = p.cache + (long long)(t >> 6) * p.page_stride;
+              const int s = t & 63;
+              const uint8_t* row = pg + s * (kFp8 ? kLatent : kTokenBytesBf16);
+#pragma unroll
+              for (int j = 0; j < (kFp8 ? 4 : 9); ++j) l2_prefetch(row + j * 128);
+              if (kFp8) l2_prefetch(pg + kRopeOffsetFp8 + s * (kRope * 2));
+            }
+          }
+          if (walk.first)
+#pragma unroll 1
+            for (int h = lane; h < heads; h += 32) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                l2_prefetch(p.ql + walk.row * p.ql_row + (head0 + h) * p.ql_head + j * 64);
+              l2_prefetch(p.qr + walk.row * p.qr_row + (head0 + h) * p.qr_head);
+            }
+        }
+      }
       walk.step(p);
-      if (walk.left > 0) walk.step(p);
     }
   } else if (warp == kMmaWarp) {
     // ---- MMA issue -----------------------------------------------------------
-    if (lane == 0) {
-      const uint32_t q = sbase + kOffQ, pt = sbase + kOffP;
-      auto scores = [&](int it, bool last) {
-        wait(&m->full[it & 1], (it >> 1) & 1);
-        if (!wait.ok) return;
-        tc_fence_after();
-        fence_proxy_async_smem();
-        const uint32_t a = sbase + (it & 1) * kTileBytes;
-        const uint32_t d = tmem + kTmemS + (it & 1) * kAttnHeads;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16(d, smem_desc_sw128(a + b * kBlockBytes + k * 32, 1024),
-                    smem_desc_sw128(q + b * kBlockBytes + k * 32, 1024), kIdescS, b + k > 0);
-        mma_commit(&m->sfull[it & 1]);
-        if (last) mma_commit(&m->qfree);
-      };
-      TileWalk ahead = walk;
-      int it = 0;
-      if (walk.left > 0) scores(0, walk.last());
-      while (walk.left > 0) {
-        ahead.step(p);
-        const bool more = ahead.left > 0;
-        // the next tile's scores go before this tile's values, except across
-        // rows, where they wait for the next row's queries
-        if (more && !ahead.first) scores(it + 1, ahead.last());
-        wait(&m->pfull, it & 1);
-        if (walk.first && walk.piece > 0) wait(&m->ofree, (walk.piece - 1) & 1);
-        if (wait.ok) {
-          tc_fence_after();
-          const uint32_t a = sbase + (it & 1) * kTileBytes;
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt)
+    fewer_registers<kRegsMisc>();
+    if (elect_one()) {
+      Waiter<false> wait{p.status, true};
+      for (int it = 0; walk.left > 0; ++it) {
+        uint64_t a_d = smem_desc_sw128(sbase, 1024), b_d = smem_desc_sw128(sbase + kOffQ, 1024);
+#pragma unroll 1
+        for (int b = 0; b < 9; ++b) {
+          if (b % 2 == 0) {
+            wait(&m->full[b / 2], it & 1);
+            tc_fence_after();
+          }
+          const bool own = kFp8 && b == kRopeBlock;  // an accumulator of its own
+          if (wait.ok)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16(tmem + mt * kAttnHeads,
-                      smem_desc_mn_sw128(a + mt * 2 * kBlockBytes + k * 2048, kBlockBytes, 1024),
-                      smem_desc_mn_sw128(pt + k * 2048, kBlockBytes, 1024), kIdescO,
-                      (k > 0 || !walk.first) ? 1u : 0u);
-          mma_commit(&m->empty[it & 1]);
-          if (walk.last()) mma_commit(&m->ofull);
+              mma_f16(tmem + (own ? kTmemR : kTmemS), a_d + (k * 32 >> 4), b_d + (k * 32 >> 4),
+                      own ? kIdescRope : idesc_s(KV), k > 0 || (b > 0 && !own));
+          a_d += kBlockBytes >> 4;
+          b_d += kQBlockBytes >> 4;
         }
-        if (more && ahead.first) scores(it + 1, ahead.last());
-        walk = ahead;
-        ++it;
+        if (wait.ok) mma_commit(&m->sfull);
+        const int steps = (walk.tokens() + 15) / 16;
+        const uint32_t keep = walk.first ? 0u : 1u;
+        wait(&m->pfull, it & 1);
+        if (walk.first && walk.piece > 0) wait(&m->ofree, (walk.piece - 1) & 1);
+        tc_fence_after();
+        if (wait.ok) {
+          a_d = smem_desc_mn_sw128(sbase, kBlockBytes, 1024);
+          b_d = smem_desc_mn_sw128(sbase + kOffP, kBlockBytes, 1024);
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k)
+              mma_f16(tmem + part * kAttnHeads, a_d + k * (2048 >> 4), b_d + k * (2048 >> 4), idesc_o(KV),
+                      k > 0 ? 1u : keep);
+            a_d += kPartBytes >> 4;
+            mma_commit(&m->empty[part]);
+          }
+        }
+        walk.step(p);
       }
       if (!wait.ok) {
         // what was issued still runs: wait for it before TMEM is given back
@@ -534,191 +864,213 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     __syncwarp();
   } else {
     // ---- softmax and output --------------------------------------------------
-    // this thread: keys 16 warp + gq and + 8, heads 8j + 2c and + 1
-    const int gq = lane >> 2, c = lane & 3;
-    const uint32_t my_lanes = (uint32_t)(warp * 32) << 16;
-    const uint32_t prow = sbase + kOffP + (warp * 16 + gq) * 128;
-    float mx[16], sum[16];
-    bool bad = false;
-    int split_row = -1, split_last = 0;
-    long long tile_at = begin;                 // global index of the current tile
+    more_registers<kRegsSoftmax>();
+    // this thread: token 32 quarter + lane, heads 32 half .. 32 half + 31
+    const int quarter = warp & 3, half = warp >> 2;
+    const int hbase = half * 32, bar_half = 2 + half;
+    const uint32_t my_tmem = tmem + ((uint32_t)(quarter * 32) << 16) + hbase;
+    const int key = quarter * 32 + lane;
+    float sum[32];
+    bool bad = false, fresh = true;              // fresh: some head has no reference yet
+    int done = 0;                                // units of the slice behind
+    int* rec = reinterpret_cast<int*>(p.ws + (long long)gridDim.x * 2 * kPartialFloats) +
+               (long long)blockIdx.x * kSplitInts;
+    if (tid == 0) rec[0] = -1;
     for (int it = 0; walk.left > 0; ++it) {
+      const int slot = it % kRing;
       if (walk.first) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) mx[j] = -CUDART_INF_F, sum[j] = 0.f;
+        for (int j = 0; j < 32; ++j) sum[j] = 0.f;
         bad = false;
+        fresh = true;
       }
-      wait(&m->sfull[it & 1], (it >> 1) & 1);
-      wait(&m->full[it & 1], (it >> 1) & 1);   // the loaders' key mask
+      wait(&m->look_full[slot], (it / kRing) & 1);
+      const bool valid = (*reinterpret_cast<volatile uint32_t*>(&m->mask[slot][quarter]) >> lane) & 1;
+      bad |= *reinterpret_cast<volatile uint32_t*>(&m->bad[slot]) != 0;
+      if (kFp8) wait(&m->scale_full[slot], (it / kRing) & 1);
+      const float key_scale = kFp8 ? m->key_scale[slot][key] : 1.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m->look_empty[slot]);
+      wait(&m->sfull, it & 1);
       __syncwarp();
       tc_fence_after();
-      uint32_t r[32];
-      tmem_ld_16x256b_x8(tmem + my_lanes + kTmemS + (it & 1) * kAttnHeads, r);
-      const uint32_t km = *reinterpret_cast<volatile uint32_t*>(&m->keymask[it & 1][warp]);
-      const bool v0 = (km >> gq) & 1, v1 = (km >> (gq + 8)) & 1;
-      bad |= (km >> 16) & 1;
-      tmem_ld_wait32(r);
-      float s[32];
-      bool over = false;
+      // weights in log2 units over the reference, e = score - reference
+      float e[32];
+      const float key_log = kFp8 ? __log2f(key_scale) : 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float a = v0 ? __uint_as_float(r[4 * j + e]) * p.scale_log2 : -CUDART_INF_F;
-          const float b = v1 ? __uint_as_float(r[4 * j + 2 + e]) * p.scale_log2 : -CUDART_INF_F;
-          s[4 * j + e] = a, s[4 * j + 2 + e] = b;
-          const float lim = mx[2 * j + e] + kSlack;
-          over |= a > lim || b > lim;
+      for (int i = 0; i < 4; ++i) {
+        uint32_t x[8], y[8];
+        tmem_ld_32x32b_x8(my_tmem + kTmemS + 8 * i, x);
+        if (kFp8) {
+          tmem_ld_32x32b_x8(my_tmem + kTmemR + 8 * i, y);
+          tmem_ld_wait8(x, y);
+        } else {
+          tmem_ld_wait8(x);
         }
-      // P's buffer and O^T are free once the previous tile's values are added
-      if (it > 0) wait(&m->empty[(it - 1) & 1], ((it - 1) >> 1) & 1);
-      if (bar_any(1, 128, over)) {
-        float top[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float v = fmaxf(s[4 * (j / 2) + j % 2], s[4 * (j / 2) + 2 + j % 2]);
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          top[j] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        for (int j4 = 0; j4 < 8; j4 += 4) {
+          const float4 n4 = *reinterpret_cast<const float4*>(&m->nref[hbase + 8 * i + j4]);
+          const float nref[4] = {n4.x, n4.y, n4.z, n4.w};
+          float mul[4] = {p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2};
+          if (kFp8) {
+            const float4 m4 = *reinterpret_cast<const float4*>(&m->mul[walk.piece & 1][hbase + 8 * i + j4]);
+            mul[0] = m4.x, mul[1] = m4.y, mul[2] = m4.z, mul[3] = m4.w;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float v = __uint_as_float(x[j4 + u]);
+            if (kFp8) v = fmaf(v, key_scale, __uint_as_float(y[j4 + u]));
+            e[8 * i + j4 + u] = fmaf(v, mul[u], nref[u]);
+          }
         }
-        if (gq == 0)
+      }
+      if (!valid)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) m->red[warp][8 * (j / 2) + 2 * c + j % 2] = top[j];
-        bar_sync(1, 128);
+        for (int j = 0; j < 32; ++j) e[j] = -CUDART_INF_F;
+      float most = e[0];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int h = 8 * (j / 2) + 2 * c + j % 2;
-          const float v = fmaxf(fmaxf(m->red[0][h], m->red[1][h]), fmaxf(m->red[2][h], m->red[3][h]));
-          const float now = fmaxf(mx[j], v);
-          const float f = now == mx[j] ? 1.f : ex2(mx[j] - now);
-          mx[j] = now;
-          sum[j] *= f;
-          if (warp == 0 && gq == 0) m->fac[h] = f;
+      for (int j = 1; j < 32; ++j) most = fmaxf(most, e[j]);
+      if (bar_any(bar_half, 128, fresh || most + key_log > ref_limit(KV))) {
+        // the tile's largest weight of each head, and the reference raised
+        // where it has to be
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float v = warp_max(e[j] + key_log);
+          top = lane == j ? v : top;
         }
+        const int h = hbase + lane;
+        m->red[quarter][h] = top;
+        bar_sync(bar_half, 128);
+        const float v = fmaxf(fmaxf(m->red[0][h], m->red[1][h]), fmaxf(m->red[2][h], m->red[3][h]));
+        const float old = m->nref[h];
+        const bool unset = __float_as_uint(old) == kUnset, seen = v > -CUDART_INF_F;
+        fresh = __any_sync(0xffffffffu, unset && !seen);
+        bar_sync(bar_half, 128);
+        if (quarter == 0) {
+          const float up = seen && (unset || v > ref_limit(KV)) ? v - ref_below(KV) : 0.f;
+          if (seen) m->nref[h] = (unset ? 0.f : old) - up;
+          m->fac[h] = up;
+          m->keep[h] = unset ? 1.f : ex2(-up);            // sums of an unset head are zero
+        }
+        bar_sync(bar_half, 128);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) e[j] -= m->fac[hbase + j];
         if (!walk.first) {
-          bar_sync(1, 128);
-          tc_fence_after();
-#pragma unroll 1
-          for (int col = 0; col < 4 * kAttnHeads; col += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(tmem + my_lanes + col, o);
-            tmem_ld_wait32(o);
+          // the scores' commit covers the last value product: O^T is at rest
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * m->fac[(col & 32) + j]);
-            tmem_st_32x32b_x32(tmem + my_lanes + col, o);
+          for (int j = 0; j < 32; ++j) sum[j] *= m->keep[hbase + j];
+#pragma unroll 1
+          for (int i = 0; i < 4 * kParts; ++i) {
+            uint32_t o[8];
+            const int c = (i & 3) * 8;
+            if (__all_sync(0xffffffffu, m->keep[hbase + c + (lane & 7)] == 1.f)) continue;
+            const uint32_t at = my_tmem + (i >> 2) * kAttnHeads + c;
+            tmem_ld_32x32b_x8(at, o);
+            tmem_ld_wait8(o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * m->keep[hbase + c + j]);
+            tmem_st_32x32b_x8(at, o);
           }
           tmem_st_wait();
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float pr[4];
+      for (int j8 = 0; j8 < 32; j8 += 8) {
+        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float ref = mx[2 * j + e] == -CUDART_INF_F ? 0.f : mx[2 * j + e];
-          pr[e] = ex2(s[4 * j + e] - ref);
-          pr[2 + e] = ex2(s[4 * j + 2 + e] - ref);
-          sum[2 * j + e] += pr[e] + pr[2 + e];
+        for (int u = 0; u < 8; u += 2) {
+          const float a = ex2(e[j8 + u]), b = ex2(e[j8 + u + 1]);
+          sum[j8 + u] += a;
+          sum[j8 + u + 1] += b;
+          if (kFp8) {
+            const __half2 v = __floats2half2_rn(a * key_scale, b * key_scale);
+            w[u / 2] = *reinterpret_cast<const uint32_t*>(&v);
+          } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+            w[u / 2] = *reinterpret_cast<const uint32_t*>(&v);
+          }
         }
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(pr[0], pr[1]), hi = __floats2bfloat162_rn(pr[2], pr[3]);
-        // rows gq and gq + 8 swizzle alike
-        const uint32_t at = prow + ((j ^ gq) << 4) + c * 4;
-        st_shared_u32(at, *reinterpret_cast<const uint32_t*>(&lo));
-        st_shared_u32(at + 8 * 128, *reinterpret_cast<const uint32_t*>(&hi));
+        st_shared_v4(sbase + kOffP + key * 128 + (((hbase + j8) / 8 ^ (key & 7)) << 4),
+                     make_uint4(w[0], w[1], w[2], w[3]));
       }
-      fence_proxy_async_smem();
       tc_fence_before();
-      if (wait.ok) mbar_arrive(&m->pfull);
-      ++tile_at;
+      if (wait.ok) warp_arrive(&m->pfull, lane);
+      done += walk.count();
 
       if (walk.last()) {
         // ---- the piece's result ------------------------------------------------
-        const bool whole = walk.t + 1 == walk.tiles() && tile_at - begin >= walk.tiles();
-        const bool begins = tile_at - begin > walk.t;   // the piece holds the row's first tile
-        bar_sync(1, 128);                               // every use of red and fac is over
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 4);
-          sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
-          sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
-        }
-        if (gq == 0)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) m->red[warp][8 * (j / 2) + 2 * c + j % 2] = sum[j];
-        if (warp == 0 && gq == 0)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) m->fac[8 * (j / 2) + 2 * c + j % 2] = mx[j];
-        wait(&m->ofull, walk.piece & 1);
-        bad = bar_any(1, 128, bad || !wait.ok);
-        float* slot = p.ws + ((long long)blockIdx.x * 2 + (begins ? 1 : 0)) * kPartialFloats;
-        float total_h = 0.f, max_h = 0.f;
-        if (warp < 2) {
-          const int h = warp * 32 + lane;
-          total_h = m->red[0][h] + m->red[1][h] + m->red[2][h] + m->red[3][h];
-          max_h = m->fac[h];
-          if (bad) total_h = CUDART_NAN_F, max_h = 0.f;
-        }
-        bar_sync(1, 128);
-        if (warp < 2) {
-          const int h = warp * 32 + lane;
+        const int u_end = walk.u + walk.count();          // the row's units done so far
+        const bool begins = done >= u_end;                // the piece holds the row's first unit
+        const bool whole = begins && u_end == walk.units();
+        bar_sync(bar_half, 128);                          // every use of red and fac is over
+        m->red[quarter][hbase + lane] = sum_columns(sum, lane);
+        wait(&m->empty[kParts - 1], it & 1);              // the last value product
+        bad = bar_any(bar_half, 128, bad || !wait.ok);
+        float* part_at = p.ws + ((long long)blockIdx.x * 2 + (begins ? 1 : 0)) * kPartialFloats;
+        if (quarter == 0) {
+          const int h = hbase + lane;
+          float total_h = m->red[0][h] + m->red[1][h] + m->red[2][h] + m->red[3][h];
+          const float nref = m->nref[h];
+          const float max_h = bad ? 0.f : __float_as_uint(nref) == kUnset ? -CUDART_INF_F : -nref;
+          if (bad) total_h = CUDART_NAN_F;
           if (whole) {
-            m->fac[h] = bad ? CUDART_NAN_F : total_h == 0.f ? 0.f : 1.f / total_h;
+            m->fac[h] = total_h == 0.f ? 0.f : 1.f / total_h;
             if (p.lse && h < heads)
               p.lse[(long long)walk.row * p.H + head0 + h] = (max_h + log2f(total_h)) * 0.69314718055994531f;
           } else {
             m->fac[h] = bad ? CUDART_NAN_F : 1.f;
-            slot[kAttnHeads * kLatent + h] = max_h;
-            slot[kAttnHeads * kLatent + kAttnHeads + h] = total_h;
+            part_at[kAttnHeads * kLatent + h] = max_h;
+            part_at[kAttnHeads * kLatent + kAttnHeads + h] = total_h;
           }
+          m->nref[h] = __uint_as_float(kUnset);
         }
-        bar_sync(1, 128);
+        bar_sync(bar_half, 128);
         tc_fence_after();
 #pragma unroll 1
-        for (int col = 0; col < 4 * kAttnHeads; col += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(tmem + my_lanes + col, o);
-          tmem_ld_wait32(o);
-          const int h0 = col & 32, dim = (col / kAttnHeads) * 128 + warp * 32 + lane;
-          if (col == 4 * kAttnHeads - 32) {
+        for (int i = 0; i < 4 * kParts; ++i) {
+          // eight heads of a part at a time: a short loop
+          uint32_t o[8];
+          const int h0 = hbase + (i & 3) * 8, dim = (i >> 2) * 128 + key;
+          tmem_ld_32x32b_x8(my_tmem + (i >> 2) * kAttnHeads + (i & 3) * 8, o);
+          tmem_ld_wait8(o);
+          if (i == 4 * kParts - 1) {
             tc_fence_before();
-            if (wait.ok) mbar_arrive(&m->ofree);
+            __syncwarp();
+            if (wait.ok && lane == 0) mbar_arrive(&m->ofree);
           }
+          if (h0 >= heads) continue;
+          const float4 fa = *reinterpret_cast<const float4*>(&m->fac[h0]);
+          const float4 fb = *reinterpret_cast<const float4*>(&m->fac[h0 + 4]);
+          const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
           if (whole) {
             // two heads of a lane pair: each lane writes two values of one head
-            uint16_t* dst = p.out + walk.row * p.out_row + (dim & ~1);
+            uint16_t* dst =
+                p.out + walk.row * p.out_row + (long long)(head0 + h0 + (lane & 1)) * p.out_head + (dim & ~1);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float a = __uint_as_float(o[j]) * m->fac[h0 + j];
-              const float b = __uint_as_float(o[j + 1]) * m->fac[h0 + j + 1];
+            for (int j = 0; j < 8; j += 2) {
+              const float a = __uint_as_float(o[j]) * f[j], b = __uint_as_float(o[j + 1]) * f[j + 1];
               const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-              const __nv_bfloat162 v =
-                  lane & 1 ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
-              const int h = h0 + j + (lane & 1);
-              if (h < heads)
-                *reinterpret_cast<__nv_bfloat162*>(dst + (long long)(head0 + h) * p.out_head) = v;
+              const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
+              if (h0 + j + (lane & 1) < heads) *reinterpret_cast<__nv_bfloat162*>(dst) = v;
+              dst += 2 * p.out_head;
             }
           } else {
+            float* dst = part_at + h0 * kLatent + dim;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (h0 + j < heads) slot[(h0 + j) * kLatent + dim] = __uint_as_float(o[j]) * m->fac[h0 + j];
+            for (int j = 0; j < 8; ++j)
+              if (h0 + j < heads) dst[j * kLatent] = __uint_as_float(o[j]) * f[j];
           }
         }
-        bar_sync(1, 128);   // fac and red are free again
-        if (!whole && begins) {
-          // the row goes on in later CTAs: the one that holds its last tile
-          const long long last_tile = tile_at - 1 + (walk.tiles() - 1 - walk.t);
-          split_row = walk.row;
-          split_last = (int)(((last_tile + 1) * ctas - 1) / total);
+        bar_sync(bar_half, 128);                          // fac and red are free again
+        if (!whole && begins && tid == 0) {
+          // the row goes on in later CTAs: the one that holds its last unit
+          const long long last_unit = (long long)m->begin + done - 1 + (walk.units() - u_end);
+          rec[0] = walk.row;
+          rec[1] = (int)(((last_unit + 1) * m->ctas - 1) / m->total);
         }
       }
       walk.step(p);
-    }
-    if (tid == 0) {
-      int* rec = reinterpret_cast<int*>(p.ws + (long long)gridDim.x * 2 * kPartialFloats) +
-                 (long long)blockIdx.x * kSplitInts;
-      rec[0] = split_row;
-      rec[1] = split_last;
     }
   }
 

@@ -269,3 +269,13 @@ def test_graph_replay_with_other_lengths(kv):
         graph.replay()
         torch.cuda.synchronize()
         c.check()
+
+
+@pytest.mark.parametrize("kv", KVS)
+def test_many_short_rows_again_and_again(kv):
+    """Rows of one tile, several per slice: queries and tile change places at every step."""
+    c = Case([40] * 300 + [128] * 40, 64, kv, seed=19)
+    first = c.run().out.clone()
+    c.check(rows=range(0, 340, 11))
+    for _ in range(8):
+        assert torch.equal(c.run().out, first)
