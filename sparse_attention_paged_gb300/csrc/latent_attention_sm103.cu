@@ -111,18 +111,22 @@ struct Misc {
   uint64_t done;
   uint32_t tmem;
   int start_row, start_unit, nzero;
-  int begin, total, ctas;      // the slice's first unit, the call's units, the CTAs that have one
+  int begin, end, total, ctas; // the slice's units, the call's units, the CTAs that have one
   int scan[kAttnThreads / 32];
   alignas(16) uint2 ratio[kRing][kTile];  // fp8: each part's scale over s(t), fp16
   int token[kRing][kTile];     // page * 64 + slot, -1 when masked
   float key_scale[kRing][kTile];  // fp8: s(t)
   uint32_t mask[kRing][4];     // valid tokens
-  uint32_t bad[kRing];         // a visible token has no page
+  uint32_t flags[kRing];       // kFirst: a row begins; kLast: it or its part ends; kEnd: so does the slice;
+                               // kBad: a visible token has no page
+  int4 piece[8];               // of the rows or parts under way: row, kBegins | kWhole
   alignas(16) float red[4][kAttnHeads];  // per quarter of the tokens and head
   float nref[kAttnHeads];      // -reference, in log2 units; nref, mul, fac are read as float4
   float mul[2][kAttnHeads];    // fp8: from a head's score sums to log2 units, this row's and the next one's
   float fac[kAttnHeads], keep[kAttnHeads];
 };
+constexpr uint32_t kFirst = 1, kLast = 2, kEnd = 4, kBad = 8;
+constexpr int kBegins = 1, kWhole = 2;          // a part holds its row's first unit / all of them
 constexpr int kMiscBytes = 9 * 1024;
 constexpr int kSmemBytes = kOffMisc + kMiscBytes + 1024;
 static_assert(sizeof(Misc) <= kMiscBytes, "misc");
@@ -231,6 +235,18 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&a)[8]) {
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7])
                :
                : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&a)[32]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+        "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]),
+        "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]),
+        "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]),
+        "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
+      :
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&a)[8], uint32_t (&b)[8]) {
@@ -381,6 +397,12 @@ __device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
   return v[0];
 }
 
+// Which row a CTA's slice leaves unfinished (-1: none), and the CTA with its
+// last unit.
+__device__ __forceinline__ int* split_record(const LatentAttnParams& p) {
+  return reinterpret_cast<int*>(p.ws + (long long)gridDim.x * 2 * kPartialFloats) + (long long)blockIdx.x * kSplitInts;
+}
+
 // What a masked token's codes are read from.
 __device__ const uint4 g_zeros[kLatent / 16] = {};
 
@@ -471,7 +493,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       m->start_row = r;
       m->start_unit = begin - at;
     }
-    if (tid == 0) m->begin = begin, m->total = total, m->ctas = ctas;
+    if (tid == 0) {
+      m->begin = begin, m->end = end, m->total = total, m->ctas = ctas;
+      split_record(p)[0] = -1;
+    }
     __syncthreads();
     if (zeros) {
       // rows without a visible token: zeros (a length past the table: NaN); the
@@ -717,6 +742,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     for (int it = 0; walk.left > 0; ++it) {
       if (it % kLookWarps == slot) {
         const int n = walk.tokens();
+        uint32_t flags = (walk.first ? kFirst : 0) | (walk.last() ? kLast : 0) | (walk.left == walk.count() ? kEnd : 0);
         int tok[4];
         bool bad = false;
 #pragma unroll
@@ -750,7 +776,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
             if (lane == 0) m->mask[slot][i] = v;
           }
         }
-        if (wait.ok && lane == 0) m->bad[slot] = any_bad;
+        if (wait.ok && lane == 0) {
+          m->flags[slot] = flags | (any_bad ? kBad : 0);
+          if (walk.first) {
+            const bool begins = walk.u == 0, whole = begins && walk.left >= walk.units();
+            m->piece[walk.piece & 7] = make_int4(walk.row, (begins ? kBegins : 0) | (whole ? kWhole : 0), 0, 0);
+            if (begins && !whole) {
+              // the row goes on in later CTAs
+              const long long last_unit = (long long)m->end - walk.left + walk.units() - 1;
+              split_record(p)[0] = walk.row;
+              split_record(p)[1] = (int)(((last_unit + 1) * m->ctas - 1) / m->total);
+            }
+          }
+        }
         if (any_bad && lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
         __syncwarp();
         if (wait.ok && lane == 0) mbar_arrive(&m->look_full[slot]);
@@ -871,22 +909,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     const uint32_t my_tmem = tmem + ((uint32_t)(quarter * 32) << 16) + hbase;
     const int key = quarter * 32 + lane;
     float sum[32];
-    bool bad = false, fresh = true;              // fresh: some head has no reference yet
-    int done = 0;                                // units of the slice behind
-    int* rec = reinterpret_cast<int*>(p.ws + (long long)gridDim.x * 2 * kPartialFloats) +
-               (long long)blockIdx.x * kSplitInts;
-    if (tid == 0) rec[0] = -1;
-    for (int it = 0; walk.left > 0; ++it) {
+    // rows and parts come as the lookup warps found them: no walk of its own
+    bool bad = false, fresh = true, more = m->end > m->begin;  // fresh: some head has no reference yet
+    uint32_t piece = 0;
+    for (int it = 0; more; ++it) {
       const int slot = it % kRing;
-      if (walk.first) {
+      wait(&m->look_full[slot], (it / kRing) & 1);
+      // a wait that ran out (here, or for the last tile) ends the loop, for the
+      // four warps together: they meet at barriers
+      if (bar_any(bar_half, 128, !wait.ok)) break;
+      const bool valid = (*reinterpret_cast<volatile uint32_t*>(&m->mask[slot][quarter]) >> lane) & 1;
+      const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&m->flags[slot]);
+      more = !(flags & kEnd);
+      if (flags & kFirst) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) sum[j] = 0.f;
         bad = false;
         fresh = true;
       }
-      wait(&m->look_full[slot], (it / kRing) & 1);
-      const bool valid = (*reinterpret_cast<volatile uint32_t*>(&m->mask[slot][quarter]) >> lane) & 1;
-      bad |= *reinterpret_cast<volatile uint32_t*>(&m->bad[slot]) != 0;
+      bad |= (flags & kBad) != 0;
       if (kFp8) wait(&m->scale_full[slot], (it / kRing) & 1);
       const float key_scale = kFp8 ? m->key_scale[slot][key] : 1.f;
       __syncwarp();
@@ -913,7 +954,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           const float nref[4] = {n4.x, n4.y, n4.z, n4.w};
           float mul[4] = {p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2};
           if (kFp8) {
-            const float4 m4 = *reinterpret_cast<const float4*>(&m->mul[walk.piece & 1][hbase + 8 * i + j4]);
+            const float4 m4 = *reinterpret_cast<const float4*>(&m->mul[piece & 1][hbase + 8 * i + j4]);
             mul[0] = m4.x, mul[1] = m4.y, mul[2] = m4.z, mul[3] = m4.w;
           }
 #pragma unroll
@@ -956,7 +997,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         bar_sync(bar_half, 128);
 #pragma unroll
         for (int j = 0; j < 32; ++j) e[j] -= m->fac[hbase + j];
-        if (!walk.first) {
+        if (!(flags & kFirst)) {
           // the scores' commit covers the last value product: O^T is at rest
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[j] *= m->keep[hbase + j];
@@ -996,17 +1037,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       }
       tc_fence_before();
       if (wait.ok) warp_arrive(&m->pfull, lane);
-      done += walk.count();
 
-      if (walk.last()) {
+      if (flags & kLast) {
         // ---- the piece's result ------------------------------------------------
-        const int u_end = walk.u + walk.count();          // the row's units done so far
-        const bool begins = done >= u_end;                // the piece holds the row's first unit
-        const bool whole = begins && u_end == walk.units();
         bar_sync(bar_half, 128);                          // every use of red and fac is over
         m->red[quarter][hbase + lane] = sum_columns(sum, lane);
         wait(&m->empty[kParts - 1], it & 1);              // the last value product
         bad = bar_any(bar_half, 128, bad || !wait.ok);
+        const int4 what = m->piece[piece & 7];
+        const bool begins = what.y & kBegins, whole = what.y & kWhole;
         float* part_at = p.ws + ((long long)blockIdx.x * 2 + (begins ? 1 : 0)) * kPartialFloats;
         if (quarter == 0) {
           const int h = hbase + lane;
@@ -1017,7 +1056,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           if (whole) {
             m->fac[h] = total_h == 0.f ? 0.f : 1.f / total_h;
             if (p.lse && h < heads)
-              p.lse[(long long)walk.row * p.H + head0 + h] = (max_h + log2f(total_h)) * 0.69314718055994531f;
+              p.lse[(long long)what.x * p.H + head0 + h] = (max_h + log2f(total_h)) * 0.69314718055994531f;
           } else {
             m->fac[h] = bad ? CUDART_NAN_F : 1.f;
             part_at[kAttnHeads * kLatent + h] = max_h;
@@ -1028,49 +1067,75 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         bar_sync(bar_half, 128);
         tc_fence_after();
 #pragma unroll 1
-        for (int i = 0; i < 4 * kParts; ++i) {
-          // eight heads of a part at a time: a short loop
-          uint32_t o[8];
-          const int h0 = hbase + (i & 3) * 8, dim = (i >> 2) * 128 + key;
-          tmem_ld_32x32b_x8(my_tmem + (i >> 2) * kAttnHeads + (i & 3) * 8, o);
-          tmem_ld_wait8(o);
-          if (i == 4 * kParts - 1) {
+        for (int part = 0; part < kParts; ++part) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(my_tmem + part * kAttnHeads, o);
+          tmem_ld_wait32(o);
+          const int dim = part * 128 + key;
+          if (part == kParts - 1) {
             tc_fence_before();
             __syncwarp();
             if (wait.ok && lane == 0) mbar_arrive(&m->ofree);
           }
-          if (h0 >= heads) continue;
-          const float4 fa = *reinterpret_cast<const float4*>(&m->fac[h0]);
-          const float4 fb = *reinterpret_cast<const float4*>(&m->fac[h0 + 4]);
-          const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
           if (whole) {
             // two heads of a lane pair: each lane writes two values of one head
             uint16_t* dst =
-                p.out + walk.row * p.out_row + (long long)(head0 + h0 + (lane & 1)) * p.out_head + (dim & ~1);
+                p.out + what.x * p.out_row + (long long)(head0 + hbase + (lane & 1)) * p.out_head + (dim & ~1);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const float a = __uint_as_float(o[j]) * f[j], b = __uint_as_float(o[j + 1]) * f[j + 1];
-              const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-              const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
-              if (h0 + j + (lane & 1) < heads) *reinterpret_cast<__nv_bfloat162*>(dst) = v;
-              dst += 2 * p.out_head;
+            for (int j4 = 0; j4 < 32; j4 += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&m->fac[hbase + j4]);
+              const float v[4] = {__uint_as_float(o[j4]) * f.x, __uint_as_float(o[j4 + 1]) * f.y,
+                                  __uint_as_float(o[j4 + 2]) * f.z, __uint_as_float(o[j4 + 3]) * f.w};
+#pragma unroll
+              for (int u = 0; u < 4; u += 2) {
+                const float mine = lane & 1 ? v[u + 1] : v[u];
+                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? v[u] : v[u + 1], 1);
+                const __nv_bfloat162 r = __floats2bfloat162_rn(lane & 1 ? other : mine, lane & 1 ? mine : other);
+                if (hbase + j4 + u + (lane & 1) < heads) *reinterpret_cast<__nv_bfloat162*>(dst) = r;
+                dst += 2 * p.out_head;
+              }
             }
           } else {
-            float* dst = part_at + h0 * kLatent + dim;
+            float* dst = part_at + hbase * kLatent + dim;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (h0 + j < heads) dst[j * kLatent] = __uint_as_float(o[j]) * f[j];
+            for (int j4 = 0; j4 < 32; j4 += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&m->fac[hbase + j4]);
+              const float v[4] = {__uint_as_float(o[j4]) * f.x, __uint_as_float(o[j4 + 1]) * f.y,
+                                  __uint_as_float(o[j4 + 2]) * f.z, __uint_as_float(o[j4 + 3]) * f.w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (hbase + j4 + u < heads) dst[(j4 + u) * kLatent] = v[u];
+            }
           }
         }
         bar_sync(bar_half, 128);                          // fac and red are free again
-        if (!whole && begins && tid == 0) {
-          // the row goes on in later CTAs: the one that holds its last unit
-          const long long last_unit = (long long)m->begin + done - 1 + (walk.units() - u_end);
-          rec[0] = walk.row;
-          rec[1] = (int)(((last_unit + 1) * m->ctas - 1) / m->total);
+        ++piece;
+      }
+    }
+    if (more) {
+      // a wait ran out: the rows and parts from this one on are NaN
+      walk.start(p, m->start_row, m->start_unit, m->end - m->begin);
+      for (uint32_t i = 0; walk.left > 0; walk.step(p)) {
+        if (!walk.first) continue;
+        if (i++ < piece) continue;
+        const bool begins = walk.u == 0, whole = begins && walk.left >= walk.units();
+        float* part_at = p.ws + ((long long)blockIdx.x * 2 + (begins ? 1 : 0)) * kPartialFloats;
+        for (int h = hbase; h < min(heads, hbase + 32); ++h) {
+          for (int d = key; whole && d < kLatent; d += 128)
+            p.out[walk.row * p.out_row + (long long)(head0 + h) * p.out_head + d] = 0x7fff;
+          if (key != 0) continue;
+          if (whole && p.lse) p.lse[(long long)walk.row * p.H + head0 + h] = CUDART_NAN_F;
+          if (!whole) {
+            part_at[kAttnHeads * kLatent + h] = 0.f;
+            part_at[kAttnHeads * kLatent + kAttnHeads + h] = CUDART_NAN_F;
+          }
+        }
+        if (begins && !whole && tid == 0) {
+          const long long last_unit = (long long)m->end - walk.left + walk.units() - 1;
+          split_record(p)[0] = walk.row;
+          split_record(p)[1] = (int)(((last_unit + 1) * m->ctas - 1) / m->total);
         }
       }
-      walk.step(p);
     }
   }
 
