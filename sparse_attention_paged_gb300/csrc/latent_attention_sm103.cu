@@ -45,8 +45,8 @@
 // them, so one long row or a few short ones spread over every SM, and a
 // batch of any lengths is balanced.
 //
-// Warps: 0-7 softmax and output, 8 MMA issue, 9-11 token lookup, 12-19
-// loaders.  The lookup warps go through selection list and block table up to
+// Warps: 0-7 softmax and output, 8 MMA issue, 9-11 token lookup, 12-27
+// loaders (four on each scheduler: the conversion is bound by latency).  The lookup warps go through selection list and block table up to
 // three tiles ahead and ask L2 for the tokens' bytes, which keeps HBM busy
 // whatever the tile buffer does.  The loaders copy (bf16) or convert (fp8) 16
 // bytes at a time; masked tokens are not read, their rows are zeros.
@@ -79,14 +79,15 @@ constexpr int kBlockBytes = kTile * 128;        // 64 values of a tile's tokens
 constexpr int kPartBytes = 2 * kBlockBytes;
 constexpr int kRopeBlock = 8;                   // index of the rotated part's block
 constexpr int kQBlockBytes = kAttnHeads * 128;  // 64 values of the queries
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLookWarp0 = 9, kLookWarps = 3, kLoadWarp0 = 12, kLoadWarps = 8;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLookWarp0 = 9, kLookWarps = 3, kLoadWarp0 = 12, kLoadWarps = 16;
 constexpr int kAttnThreads = (kLoadWarp0 + kLoadWarps) * 32;
 // Tiles of looked-up tokens: one slot per lookup warp, so that no warp can be
 // two phases of a slot's barrier ahead of another.
 constexpr int kRing = kLookWarps;
-constexpr int kKeysPerWarp = kTile / kLoadWarps;  // 16
-// Registers per thread: at launch (65,536 / 640 in steps of 8), then per role.
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsMisc = 64, kRegsLoad = 104;
+constexpr int kKeysPerWarp = kTile / kLoadWarps;  // 8
+constexpr int kHeadsPerWarp = kAttnHeads / kLoadWarps;  // 4
+// Registers per thread: at launch (65,536 / 896 in steps of 8), then per role.
+constexpr int kRegsLaunch = 72, kRegsSoftmax = 104, kRegsMisc = 64, kRegsLoad = 56;
 static_assert(kSoftmaxWarps * kRegsSoftmax + 4 * kRegsMisc + kLoadWarps * kRegsLoad <=
                   kAttnThreads / 32 * kRegsLaunch,
               "the roles' registers are those of the launch");
@@ -117,15 +118,15 @@ struct Misc {
   int token[kRing][kTile];     // page * 64 + slot, -1 when masked
   float key_scale[kRing][kTile];  // fp8: s(t)
   uint32_t mask[kRing][4];     // valid tokens
-  uint32_t flags[kRing];       // kFirst: a row begins; kLast: it or its part ends; kEnd: so does the slice;
-                               // kBad: a visible token has no page
+  int4 tile[kRing];            // row, tokens, flags, piece; flags: kFirst: a row or a part of one begins;
+                               // kLast: it ends; kEnd: so does the slice; kBad: a visible token has no page
   int4 piece[8];               // of the rows or parts under way: row, kBegins | kWhole
   alignas(16) float red[4][kAttnHeads];  // per quarter of the tokens and head
   float nref[kAttnHeads];      // -reference, in log2 units; nref, mul, fac are read as float4
   float mul[2][kAttnHeads];    // fp8: from a head's score sums to log2 units, this row's and the next one's
   float fac[kAttnHeads], keep[kAttnHeads];
 };
-constexpr uint32_t kFirst = 1, kLast = 2, kEnd = 4, kBad = 8;
+constexpr int kFirst = 1, kLast = 2, kEnd = 4, kBad = 8;
 constexpr int kBegins = 1, kWhole = 2;          // a part holds its row's first unit / all of them
 constexpr int kMiscBytes = 9 * 1024;
 constexpr int kSmemBytes = kOffMisc + kMiscBytes + 1024;
@@ -237,18 +238,6 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&a)[8]) {
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&a)[32]) {
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
-        "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]),
-        "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]),
-        "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]),
-        "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
-      :
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&a)[8], uint32_t (&b)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
@@ -324,9 +313,10 @@ struct TileWalk {
   }
 };
 
-// Waits, by a whole warp together (every lane gets the same answer) or by one
-// lane.  After one that ran out the rest return at once.  Short, because it is
-// inlined everywhere: the loops of five roles share the instruction caches.
+// Waits, by a whole warp together (every lane asks, and all get the same
+// answer: the hardware then puts the warp to sleep, which it does not when
+// one lane asks for the others) or by one lane.  After one that ran out the
+// rest return at once.
 template <bool WARP>
 struct Waiter {
   int* status;
@@ -533,35 +523,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
 
   if (warp >= kLoadWarp0) {
     // ---- loaders -------------------------------------------------------------
-    more_registers<kRegsLoad>();
-    // warp w brings tokens 16w .. 16w+15 of every tile
+    fewer_registers<kRegsLoad>();
+    // warp w brings tokens 8w .. 8w+7 of every tile
     const int w = warp - kLoadWarp0;
     const int sub = lane >> 3, col = lane & 7;     // rotated part and fp8: 4 tokens x 8 lanes
     auto token_at = [&](int slot, int j) { return m->token[slot][w * kKeysPerWarp + j]; };
     auto page_of = [&](int t) { return p.cache + (long long)(t >> 6) * p.page_stride; };
 
-    // fp8: tokens 4i + sub of the tile, and the codes of its first three parts,
-    // already in registers when the buffer falls free (the fourth part's
-    // follow into the first one's place)
-    uint4 codes[kParts - 1][4];
-    int tok[4];
+    // fp8: tokens 4i + sub of the tile, and the codes of its first two parts,
+    // already in registers when the buffer falls free (the other two parts'
+    // follow into their place)
+    constexpr int kSteps = kKeysPerWarp / 4;
+    uint4 codes[2][kSteps];
+    int tok[kSteps];
     auto code_row = [&](int t) {
       return (t >= 0 ? page_of(t) + (t & 63) * kLatent : reinterpret_cast<const uint8_t*>(g_zeros)) + col * 16;
     };
+    int4 tile = make_int4(0, 0, kEnd, 0);          // as the lookup warps found it
     auto fetch = [&](int it) {
       const int slot = it % kRing;
       wait(&m->look_full[slot], (it / kRing) & 1);
+      tile = m->tile[slot];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kSteps; ++i) {
         tok[i] = wait.ok ? token_at(slot, 4 * i + sub) : -1;
         const uint8_t* row = code_row(tok[i]);
 #pragma unroll
-        for (int part = 0; part < kParts - 1; ++part) codes[part][i] = ld_stream(row + part * 128);
+        for (int part = 0; part < 2; ++part) codes[part][i] = ld_stream(row + part * 128);
       }
     };
-    if (kFp8 && walk.left > 0) fetch(0);
+    bool more = m->end > m->begin;
+    if (kFp8 && more) fetch(0);
 
-    for (int it = 0; walk.left > 0; ++it) {
+    // a wait that ran out ends the loop
+    for (int it = 0; more && wait.ok; ++it) {
 #ifdef DSA_TEST_SKIP_FIRST_TILE
       // test builds only: never deliver the first tile, so that the waits for
       // it run out
@@ -569,39 +564,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
 #else
       constexpr bool deliver = true;
 #endif
-      const bool mine_used = w * kKeysPerWarp < walk.tokens();  // else no product reads these rows
       const int slot = it % kRing;
+      if (!kFp8) {
+        wait(&m->look_full[slot], (it / kRing) & 1);
+        tile = m->tile[slot];
+      }
+      // no product reads further than the tokens' last 16 rows
+      const bool mine_used = (w * kKeysPerWarp & ~15) < tile.y;
+      more = !(tile.z & kEnd);
       const uint32_t prev = (it - 1) & 1;
-      if (walk.first) {
+      if (tile.z & kFirst) {
         // the row's queries; their place is free once the last scores are done
         if (it > 0) wait(&m->sfull, prev);
         if (wait.ok && !kFp8) {
 #pragma unroll 2
-          for (int h = w * 8; h < w * 8 + 8; ++h) {
+          for (int h = w * kHeadsPerWarp; h < (w + 1) * kHeadsPerWarp; ++h) {
             const uint32_t n = h < heads ? 16u : 0u;
             const long long hh = h < heads ? head0 + h : head0;
-            const uint16_t* ql = p.ql + walk.row * p.ql_row + hh * p.ql_head + lane * 8;
+            const uint16_t* ql = p.ql + tile.x * p.ql_row + hh * p.ql_head + lane * 8;
             const uint32_t dst = sbase + kOffQ + sub * kQBlockBytes + h * 128 + ((col ^ (h & 7)) << 4);
             cp_async16(dst, ql, n);
             cp_async16(dst + 4 * kQBlockBytes, ql + 256, n);
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int h = w * 8 + i * 4 + sub;
+          {
+            const int h = w * kHeadsPerWarp + sub;
             const long long hh = h < heads ? head0 + h : head0;
             cp_async16(sbase + kOffQ + kRopeBlock * kQBlockBytes + h * 128 + ((col ^ (h & 7)) << 4),
-                       p.qr + walk.row * p.qr_row + hh * p.qr_head + col * 8, h < heads ? 16u : 0u);
+                       p.qr + tile.x * p.qr_row + hh * p.qr_head + col * 8, h < heads ? 16u : 0u);
           }
         } else if (wait.ok) {
 #pragma unroll 1
-          for (int h = w * 8; h < w * 8 + 8; ++h) {
+          for (int h = w * kHeadsPerWarp; h < (w + 1) * kHeadsPerWarp; ++h) {
             uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a, r = a;
             if (h < heads) {
-              const uint4* ql = reinterpret_cast<const uint4*>(p.ql + walk.row * p.ql_row + (head0 + h) * p.ql_head);
+              const uint4* ql = reinterpret_cast<const uint4*>(p.ql + tile.x * p.ql_row + (head0 + h) * p.ql_head);
               a = __ldg(ql + lane);
               b = __ldg(ql + 32 + lane);
               if (lane < 8)
-                r = __ldg(reinterpret_cast<const uint4*>(p.qr + walk.row * p.qr_row + (head0 + h) * p.qr_head) + lane);
+                r = __ldg(reinterpret_cast<const uint4*>(p.qr + tile.x * p.qr_row + (head0 + h) * p.qr_head) + lane);
             }
             float x[8], y[8];
             unpack8(a, x);
@@ -633,24 +633,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
               }
               st_shared_v4(dst + kRopeBlock * kQBlockBytes, make_uint4(o[0], o[1], o[2], o[3]));
             }
-            if (lane == 0) m->mul[walk.piece & 1][h] = p.scale_log2 * __uint_as_float((uint32_t)(127 - n) << 23);
+            if (lane == 0) m->mul[tile.w & 1][h] = p.scale_log2 * __uint_as_float((uint32_t)(127 - n) << 23);
           }
         }
       }
       if (!kFp8) {
         // every address before the first part falls free
-        wait(&m->look_full[slot], (it / kRing) & 1);
-        const uint8_t* src[8];
-        const uint8_t* rsrc[4];
+        const uint8_t* src[kKeysPerWarp / 2];
+        const uint8_t* rsrc[kSteps];
         uint32_t valid = 0, rvalid = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kKeysPerWarp / 2; ++i) {
           const int t = wait.ok ? token_at(slot, 2 * i + (lane >> 4)) : -1;
           valid |= (t >= 0 ? 1u : 0u) << i;
           src[i] = page_of(max(t, 0)) + (max(t, 0) & 63) * kTokenBytesBf16 + (lane & 15) * 16;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
           const int t = wait.ok ? token_at(slot, 4 * i + sub) : -1;
           rvalid |= (t >= 0 ? 1u : 0u) << i;
           rsrc[i] = page_of(max(t, 0)) + (max(t, 0) & 63) * kTokenBytesBf16 + kLatent * 2 + col * 16;
@@ -663,7 +662,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           if (it > 0) wait(&m->empty[part], prev);
           if (wait.ok && mine_used) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < kKeysPerWarp / 2; ++i)
               cp_async16(dst + part * kPartBytes + i * 256 + ((col ^ ((2 * i + (lane >> 4)) & 7)) << 4),
                          src[i] + part * 256, (valid >> i) & 1 ? 16u : 0u);
           }
@@ -671,7 +670,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         }
         if (wait.ok && mine_used) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < kSteps; ++i)
             cp_async16(sbase + kOffP + (w * kKeysPerWarp + 4 * i + sub) * 128 + ((col ^ ((4 * i + sub) & 7)) << 4),
                        rsrc[i], (rvalid >> i) & 1 ? 16u : 0u);
         }
@@ -686,54 +685,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         if (wait.ok && deliver) warp_arrive(&m->full[3], lane);
         cp_async_wait<0>();
         if (wait.ok && deliver) warp_arrive(&m->full[kParts], lane);
-        walk.step(p);
       } else {
-        uint2 ratio[4];
+        uint2 ratio[kSteps];
         wait(&m->scale_full[slot], (it / kRing) & 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ratio[i] = m->ratio[slot][w * kKeysPerWarp + 4 * i + sub];
+        for (int i = 0; i < kSteps; ++i) ratio[i] = m->ratio[slot][w * kKeysPerWarp + 4 * i + sub];
         __syncwarp();
         if (lane == 0) mbar_arrive(&m->look_empty[slot]);
         // lanes 4-7 of eight take their halves in the other order: no two
         // lanes of a store meet in a bank
         const int flip = col >> 2, c = (col & 3) * 2;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int part = 0; part < kParts; ++part) {
-          if (it > 0) wait(&m->empty[part], prev);
-          if (wait.ok && mine_used) {
+          for (int odd = 0; odd < 2; ++odd) {
+            const int part = 2 * half + odd;
+            if (it > 0) wait(&m->empty[part], prev);
+            if (wait.ok && mine_used) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t two = part < 2 ? ratio[i].x : ratio[i].y;
-              const uint32_t f = __byte_perm(two, two, part & 1 ? 0x3232 : 0x1010);
-              const uint4 c4 = codes[part % (kParts - 1)][i];
-              const uint4 a = widen8(flip ? c4.z : c4.x, flip ? c4.w : c4.y, f);
-              const uint4 b = widen8(flip ? c4.x : c4.z, flip ? c4.y : c4.w, f);
-              const int r = w * kKeysPerWarp + 4 * i + sub;
-              const uint32_t row = sbase + part * kPartBytes + flip * kBlockBytes + r * 128;
-              st_shared_v4(row + (((c + flip) ^ (r & 7)) << 4), a);
-              st_shared_v4(row + (((c + 1 - flip) ^ (r & 7)) << 4), b);
+              for (int i = 0; i < kSteps; ++i) {
+                const uint32_t two = half ? ratio[i].y : ratio[i].x;
+                const uint32_t f = __byte_perm(two, two, odd ? 0x3232 : 0x1010);
+                const uint4 c4 = codes[odd][i];
+                const uint4 a = widen8(flip ? c4.z : c4.x, flip ? c4.w : c4.y, f);
+                const uint4 b = widen8(flip ? c4.x : c4.z, flip ? c4.y : c4.w, f);
+                const int r = w * kKeysPerWarp + 4 * i + sub;
+                const uint32_t row = sbase + part * kPartBytes + flip * kBlockBytes + r * 128;
+                st_shared_v4(row + (((c + flip) ^ (r & 7)) << 4), a);
+                st_shared_v4(row + (((c + 1 - flip) ^ (r & 7)) << 4), b);
+              }
             }
-          }
-          if (part == 0) {
+            if (half == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) codes[0][i] = ld_stream(code_row(tok[i]) + (kParts - 1) * 128);
-          }
-          if (part == kParts - 1 && wait.ok && mine_used) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = max(tok[i], 0);
-              cp_async16(sbase + kOffP + (w * kKeysPerWarp + 4 * i + sub) * 128 + ((col ^ ((4 * i + sub) & 7)) << 4),
-                         page_of(t) + kRopeOffsetFp8 + (t & 63) * (kRope * 2) + col * 16, tok[i] < 0 ? 0u : 16u);
+              for (int i = 0; i < kSteps; ++i) codes[odd][i] = ld_stream(code_row(tok[i]) + (odd + 2) * 128);
             }
+            if (wait.ok && deliver) warp_arrive(&m->full[part], lane);
           }
-          if (wait.ok && deliver) warp_arrive(&m->full[part], lane);
+        }
+        if (wait.ok && mine_used) {
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const int t = max(tok[i], 0);
+            cp_async16(sbase + kOffP + (w * kKeysPerWarp + 4 * i + sub) * 128 + ((col ^ ((4 * i + sub) & 7)) << 4),
+                       page_of(t) + kRopeOffsetFp8 + (t & 63) * (kRope * 2) + col * 16, tok[i] < 0 ? 0u : 16u);
+          }
         }
         cp_async_wait_all();
         if (wait.ok && deliver) warp_arrive(&m->full[kParts], lane);
-        walk.step(p);
-        if (walk.left > 0) fetch(it + 1);
+        if (more) fetch(it + 1);
       }
     }
+    cp_async_wait_all();
   } else if (warp >= kLookWarp0) {
     // ---- token lookup ----------------------------------------------------------
     fewer_registers<kRegsMisc>();
@@ -742,7 +744,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     for (int it = 0; walk.left > 0; ++it) {
       if (it % kLookWarps == slot) {
         const int n = walk.tokens();
-        uint32_t flags = (walk.first ? kFirst : 0) | (walk.last() ? kLast : 0) | (walk.left == walk.count() ? kEnd : 0);
+        const int flags = (walk.first ? kFirst : 0) | (walk.last() ? kLast : 0) | (walk.left == walk.count() ? kEnd : 0);
         int tok[4];
         bool bad = false;
 #pragma unroll
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           }
         }
         if (wait.ok && lane == 0) {
-          m->flags[slot] = flags | (any_bad ? kBad : 0);
+          m->tile[slot] = make_int4(walk.row, n, flags | (any_bad ? kBad : 0), walk.piece);
           if (walk.first) {
             const bool begins = walk.u == 0, whole = begins && walk.left >= walk.units();
             m->piece[walk.piece & 7] = make_int4(walk.row, (begins ? kBegins : 0) | (whole ? kWhole : 0), 0, 0);
@@ -856,22 +858,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     if (elect_one()) {
       Waiter<false> wait{p.status, true};
       for (int it = 0; walk.left > 0; ++it) {
+        // eight MMAs to a step of these loops: all 68 in a row push the other
+        // roles out of the instruction cache, four leave the tensor pipe idle
         uint64_t a_d = smem_desc_sw128(sbase, 1024), b_d = smem_desc_sw128(sbase + kOffQ, 1024);
 #pragma unroll 1
-        for (int b = 0; b < 9; ++b) {
-          if (b % 2 == 0) {
-            wait(&m->full[b / 2], it & 1);
-            tc_fence_after();
-          }
-          const bool own = kFp8 && b == kRopeBlock;  // an accumulator of its own
+        for (int part = 0; part < kParts; ++part) {
+          wait(&m->full[part], it & 1);
+          tc_fence_after();
           if (wait.ok)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16(tmem + (own ? kTmemR : kTmemS), a_d + (k * 32 >> 4), b_d + (k * 32 >> 4),
-                      own ? kIdescRope : idesc_s(KV), k > 0 || (b > 0 && !own));
-          a_d += kBlockBytes >> 4;
-          b_d += kQBlockBytes >> 4;
+            for (int k = 0; k < 8; ++k)
+              mma_f16(tmem + kTmemS, a_d + (((k / 4) * kBlockBytes + (k % 4) * 32) >> 4),
+                      b_d + (((k / 4) * kQBlockBytes + (k % 4) * 32) >> 4), idesc_s(KV), k > 0 || part > 0);
+          a_d += kPartBytes >> 4;
+          b_d += 2 * kQBlockBytes >> 4;
         }
+        wait(&m->full[kParts], it & 1);
+        tc_fence_after();
+        if (wait.ok)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16(tmem + (kFp8 ? kTmemR : kTmemS), a_d + (k * 32 >> 4), b_d + (k * 32 >> 4),
+                    kFp8 ? kIdescRope : idesc_s(KV), !kFp8 || k > 0);
         if (wait.ok) mma_commit(&m->sfull);
         const int steps = (walk.tokens() + 15) / 16;
         const uint32_t keep = walk.first ? 0u : 1u;
@@ -883,12 +891,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           b_d = smem_desc_mn_sw128(sbase + kOffP, kBlockBytes, 1024);
 #pragma unroll 1
           for (int part = 0; part < kParts; ++part) {
-#pragma unroll 1
-            for (int k = 0; k < steps; ++k)
-              mma_f16(tmem + part * kAttnHeads, a_d + k * (2048 >> 4), b_d + k * (2048 >> 4), idesc_o(KV),
-                      k > 0 ? 1u : keep);
-            a_d += kPartBytes >> 4;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              if (k < steps)
+                mma_f16(tmem + part * kAttnHeads, a_d + (k * 2048 >> 4), b_d + (k * 2048 >> 4), idesc_o(KV),
+                        k > 0 ? 1u : keep);
             mma_commit(&m->empty[part]);
+            a_d += kPartBytes >> 4;
           }
         }
         walk.step(p);
@@ -919,7 +928,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       // four warps together: they meet at barriers
       if (bar_any(bar_half, 128, !wait.ok)) break;
       const bool valid = (*reinterpret_cast<volatile uint32_t*>(&m->mask[slot][quarter]) >> lane) & 1;
-      const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&m->flags[slot]);
+      const int flags = m->tile[slot].z;
       more = !(flags & kEnd);
       if (flags & kFirst) {
 #pragma unroll
@@ -996,7 +1005,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         }
         bar_sync(bar_half, 128);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) e[j] -= m->fac[hbase + j];
+        for (int j = 0; j < 32; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&m->fac[hbase + j]);
+          e[j] -= f.x, e[j + 1] -= f.y, e[j + 2] -= f.z, e[j + 3] -= f.w;
+        }
         if (!(flags & kFirst)) {
           // the scores' commit covers the last value product: O^T is at rest
 #pragma unroll
@@ -1066,48 +1078,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         }
         bar_sync(bar_half, 128);
         tc_fence_after();
+        // eight heads of a part at a time.  A warp's instructions come one in
+        // about eight cycles here, so the loop is short rather than wide: bf16
+        // pairs change lanes as one word, and pointers only move on
+        const int odd = lane & 1, mine = heads - hbase;   // this half's heads
+        uint16_t* row = p.out + what.x * p.out_row + (long long)(head0 + hbase + odd) * p.out_head + (key & ~1);
+        const uint32_t pick = odd ? 0x3276 : 0x5410;
 #pragma unroll 1
         for (int part = 0; part < kParts; ++part) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(my_tmem + part * kAttnHeads, o);
-          tmem_ld_wait32(o);
-          const int dim = part * 128 + key;
-          if (part == kParts - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (wait.ok && lane == 0) mbar_arrive(&m->ofree);
-          }
-          if (whole) {
-            // two heads of a lane pair: each lane writes two values of one head
-            uint16_t* dst =
-                p.out + what.x * p.out_row + (long long)(head0 + hbase + (lane & 1)) * p.out_head + (dim & ~1);
+          uint16_t* dst = row + part * 128;
+          float* sum_at = part_at + hbase * kLatent + part * 128 + key;
+#pragma unroll 1
+          for (int h0 = 0; h0 < 32; h0 += 8) {
+            uint32_t o[8];
+            tmem_ld_32x32b_x8(my_tmem + part * kAttnHeads + h0, o);
+            tmem_ld_wait8(o);
+            const float4 fa = *reinterpret_cast<const float4*>(&m->fac[hbase + h0]);
+            const float4 fb = *reinterpret_cast<const float4*>(&m->fac[hbase + h0 + 4]);
+            const float v[8] = {__uint_as_float(o[0]) * fa.x, __uint_as_float(o[1]) * fa.y,
+                                __uint_as_float(o[2]) * fa.z, __uint_as_float(o[3]) * fa.w,
+                                __uint_as_float(o[4]) * fb.x, __uint_as_float(o[5]) * fb.y,
+                                __uint_as_float(o[6]) * fb.z, __uint_as_float(o[7]) * fb.w};
+            if (whole) {
+              // two heads of a lane pair: each lane writes two values of one head
 #pragma unroll
-            for (int j4 = 0; j4 < 32; j4 += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&m->fac[hbase + j4]);
-              const float v[4] = {__uint_as_float(o[j4]) * f.x, __uint_as_float(o[j4 + 1]) * f.y,
-                                  __uint_as_float(o[j4 + 2]) * f.z, __uint_as_float(o[j4 + 3]) * f.w};
-#pragma unroll
-              for (int u = 0; u < 4; u += 2) {
-                const float mine = lane & 1 ? v[u + 1] : v[u];
-                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? v[u] : v[u + 1], 1);
-                const __nv_bfloat162 r = __floats2bfloat162_rn(lane & 1 ? other : mine, lane & 1 ? mine : other);
-                if (hbase + j4 + u + (lane & 1) < heads) *reinterpret_cast<__nv_bfloat162*>(dst) = r;
+              for (int j = 0; j < 8; j += 2) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(v[j], v[j + 1]);
+                const uint32_t a = *reinterpret_cast<const uint32_t*>(&two);
+                const uint32_t c = __byte_perm(a, __shfl_xor_sync(0xffffffffu, a, 1), pick);
+                if (h0 + j + odd < mine) *reinterpret_cast<uint32_t*>(dst) = c;
                 dst += 2 * p.out_head;
               }
-            }
-          } else {
-            float* dst = part_at + hbase * kLatent + dim;
+            } else {
 #pragma unroll
-            for (int j4 = 0; j4 < 32; j4 += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&m->fac[hbase + j4]);
-              const float v[4] = {__uint_as_float(o[j4]) * f.x, __uint_as_float(o[j4 + 1]) * f.y,
-                                  __uint_as_float(o[j4 + 2]) * f.z, __uint_as_float(o[j4 + 3]) * f.w};
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (hbase + j4 + u < heads) dst[(j4 + u) * kLatent] = v[u];
+              for (int j = 0; j < 8; ++j)
+                if (h0 + j < mine) sum_at[j * kLatent] = v[j];
+              sum_at += 8 * kLatent;
             }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (wait.ok && lane == 0) mbar_arrive(&m->ofree);
         bar_sync(bar_half, 128);                          // fac and red are free again
         ++piece;
       }
