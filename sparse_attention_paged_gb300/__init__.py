@@ -241,64 +241,18 @@ def dsa_latent_attention_workspace() -> int:
     return int(_native.load().dsa_latent_attention_workspace())
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+_calls = None
 
 
-def _ints(x, name, shape=None):
-    import torch
-    _need(x.dtype is torch.int32 and x.is_contiguous(), f"{name}: contiguous int32 expected")
-    _need(shape is None or tuple(x.shape) == shape, f"{name}: shape {shape} expected")
-    return x
+def _tensor_calls():
+    global _calls
+    if _calls is None:
+        _calls = _native.load_calls()
+    return _calls
 
 
-def _floats(x, name, shape):
-    import torch
-    if x is not None:
-        _need(x.dtype is torch.float32 and x.is_contiguous() and tuple(x.shape) == shape,
-              f"{name}: contiguous float32 of shape {shape} expected")
-    return x
-
-
-def _pool(cache, kv_dtype):
-    """(page stride in bytes, pages) of a pool: uint8 [pages, page bytes], rows contiguous."""
-    import torch
-    _need(cache.dtype is torch.uint8 and cache.dim() == 2 and cache.stride(1) == 1,
-          "cache: uint8 [pages, page bytes] expected")
-    _need(kv_dtype in LATENT_PAGE_BYTES, "kv_dtype: KV_FP8_E4M3 or KV_BF16")
-    _need(cache.shape[1] >= LATENT_PAGE_BYTES[kv_dtype], "cache: rows shorter than a page")
-    return (cache.stride(0) if cache.shape[0] > 1 else cache.shape[1]), cache.shape[0]
-
-
-def _table_rows(block_table, rows, name="block_table"):
-    """(stride, W) of an int32 [rows, W] table, or of one shared row [W] or [1, W]."""
-    import torch
-    _need(block_table.dtype is torch.int32 and block_table.dim() in (1, 2)
-          and block_table.stride(-1) == 1, f"{name}: int32 [rows, W] expected")
-    W = block_table.shape[-1]
-    if block_table.dim() == 1 or block_table.shape[0] == 1:
-        return 0, W
-    _need(block_table.shape[0] == rows, f"{name}: one row, or one per request")
-    return block_table.stride(0), W
-
-
-def _check(status):
-    if status != 0:
-        raise DsaError(status)
-
-
-_DTYPES = None
-
-
-def _dtype(t):
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
-    code = _DTYPES.get(t.dtype)
-    _need(code is not None, f"{t.dtype}: bfloat16, float16 or float32 expected")
-    return code
+def _stream_address(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def rope_table(max_pos, rot_dims, base=10000.0, device="cuda"):
@@ -319,39 +273,17 @@ def qk_norm_rope(q, k, positions=None, table=None, *, rot_dims=None, rot_offset=
     as ``rope_table`` makes it.  Outputs are allocated unless given (in place: pass q and k).
     Returns (q_out, k_out).  Raises DsaError on a host-side error.
     """
-    import torch
-    T, Hq, D = q.shape
-    dtype = _dtype(q)
-    _need(q.stride(2) == 1 or D == 1, "q: the last dimension must be contiguous")
+    if rot_dims is not None and table is not None and rot_dims != table.shape[1]:
+        raise ValueError("rot_dims: the table's width")
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.stride(2) == 1,
-          "q_out: like q")
-    Hk, ks, kos = 0, (0, 0), (0, 0)
-    if k is not None:
-        _need(k.dim() == 3 and k.shape[0] == T and k.shape[2] == D and k.dtype == q.dtype
-              and k.stride(2) == 1, "k: [T, Hk, D] of q's type")
-        Hk = k.shape[1]
-        if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=k.dtype, device=k.device)
-        _need(k_out.shape == k.shape and k_out.dtype == k.dtype and k_out.stride(2) == 1,
-              "k_out: like k")
-        ks, kos = k.stride(), k_out.stride()
-    max_pos = rot = 0
-    if positions is not None:
-        _ints(positions, "positions", (T,))
-        _need(table is not None, "positions need a table")
-        max_pos, rot = table.shape
-        _need(rot_dims is None or rot_dims == rot, "rot_dims: the table's width")
-        _floats(table, "table", (max_pos, rot))
-    for name, x in (("q_weight", q_weight), ("k_weight", k_weight), ("q_bias", q_bias),
-                    ("k_bias", k_bias)):
-        _floats(x, name, (D,))
-    qs, qos = q.stride(), q_out.stride()
-    _check(dsa_qk_norm_rope(q, qs[0], qs[1], Hq, k, ks[0], ks[1], Hk, T, D, dtype, norm, q_weight,
-                            k_weight, q_bias, k_bias, eps, positions, table, max_pos, rot,
-                            rot_offset, interleaved, q_out, qos[0], qos[1], k_out, kos[0], kos[1],
-                            dev_status, stream))
+        q_out = q.new_empty(q.shape)
+    if k_out is None and k is not None:
+        k_out = k.new_empty(k.shape)
+    status = (_calls or _tensor_calls()).qk_norm_rope(
+        q, k, positions, table, rot_offset, interleaved, norm, q_weight, k_weight, q_bias, k_bias,
+        eps, q_out, k_out, dev_status, _stream_address(stream))
+    if status:
+        raise DsaError(status)
     return q_out, k_out
 
 
@@ -362,24 +294,11 @@ def latent_store(latent, rope, slot_mapping, cache, kv_dtype, *, norm_weight=Non
     Optionally normalises the latent and rotates the other part on the way.  ``cache``: uint8
     [pages, LATENT_PAGE_BYTES[kv_dtype]].  Raises DsaError on a host-side error.
     """
-    import torch
-    n = latent.shape[0]
-    _need(latent.dtype is torch.bfloat16 and tuple(latent.shape) == (n, LATENT)
-          and latent.stride(1) == 1, "latent: bfloat16 [n, 512], rows contiguous")
-    _need(rope.dtype is torch.bfloat16 and tuple(rope.shape) == (n, ROPE) and rope.stride(1) == 1,
-          "rope: bfloat16 [n, 64], rows contiguous")
-    _ints(slot_mapping, "slot_mapping", (n,))
-    _floats(norm_weight, "norm_weight", (LATENT,))
-    max_pos = 0
-    if positions is not None:
-        _ints(positions, "positions", (n,))
-        _need(rope_table is not None, "positions need a rope_table")
-        max_pos = rope_table.shape[0]
-        _floats(rope_table, "rope_table", (max_pos, ROPE))
-    stride, pages = _pool(cache, kv_dtype)
-    _check(dsa_latent_store(latent, latent.stride(0), rope, rope.stride(0), n, LATENT, ROPE,
-                            norm_weight, eps, positions, rope_table, max_pos, interleaved,
-                            slot_mapping, cache, stride, pages, kv_dtype, PAGE, dev_status, stream))
+    status = (_calls or _tensor_calls()).latent_store(
+        latent, rope, slot_mapping, cache, kv_dtype, norm_weight, eps, positions, rope_table,
+        interleaved, dev_status, _stream_address(stream))
+    if status:
+        raise DsaError(status)
     return cache
 
 
@@ -390,19 +309,13 @@ def latent_load(cache, kv_dtype, block_table, cu_rows, n, *, starts=None, out=No
     ``cu_rows`` int32 [requests + 1] on the device: request r's rows of the output.  Raises
     DsaError on a host-side error.
     """
-    import torch
-    n_req = cu_rows.shape[0] - 1
-    _ints(cu_rows, "cu_rows")
-    if starts is not None:
-        _ints(starts, "starts", (n_req,))
     if out is None:
+        import torch
         out = torch.empty((n, LATENT + ROPE), dtype=torch.bfloat16, device=cache.device)
-    _need(out.dtype is torch.bfloat16 and tuple(out.shape) == (n, LATENT + ROPE)
-          and out.stride(1) == 1, "out: bfloat16 [n, 576], rows contiguous")
-    stride, pages = _pool(cache, kv_dtype)
-    bt_stride, W = _table_rows(block_table, n_req)
-    _check(dsa_latent_load(cache, stride, pages, kv_dtype, PAGE, block_table, bt_stride, W, starts,
-                           cu_rows, n_req, n, LATENT, ROPE, out, out.stride(0), dev_status, stream))
+    status = (_calls or _tensor_calls()).latent_load(
+        cache, kv_dtype, block_table, cu_rows, n, starts, out, dev_status, _stream_address(stream))
+    if status:
+        raise DsaError(status)
     return out
 
 
@@ -414,34 +327,15 @@ def latent_attention(q_latent, q_rope, cache, kv_dtype, block_table, seqlens, sc
     as the top-k calls write them).  Returns out, bf16 [rows, H, 512]; ``lse`` (fp32 [rows, H])
     is written when given.  Raises DsaError on a host-side error.
     """
-    import torch
-    rows, H, _ = q_latent.shape
-    _need(q_latent.dtype is torch.bfloat16 and q_latent.shape[2] == LATENT
-          and q_latent.stride(2) == 1, "q_latent: bfloat16 [rows, H, 512]")
-    _need(q_rope.dtype is torch.bfloat16 and tuple(q_rope.shape) == (rows, H, ROPE)
-          and q_rope.stride(2) == 1, "q_rope: bfloat16 [rows, H, 64]")
-    _ints(seqlens, "seqlens", (rows,))
-    idx_stride = k = 0
-    if idx is not None:
-        _need(idx.dtype is torch.int32 and idx.dim() == 2 and idx.shape[0] == rows
-              and idx.stride(1) == 1, "idx: int32 [rows, k]")
-        k = idx.shape[1]
-        idx_stride = idx.stride(0) if rows > 1 else k
     if out is None:
-        out = torch.empty((rows, H, LATENT), dtype=torch.bfloat16, device=q_latent.device)
-    _need(out.dtype is torch.bfloat16 and tuple(out.shape) == (rows, H, LATENT)
-          and out.stride(2) == 1, "out: bfloat16 [rows, H, 512]")
-    _floats(lse, "lse", (rows, H))
+        out = q_latent.new_empty(q_latent.shape)
     if workspace is None:
-        workspace = torch.empty(dsa_latent_attention_workspace(), dtype=torch.float32,
+        import torch
+        workspace = torch.empty(max(dsa_latent_attention_workspace(), 0), dtype=torch.float32,
                                 device=q_latent.device)
-    _need(workspace.dtype is torch.float32 and workspace.is_contiguous(),
-          "workspace: contiguous float32")
-    stride, pages = _pool(cache, kv_dtype)
-    bt_stride, W = _table_rows(block_table, rows)
-    _check(dsa_latent_attention(q_latent, q_latent.stride(0), q_latent.stride(1), q_rope,
-                                q_rope.stride(0), q_rope.stride(1), rows, H, LATENT, ROPE, scale,
-                                cache, stride, pages, kv_dtype, PAGE, block_table, bt_stride, W,
-                                seqlens, idx, idx_stride, k, out, out.stride(0), out.stride(1),
-                                lse, workspace, workspace.numel(), dev_status, stream))
+    status = (_calls or _tensor_calls()).latent_attention(
+        q_latent, q_rope, cache, kv_dtype, block_table, seqlens, scale, idx, out, lse, workspace,
+        dev_status, _stream_address(stream))
+    if status:
+        raise DsaError(status)
     return out

@@ -18,6 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD, "libdsa_indexer.so")
+CALLS_PATH = os.path.join(BUILD, "_dsa_torch.so")      # the tensor-level calls (torch_calls.cpp)
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "nvcc")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -43,20 +45,21 @@ def _sources():
 
 def _deps():
     files = _sources()
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     return files
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu under csrc/ for sm_103a and link the shared library."""
+    """Compile every .cu under csrc/ for sm_103a and link the shared library; compile the
+    CPython module of the tensor-level calls against it."""
     if not force and not is_stale():
         return LIB_PATH
     os.makedirs(BUILD, exist_ok=True)
@@ -73,8 +76,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_compile_calls)
         results = list(ex.map(compile_one, srcs))
+        calls_obj = calls.result()
     for obj, log in results:
         objs.append(obj)
         if verbose and log:
@@ -85,7 +90,56 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_calls(calls_obj)
     return LIB_PATH
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_calls() -> str:
+    import sysconfig
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    include = [INCLUDE, base, os.path.join(base, "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"],
+               os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    obj = os.path.join(BUILD, "torch_calls.o")
+    _run([CXX, "-O2", "-std=c++17", "-fPIC",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[f"-I{d}" for d in include], "-c", os.path.join(CSRC, "torch_calls.cpp"), "-o", obj],
+         "compiling torch_calls.cpp")
+    return obj
+
+
+def _link_calls(obj):
+    import torch
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    _run([CXX, "-shared", obj, "-o", tmp, "-L" + BUILD, "-l:libdsa_indexer.so", "-Wl,-rpath,$ORIGIN",
+          "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+          "-lc10", "-lc10_cuda"], "linking the tensor-level calls")
+    os.replace(tmp, CALLS_PATH)
+
+
+_calls = None
+
+
+def load_calls():
+    """The CPython module of the tensor-level calls (building it first if it is missing or stale)."""
+    global _calls
+    if _calls is None:
+        load()
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (its libraries are the module's)
+        loader = importlib.machinery.ExtensionFileLoader("_dsa_torch", CALLS_PATH)
+        spec = importlib.util.spec_from_loader("_dsa_torch", loader)
+        _calls = importlib.util.module_from_spec(spec)
+        loader.exec_module(_calls)
+    return _calls
 
 
 def load() -> ctypes.CDLL:
