@@ -30,6 +30,39 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 8;  // values a lane holds
 
+// Two floats in one 64-bit register pair: half the instructions of the sums
+// and products, which bound this kernel once its loads are wide.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 pack(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  float x, y;
+  unpair(a, x, y);
+  return x + y;
+}
+
 // Four values as they lie in memory, and as floats.
 template <typename T>
 struct Raw4 {
@@ -45,35 +78,41 @@ struct Raw4<float> {
   __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
 };
 
-__device__ __forceinline__ void unpack(const Raw4<__nv_bfloat16>& x, float* v) {
-  v[0] = __uint_as_float(x.r.x << 16), v[1] = __uint_as_float(x.r.x & 0xffff0000u);
-  v[2] = __uint_as_float(x.r.y << 16), v[3] = __uint_as_float(x.r.y & 0xffff0000u);
+__device__ __forceinline__ void unpack(const Raw4<__nv_bfloat16>& x, F2* v) {
+  v[0] = pack(__uint_as_float(x.r.x << 16), __uint_as_float(x.r.x & 0xffff0000u));
+  v[1] = pack(__uint_as_float(x.r.y << 16), __uint_as_float(x.r.y & 0xffff0000u));
 }
 
-__device__ __forceinline__ void unpack(const Raw4<__half>& x, float* v) {
+__device__ __forceinline__ void unpack(const Raw4<__half>& x, F2* v) {
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x.r.x));
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&x.r.y));
-  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+  v[0] = pack(a.x, a.y), v[1] = pack(b.x, b.y);
 }
 
-__device__ __forceinline__ void unpack(const Raw4<float>& x, float* v) {
-  v[0] = x.r.x, v[1] = x.r.y, v[2] = x.r.z, v[3] = x.r.w;
+__device__ __forceinline__ void unpack(const Raw4<float>& x, F2* v) {
+  v[0] = pack(x.r.x, x.r.y), v[1] = pack(x.r.z, x.r.w);
 }
 
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const F2* v) {
+  float a, b, c, d;
+  unpair(v[0], a, b), unpair(v[1], c, d);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
   *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-__device__ __forceinline__ void store4(__half* p, const float* v) {
-  const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+__device__ __forceinline__ void store4(__half* p, const F2* v) {
+  float a, b, c, d;
+  unpair(v[0], a, b), unpair(v[1], c, d);
+  const __half2 lo = __floats2half2_rn(a, b), hi = __floats2half2_rn(c, d);
   *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-__device__ __forceinline__ void store4(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void store4(float* p, const F2* v) {
+  float a, b, c, d;
+  unpair(v[0], a, b), unpair(v[1], c, d);
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
 
 // Four floats of a vector that every row shares; `wide`: 16-byte aligned.
@@ -96,10 +135,10 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// LANES: lanes per row (8 * LANES >= dim); HEADS: heads a group takes.  The
-// loads stay packed until their head's turn, so that three blocks fit an SM.
-template <typename T, int LANES, int HEADS, bool INTER>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) norm_rope_kernel(const NormRopeParams p) {
+// LANES: lanes per row (8 * LANES >= dim; FULL: equal); HEADS: heads a group
+// takes; INTER: interleaved pairs.  The loads stay packed until their head's turn, so that three blocks fit an SM.
+template <typename T, int LANES, int HEADS, bool INTER, bool FULL>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(const NormRopeParams p) {
   const long long unit = ((long long)blockIdx.x * kThreads + threadIdx.x) / LANES;
   const int c = threadIdx.x % LANES;
   const int units_q = (p.heads[0] + HEADS - 1) / HEADS;
@@ -157,47 +196,64 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) norm_rope_ke
   }
   if (bad && c == 0) raise_status(p.status, DSA_ERR_BAD_POSITION);
 
+  F2 w2[4], b2[4], cs2[4], sn2[4], ms2[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w2[i] = pack(w[2 * i], w[2 * i + 1]), b2[i] = pack(b[2 * i], b[2 * i + 1]);
+  // half layout: cosines and sines of two pairs; interleaved: of one, twice
+#pragma unroll
+  for (int i = 0; i < (INTER ? 4 : 2); ++i) {
+    cs2[i] = INTER ? pack(cs[i], cs[i]) : pack(cs[2 * i], cs[2 * i + 1]);
+    sn2[i] = INTER ? pack(-sn[i], sn[i]) : pack(sn[2 * i], sn[2 * i + 1]);
+    if (!INTER) ms2[i] = pack(-sn[2 * i], -sn[2 * i + 1]);
+  }
   const float inv_dim = 1.f / (float)p.dim;
+  const float poison = bad ? CUDART_NAN_F : 1.f;
   T* y = static_cast<T*>(p.y[side]) + token * p.yt[side] + j * p.yh[side];
 #pragma unroll
   for (int h = 0; h < HEADS; ++h) {
-    float v[8];
+    F2 v[4];
     unpack(raw[h][0], v);
-    unpack(raw[h][1], v + 4);
+    unpack(raw[h][1], v + 2);
     if (p.norm == DSA_NORM_LAYER) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i];
+      const float s = sum2(add2(add2(v[0], v[1]), add2(v[2], v[3])));
       const float mean = group_sum<LANES>(s) * inv_dim;
+      const F2 off = pack(-mean, -mean);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = mine ? v[i] - mean : 0.f;
+      for (int i = 0; i < 4; ++i) v[i] = FULL || mine ? add2(v[i], off) : pack(0.f, 0.f);
     }
     if (p.norm != DSA_NORM_NONE) {
-      float s = 0.f;
+      const F2 s = fma2(v[3], v[3], fma2(v[2], v[2], fma2(v[1], v[1], mul2(v[0], v[0]))));
+      const float r = rsqrtf(group_sum<LANES>(sum2(s)) * inv_dim + p.eps) * poison;
+      const F2 r2 = pack(r, r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
-      const float r = rsqrtf(group_sum<LANES>(s) * inv_dim + p.eps);
+      for (int i = 0; i < 4; ++i) v[i] = fma2(mul2(v[i], r2), w2[i], b2[i]);
+    } else if (bad) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i] * r, w[i], b[i]);
+      for (int i = 0; i < 4; ++i) v[i] = pack(poison, poison);
     }
     if (turned) {
+      if (INTER) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a0 = INTER ? v[2 * i] : v[i], a1 = INTER ? v[2 * i + 1] : v[4 + i];
-        v[INTER ? 2 * i : i] = a0 * cs[i] - a1 * sn[i];
-        v[INTER ? 2 * i + 1 : 4 + i] = a1 * cs[i] + a0 * sn[i];
+        for (int i = 0; i < 4; ++i) {
+          float a0, a1;
+          unpair(v[i], a0, a1);
+          v[i] = fma2(v[i], cs2[i], mul2(pack(a1, a0), sn2[i]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const F2 a0 = v[i], a1 = v[2 + i];
+          v[i] = fma2(a0, cs2[i], mul2(a1, ms2[i]));
+          v[2 + i] = fma2(a1, cs2[i], mul2(a0, sn2[i]));
+        }
       }
     }
-    if (bad) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = CUDART_NAN_F;
-    }
-    if (mine && h < heads) store4(y + lo, v), store4(y + hi, v + 4);
+    if (mine && h < heads) store4(y + lo, v), store4(y + hi, v + 2);
     y += p.yh[side];
   }
 }
 
-template <typename T, int LANES, int HEADS, bool INTER>
+template <typename T, int LANES, int HEADS, bool INTER, bool FULL>
 cudaError_t launch_t(const NormRopeParams& p, cudaStream_t stream) {
   const long long units = (long long)p.tokens * ((p.heads[0] + HEADS - 1) / HEADS +
                                                  (p.heads[1] + HEADS - 1) / HEADS);
@@ -210,14 +266,20 @@ cudaError_t launch_t(const NormRopeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, LANES, HEADS, INTER>, p);
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, LANES, HEADS, INTER, FULL>, p);
+}
+
+template <typename T, int LANES, bool INTER>
+cudaError_t launch_lanes(const NormRopeParams& p, cudaStream_t stream) {
+  if (p.dim == kChunk * LANES) return launch_t<T, LANES, 4, INTER, true>(p, stream);
+  return launch_t<T, LANES, 4, INTER, false>(p, stream);
 }
 
 template <typename T, bool INTER>
 cudaError_t launch_dim(const NormRopeParams& p, cudaStream_t stream) {
-  if (p.dim <= 64) return launch_t<T, 8, 4, INTER>(p, stream);
-  if (p.dim <= 128) return launch_t<T, 16, 4, INTER>(p, stream);
-  return launch_t<T, 32, 4, INTER>(p, stream);
+  if (p.dim <= 64) return launch_lanes<T, 8, INTER>(p, stream);
+  if (p.dim <= 128) return launch_lanes<T, 16, INTER>(p, stream);
+  return launch_lanes<T, 32, INTER>(p, stream);
 }
 
 template <typename T>
