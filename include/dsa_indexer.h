@@ -326,7 +326,8 @@ typedef enum { DSA_NORM_NONE = 0, DSA_NORM_RMS = 1, DSA_NORM_LAYER = 2 } dsa_nor
  * positions NULL: no rotation.  Hq or Hk may be 0 (that side's pointers are
  * not used).  8 <= D <= 256, a multiple of 8; rot_dims a multiple of 16
  * (interleaved: of 8), rot_offset of 8 (DSA_ERR_UNSUPPORTED).  Arrays and
- * rows 16-byte aligned, rope_table too (DSA_ERR_MISALIGNED).  A position
+ * rows 16-byte aligned, weights, biases and rope_table too
+ * (DSA_ERR_MISALIGNED).  A position
  * outside [0, max_pos) is a data error: that token's rows are NaN, status
  * DSA_ERR_BAD_POSITION.
  */

@@ -86,7 +86,7 @@ int dsa_qk_norm_rope(const void* q, long long q_token_stride, long long q_head_s
   if (Hk > 0 && (!aligned(k, 16) || !aligned(k_out, 16) || k_token_stride % unit ||
                  k_head_stride % unit || ko_token_stride % unit || ko_head_stride % unit))
     return DSA_ERR_MISALIGNED;
-  if (!aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(q_bias, 4) || !aligned(k_bias, 4))
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(q_bias, 16) || !aligned(k_bias, 16))
     return DSA_ERR_MISALIGNED;
   if (T == 0 || Hq + (long long)Hk == 0) return DSA_OK;
   // at most one unit of 32 lanes per head: the grid stays below 2^31 blocks

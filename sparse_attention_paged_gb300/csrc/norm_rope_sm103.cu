@@ -115,18 +115,11 @@ __device__ __forceinline__ void store4(float* p, const F2* v) {
   *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
 
-// Four floats of a vector that every row shares; `wide`: 16-byte aligned.
-__device__ __forceinline__ void load_shared4(const float* p, bool wide, float* v) {
-  if (wide) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __ldg(p + i);
+// Four floats of a vector that every row shares.
+__device__ __forceinline__ void load_shared4(const float* p, float* v) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
 }
-
-__device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -182,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_ke
     bad = pos < 0 || pos >= p.max_pos;
     if (turned && !bad) {
       const float* row = p.table + (long long)pos * p.rot + at / 2;
-      load_shared4(row, true, cs);
-      load_shared4(row + p.rot / 2, true, sn);
+      load_shared4(row, cs);
+      load_shared4(row + p.rot / 2, sn);
     }
   }
   float w[8], b[8];
@@ -191,8 +184,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_ke
   for (int i = 0; i < 8; ++i) w[i] = 1.f, b[i] = 0.f;
   if (mine && p.norm != DSA_NORM_NONE) {
     const float *pw = p.weight[side], *pb = p.bias[side];
-    if (pw) load_shared4(pw + lo, aligned16(pw), w), load_shared4(pw + hi, aligned16(pw), w + 4);
-    if (pb) load_shared4(pb + lo, aligned16(pb), b), load_shared4(pb + hi, aligned16(pb), b + 4);
+    if (pw) load_shared4(pw + lo, w), load_shared4(pw + hi, w + 4);
+    if (pb) load_shared4(pb + lo, b), load_shared4(pb + hi, b + 4);
   }
   if (bad && c == 0) raise_status(p.status, DSA_ERR_BAD_POSITION);
 
