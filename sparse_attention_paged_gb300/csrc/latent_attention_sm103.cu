@@ -108,6 +108,7 @@ struct Misc {
   uint64_t sfull;              // S^T is there
   uint64_t pfull;              // P is there
   uint64_t ofree;              // O^T has been read
+  uint64_t qfirst;             // the first row's queries are there
   uint64_t look_full[kRing], look_empty[kRing], scale_full[kRing];
   uint64_t done;
   uint32_t tmem;
@@ -396,6 +397,83 @@ __device__ __forceinline__ int* split_record(const LatentAttnParams& p) {
 // What a masked token's codes are read from.
 __device__ const uint4 g_zeros[kLatent / 16] = {};
 
+// Brings `count` heads' queries of a row to their place, head by head, UNROLL
+// heads' loads at a time.  bf16: as they are (cp.async; the caller waits for
+// them).  fp8: the latent part as fp16, both parts times a power of two that
+// brings the head's largest into [2^14, 2^15), and the factor that takes the
+// scores back into `mul`.  Heads past `heads` are zeros.
+template <int KV, int UNROLL>
+__device__ __forceinline__ void load_queries(const LatentAttnParams& p, int row, int head0, int heads, int first,
+                                             int count, uint32_t sbase, int lane, float* mul) {
+  const int sub = lane >> 3, col = lane & 7;
+  const uint16_t* ql = p.ql + row * p.ql_row + head0 * p.ql_head;
+  const uint16_t* qr = p.qr + row * p.qr_row + head0 * p.qr_head;
+  if constexpr (KV == DSA_KV_BF16) {
+#pragma unroll 2
+    for (int h = first; h < first + count; ++h) {
+      const uint32_t n = h < heads ? 16u : 0u;
+      const uint16_t* src = ql + (h < heads ? h : 0) * p.ql_head + lane * 8;
+      const uint32_t dst = sbase + kOffQ + sub * kQBlockBytes + h * 128 + ((col ^ (h & 7)) << 4);
+      cp_async16(dst, src, n);
+      cp_async16(dst + 4 * kQBlockBytes, src + 256, n);
+    }
+#pragma unroll 1
+    for (int h = first + sub; h < first + count; h += 4)
+      cp_async16(sbase + kOffQ + kRopeBlock * kQBlockBytes + h * 128 + ((col ^ (h & 7)) << 4),
+                 qr + (h < heads ? h : 0) * p.qr_head + col * 8, h < heads ? 16u : 0u);
+  } else {
+#pragma unroll 1
+    for (int h0 = first; h0 < first + count; h0 += UNROLL) {
+      uint4 a[UNROLL], b[UNROLL], r[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int h = h0 + u;
+        a[u] = b[u] = r[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < heads) {
+          const uint4* src = reinterpret_cast<const uint4*>(ql + h * p.ql_head) + lane;
+          a[u] = __ldg(src);
+          b[u] = __ldg(src + 32);
+          if (lane < 8) r[u] = __ldg(reinterpret_cast<const uint4*>(qr + h * p.qr_head) + lane);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int h = h0 + u;
+        float x[8], y[8];
+        unpack8(a[u], x);
+        unpack8(b[u], y);
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
+        top = warp_max(top);
+        const int n = top > 0.f ? min(max(127 + 14 - (int)(__float_as_uint(top) >> 23), -100), 100) : 0;
+        const float f = __uint_as_float((uint32_t)(n + 127) << 23);
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2 lo = __floats2half2_rn(x[2 * j] * f, x[2 * j + 1] * f);
+          const __half2 hi = __floats2half2_rn(y[2 * j] * f, y[2 * j + 1] * f);
+          o[j] = *reinterpret_cast<const uint32_t*>(&lo);
+          o[4 + j] = *reinterpret_cast<const uint32_t*>(&hi);
+        }
+        const uint32_t dst = sbase + kOffQ + h * 128 + ((col ^ (h & 7)) << 4);
+        st_shared_v4(dst + sub * kQBlockBytes, make_uint4(o[0], o[1], o[2], o[3]));
+        st_shared_v4(dst + (4 + sub) * kQBlockBytes, make_uint4(o[4], o[5], o[6], o[7]));
+        if (lane < 8) {
+          unpack8(r[u], x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
+            o[j] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          st_shared_v4(dst + kRopeBlock * kQBlockBytes, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        if (lane == 0) mul[h] = p.scale_log2 * __uint_as_float((uint32_t)(127 - n) << 23);
+      }
+    }
+  }
+}
+
 template <int KV>
 __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const LatentAttnParams p) {
   constexpr bool kFp8 = KV != DSA_KV_BF16;
@@ -415,6 +493,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     mbar_init(&m->sfull, 1);
     mbar_init(&m->pfull, kSoftmaxWarps);
     mbar_init(&m->ofree, kSoftmaxWarps);
+    mbar_init(&m->qfirst, kSoftmaxWarps);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&m->look_full[i], 1);
       mbar_init(&m->scale_full[i], 1);
@@ -437,33 +516,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
   // finds the row in which this CTA's slice begins
   TileWalk walk;
   {
-    const int per = (p.rows + kAttnThreads - 1) / kAttnThreads;
-    const int r0 = min(p.rows, tid * per), r1 = min(p.rows, r0 + per);
-    int mine = 0;
-    bool zero = false;
-    for (int r = r0; r < r1; ++r) {
-      const int t = row_units(p, r);
-      mine += t;
-      zero |= t == 0 && r % p.ctas == cta;
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) m->scan[warp] = incl;
-    const bool zeros = __syncthreads_or(zero);
-    int base = 0, total = 0;
-#pragma unroll 4
-    for (int w = 0; w < kAttnThreads / 32; ++w) {
-      const int v = m->scan[w];
-      if (w < warp) base += v;
-      total += v;
-    }
-    const int ctas = min(p.ctas, total);            // every slice has a unit
-    int begin = 0, end = 0;
-    if (cta < ctas) {
+    int begin = 0, end = 0, total = 0, ctas = 0, start_row = 0, start_unit = 0;
+    // the equal part of `total` units that this CTA takes
+    auto take = [&] {
+      ctas = min(p.ctas, total);                    // every slice has a unit
+      if (cta >= ctas) return;
       if (total < (1 << 22)) {                      // p.ctas < 512
         begin = (int)((unsigned)(cta * total) / (unsigned)ctas);
         end = (int)((unsigned)((cta + 1) * total) / (unsigned)ctas);
@@ -471,50 +528,98 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         begin = (int)((long long)cta * total / ctas);
         end = (int)((long long)(cta + 1) * total / ctas);
       }
-    }
-    int at = base + incl - mine;
-    if (end > begin && at <= begin && begin < at + mine) {
-      int r = r0;
-      for (;; ++r) {
-        const int t = row_units(p, r);
-        if (begin < at + t) break;
-        at += t;
+    };
+    // a row without a visible token: zeros (a length past the table: NaN), by
+    // threads `first`, `first` + `step`, ..
+    auto clear = [&](int row, int first, int step) {
+      const bool bad = __ldg(p.seqlens + row) > 0;
+      if (bad && first == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
+      const uint32_t v = bad ? 0x7fff7fffu : 0u;
+#pragma unroll 1
+      for (int j = first; j < heads * (kLatent / 8); j += step)
+        *reinterpret_cast<uint4*>(p.out + row * p.out_row + (long long)(head0 + j / (kLatent / 8)) * p.out_head +
+                                  (j % (kLatent / 8)) * 8) = make_uint4(v, v, v, v);
+      for (int h = first; p.lse && h < heads; h += step)
+        p.lse[(long long)row * p.H + head0 + h] = bad ? CUDART_NAN_F : -CUDART_INF_F;
+    };
+    if (p.rows <= 32) {
+      // few rows: every warp scans them for itself
+      const int mine = lane < p.rows ? row_units(p, lane) : 0;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
       }
-      m->start_row = r;
-      m->start_unit = begin - at;
+      total = __shfl_sync(0xffffffffu, incl, 31);
+      take();
+      const uint32_t here = __ballot_sync(0xffffffffu, end > begin && incl - mine <= begin && begin < incl);
+      start_row = here ? __ffs(here) - 1 : 0;
+      start_unit = begin - __shfl_sync(0xffffffffu, incl - mine, start_row);
+      uint32_t empty = __ballot_sync(0xffffffffu, lane < p.rows && mine == 0 && lane % p.ctas == cta);
+      for (; empty; empty &= empty - 1) clear(__ffs(empty) - 1, tid, kAttnThreads);
+      if (tid == 0) m->start_row = start_row, m->start_unit = start_unit;
+    } else {
+      // thread i owns a run of rows; an exclusive scan of the runs' unit counts
+      // finds the row in which this CTA's slice begins
+      const int per = (p.rows + kAttnThreads - 1) / kAttnThreads;
+      const int r0 = min(p.rows, tid * per), r1 = min(p.rows, r0 + per);
+      int mine = 0;
+      bool zero = false;
+      for (int r = r0; r < r1; ++r) {
+        const int t = row_units(p, r);
+        mine += t;
+        zero |= t == 0 && r % p.ctas == cta;
+      }
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) m->scan[warp] = incl;
+      const bool zeros = __syncthreads_or(zero);
+      // the warps' totals: one per lane, scanned once more
+      int sums = lane < kAttnThreads / 32 ? m->scan[lane] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sums, o);
+        if (lane >= o) sums += v;
+      }
+      total = __shfl_sync(0xffffffffu, sums, 31);
+      const int base = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+      take();
+      int at = (warp > 0 ? base : 0) + incl - mine;
+      if (end > begin && at <= begin && begin < at + mine) {
+        int r = r0;
+        for (;; ++r) {
+          const int t = row_units(p, r);
+          if (begin < at + t) break;
+          at += t;
+        }
+        m->start_row = r;
+        m->start_unit = begin - at;
+      }
+      if (zeros) {
+        // the list of empty rows lies where the tile will
+        int* list = reinterpret_cast<int*>(smem);
+        for (int i = 0; i < per; ++i) {
+          if (r0 + i < r1 && (r0 + i) % p.ctas == cta && row_units(p, r0 + i) == 0)
+            list[atomicAdd(&m->nzero, 1)] = r0 + i;
+          __syncthreads();
+          const int n = m->nzero;
+          __syncthreads();
+          if (tid == 0) m->nzero = 0;
+          for (int z = 0; z < n; ++z) clear(list[z], tid, kAttnThreads);
+          __syncthreads();
+        }
+      }
     }
     if (tid == 0) {
       m->begin = begin, m->end = end, m->total = total, m->ctas = ctas;
       split_record(p)[0] = -1;
     }
     __syncthreads();
-    if (zeros) {
-      // rows without a visible token: zeros (a length past the table: NaN); the
-      // list lies where the tile will
-      int* list = reinterpret_cast<int*>(smem);
-      for (int i = 0; i < per; ++i) {
-        if (r0 + i < r1 && (r0 + i) % p.ctas == cta && row_units(p, r0 + i) == 0)
-          list[atomicAdd(&m->nzero, 1)] = r0 + i;
-        __syncthreads();
-        const int n = m->nzero;
-        __syncthreads();
-        if (tid == 0) m->nzero = 0;
-        for (int z = 0; z < n; ++z) {
-          const int row = list[z];
-          const bool bad = __ldg(p.seqlens + row) > 0;
-          if (bad && tid == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
-          const uint32_t v = bad ? 0x7fff7fffu : 0u;
-          for (int j = tid; j < heads * (kLatent / 8); j += kAttnThreads) {
-            const int h = head0 + j / (kLatent / 8);
-            *reinterpret_cast<uint4*>(p.out + row * p.out_row + h * p.out_head + (j % (kLatent / 8)) * 8) =
-                make_uint4(v, v, v, v);
-          }
-          if (p.lse && tid < heads)
-            p.lse[(long long)row * p.H + head0 + tid] = bad ? CUDART_NAN_F : -CUDART_INF_F;
-        }
-        __syncthreads();
-      }
-    }
     walk.start(p, m->start_row, m->start_unit, end - begin);
   }
   tc_fence_after();
@@ -576,66 +681,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       if (tile.z & kFirst) {
         // the row's queries; their place is free once the last scores are done
         if (it > 0) wait(&m->sfull, prev);
-        if (wait.ok && !kFp8) {
-#pragma unroll 2
-          for (int h = w * kHeadsPerWarp; h < (w + 1) * kHeadsPerWarp; ++h) {
-            const uint32_t n = h < heads ? 16u : 0u;
-            const long long hh = h < heads ? head0 + h : head0;
-            const uint16_t* ql = p.ql + tile.x * p.ql_row + hh * p.ql_head + lane * 8;
-            const uint32_t dst = sbase + kOffQ + sub * kQBlockBytes + h * 128 + ((col ^ (h & 7)) << 4);
-            cp_async16(dst, ql, n);
-            cp_async16(dst + 4 * kQBlockBytes, ql + 256, n);
-          }
-          {
-            const int h = w * kHeadsPerWarp + sub;
-            const long long hh = h < heads ? head0 + h : head0;
-            cp_async16(sbase + kOffQ + kRopeBlock * kQBlockBytes + h * 128 + ((col ^ (h & 7)) << 4),
-                       p.qr + tile.x * p.qr_row + hh * p.qr_head + col * 8, h < heads ? 16u : 0u);
-          }
-        } else if (wait.ok) {
-#pragma unroll 1
-          for (int h = w * kHeadsPerWarp; h < (w + 1) * kHeadsPerWarp; ++h) {
-            uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a, r = a;
-            if (h < heads) {
-              const uint4* ql = reinterpret_cast<const uint4*>(p.ql + tile.x * p.ql_row + (head0 + h) * p.ql_head);
-              a = __ldg(ql + lane);
-              b = __ldg(ql + 32 + lane);
-              if (lane < 8)
-                r = __ldg(reinterpret_cast<const uint4*>(p.qr + tile.x * p.qr_row + (head0 + h) * p.qr_head) + lane);
-            }
-            float x[8], y[8];
-            unpack8(a, x);
-            unpack8(b, y);
-            float top = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
-            top = warp_max(top);
-            // 2^n that brings the largest into [2^14, 2^15)
-            const int n = top > 0.f ? min(max(127 + 14 - (int)(__float_as_uint(top) >> 23), -100), 100) : 0;
-            const float f = __uint_as_float((uint32_t)(n + 127) << 23);
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __half2 u = __floats2half2_rn(x[2 * j] * f, x[2 * j + 1] * f);
-              const __half2 v = __floats2half2_rn(y[2 * j] * f, y[2 * j + 1] * f);
-              o[j] = *reinterpret_cast<const uint32_t*>(&u);
-              o[4 + j] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            const uint32_t dst = sbase + kOffQ + h * 128 + ((col ^ (h & 7)) << 4);
-            st_shared_v4(dst + sub * kQBlockBytes, make_uint4(o[0], o[1], o[2], o[3]));
-            st_shared_v4(dst + (4 + sub) * kQBlockBytes, make_uint4(o[4], o[5], o[6], o[7]));
-            if (lane < 8) {
-              unpack8(r, x);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 u = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
-                o[j] = *reinterpret_cast<const uint32_t*>(&u);
-              }
-              st_shared_v4(dst + kRopeBlock * kQBlockBytes, make_uint4(o[0], o[1], o[2], o[3]));
-            }
-            if (lane == 0) m->mul[tile.w & 1][h] = p.scale_log2 * __uint_as_float((uint32_t)(127 - n) << 23);
-          }
-        }
+        // the first row's are the softmax warps' to bring: they have nothing
+        // else to do then
+        if (it > 0 && wait.ok) load_queries<KV, 1>(p, tile.x, head0, heads, w * kHeadsPerWarp, kHeadsPerWarp, sbase, lane, m->mul[tile.w & 1]);
       }
       if (!kFp8) {
         // every address before the first part falls free
@@ -857,6 +905,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     fewer_registers<kRegsMisc>();
     if (elect_one()) {
       Waiter<false> wait{p.status, true};
+      if (walk.left > 0) wait(&m->qfirst, 0);
       for (int it = 0; walk.left > 0; ++it) {
         // eight MMAs to a step of these loops: all 68 in a row push the other
         // roles out of the instruction cache, four leave the tensor pipe idle
@@ -921,6 +970,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     // rows and parts come as the lookup warps found them: no walk of its own
     bool bad = false, fresh = true, more = m->end > m->begin;  // fresh: some head has no reference yet
     uint32_t piece = 0;
+    if (more) {
+      load_queries<KV, 4>(p, walk.row, head0, heads, warp * 8, 8, sbase, lane, m->mul[0]);
+      cp_async_wait_all();
+      warp_arrive(&m->qfirst, lane);
+    }
     for (int it = 0; more; ++it) {
       const int slot = it % kRing;
       wait(&m->look_full[slot], (it / kRing) & 1);
@@ -1089,7 +1143,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           uint16_t* dst = row + part * 128;
           float* sum_at = part_at + hbase * kLatent + part * 128 + key;
 #pragma unroll 1
-          for (int h0 = 0; h0 < 32; h0 += 8) {
+          for (int h0 = 0; h0 < min(32, mine); h0 += 8) {
             uint32_t o[8];
             tmem_ld_32x32b_x8(my_tmem + part * kAttnHeads + h0, o);
             tmem_ld_wait8(o);
@@ -1175,23 +1229,41 @@ __global__ void __launch_bounds__(kJoinHeads * 128) latent_join_kernel(const Lat
   // the later pieces lie in slot 0 of their CTAs
   const float* rest = p.ws + (long long)blockIdx.x * 2 * kPartialFloats + step;
   const int n = last - cta;
-  float top = first[kAttnHeads * kLatent + h];
-  for (int i = 0; i < n; ++i) top = fmaxf(top, rest[i * step + kAttnHeads * kLatent + h]);
-  const float ref = top == -CUDART_INF_F ? 0.f : top;
-  float wgt = ex2(first[kAttnHeads * kLatent + h] - ref);
-  float total = first[kAttnHeads * kLatent + kAttnHeads + h] * wgt;
-  float4 v = *reinterpret_cast<const float4*>(first + h * kLatent + d);
-  float4 acc = make_float4(v.x * wgt, v.y * wgt, v.z * wgt, v.w * wgt);
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* s = rest + i * step;
-    wgt = ex2(s[kAttnHeads * kLatent + h] - ref);
-    total = fmaf(s[kAttnHeads * kLatent + kAttnHeads + h], wgt, total);
-    v = *reinterpret_cast<const float4*>(s + h * kLatent + d);
-    acc.x = fmaf(v.x, wgt, acc.x);
-    acc.y = fmaf(v.y, wgt, acc.y);
-    acc.z = fmaf(v.z, wgt, acc.z);
-    acc.w = fmaf(v.w, wgt, acc.w);
+  // pieces eight at a time, their loads together: piece -1 is the first
+  float top = -CUDART_INF_F, total = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int i0 = -1; i0 < n; i0 += 8) {
+    float mx[8], sm[8];
+    float4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u;
+      mx[u] = -CUDART_INF_F, sm[u] = 0.f, v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const float* s = i < 0 ? first : rest + i * step;
+        mx[u] = s[kAttnHeads * kLatent + h];
+        sm[u] = s[kAttnHeads * kLatent + kAttnHeads + h];
+        v[u] = *reinterpret_cast<const float4*>(s + h * kLatent + d);
+      }
+    }
+    float now = top;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) now = fmaxf(now, mx[u]);
+    const float ref = now == -CUDART_INF_F ? 0.f : now;
+    float wgt = ex2(top - ref);
+    total *= wgt;
+    acc.x *= wgt, acc.y *= wgt, acc.z *= wgt, acc.w *= wgt;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      wgt = ex2(mx[u] - ref);
+      total = fmaf(sm[u], wgt, total);
+      acc.x = fmaf(v[u].x, wgt, acc.x);
+      acc.y = fmaf(v[u].y, wgt, acc.y);
+      acc.z = fmaf(v[u].z, wgt, acc.z);
+      acc.w = fmaf(v[u].w, wgt, acc.w);
+    }
+    top = now;
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
