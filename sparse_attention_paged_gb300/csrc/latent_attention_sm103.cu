@@ -45,8 +45,8 @@
 // them, so one long row or a few short ones spread over every SM, and a
 // batch of any lengths is balanced.
 //
-// Warps: 0-7 softmax and output, 8 MMA issue, 9-11 token lookup, 12-27
-// loaders (four on each scheduler: the conversion is bound by latency).  The lookup warps go through selection list and block table up to
+// Warps: 0-7 softmax and output, 8 MMA issue, 9-11 token lookup, 12-19
+// loaders.  The lookup warps go through selection list and block table up to
 // three tiles ahead and ask L2 for the tokens' bytes, which keeps HBM busy
 // whatever the tile buffer does.  The loaders copy (bf16) or convert (fp8) 16
 // bytes at a time; masked tokens are not read, their rows are zeros.
@@ -79,15 +79,15 @@ constexpr int kBlockBytes = kTile * 128;        // 64 values of a tile's tokens
 constexpr int kPartBytes = 2 * kBlockBytes;
 constexpr int kRopeBlock = 8;                   // index of the rotated part's block
 constexpr int kQBlockBytes = kAttnHeads * 128;  // 64 values of the queries
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLookWarp0 = 9, kLookWarps = 3, kLoadWarp0 = 12, kLoadWarps = 16;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLookWarp0 = 9, kLookWarps = 3, kLoadWarp0 = 12, kLoadWarps = 8;
 constexpr int kAttnThreads = (kLoadWarp0 + kLoadWarps) * 32;
 // Tiles of looked-up tokens: one slot per lookup warp, so that no warp can be
 // two phases of a slot's barrier ahead of another.
 constexpr int kRing = kLookWarps;
-constexpr int kKeysPerWarp = kTile / kLoadWarps;  // 8
-constexpr int kHeadsPerWarp = kAttnHeads / kLoadWarps;  // 4
-// Registers per thread: at launch (65,536 / 896 in steps of 8), then per role.
-constexpr int kRegsLaunch = 72, kRegsSoftmax = 104, kRegsMisc = 64, kRegsLoad = 56;
+constexpr int kKeysPerWarp = kTile / kLoadWarps;  // 16
+constexpr int kHeadsPerWarp = kAttnHeads / kLoadWarps;  // 8
+// Registers per thread: at launch (65,536 / 640 in steps of 8), then per role.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsMisc = 64, kRegsLoad = 104;
 static_assert(kSoftmaxWarps * kRegsSoftmax + 4 * kRegsMisc + kLoadWarps * kRegsLoad <=
                   kAttnThreads / 32 * kRegsLaunch,
               "the roles' registers are those of the launch");
@@ -322,13 +322,17 @@ template <bool WARP>
 struct Waiter {
   int* status;
   bool ok;
+  __device__ __forceinline__ bool reached(uint64_t* bar, uint32_t parity) {
+    const bool r = mbar_try_wait(bar, parity);
+    return WARP ? __all_sync(0xffffffffu, r) : r;
+  }
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
     if (!ok) return false;
+    if (reached(bar, parity)) return true;
     const uint32_t t0 = (uint32_t)clock();
 #pragma unroll 1
     do {
-      const bool r = mbar_try_wait(bar, parity);
-      if (WARP ? __all_sync(0xffffffffu, r) : r) return true;
+      if (reached(bar, parity)) return true;
       const bool late = (uint32_t)clock() - t0 > kWaitLimit;
       ok = WARP ? !__any_sync(0xffffffffu, late) : !late;
     } while (ok);
@@ -375,8 +379,39 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// Sums 32 values per lane over the warp's lanes: lane l gets sum l.
-__device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
+// Two floats in one register pair: half the instructions.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 pair(uint32_t a, uint32_t b) { return pair(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ void unpair(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Sums 32 values per lane (16 pairs) over the warp's lanes: lane l gets sum l.
+__device__ __forceinline__ float sum_columns(const F2 (&pairs)[16], int lane) {
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) unpair(pairs[j], v[2 * j], v[2 * j + 1]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -628,22 +663,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
 
   if (warp >= kLoadWarp0) {
     // ---- loaders -------------------------------------------------------------
-    fewer_registers<kRegsLoad>();
-    // warp w brings tokens 8w .. 8w+7 of every tile
+    more_registers<kRegsLoad>();
+    // warp w brings tokens 16w .. 16w+15 of every tile
     const int w = warp - kLoadWarp0;
     const int sub = lane >> 3, col = lane & 7;     // rotated part and fp8: 4 tokens x 8 lanes
     auto token_at = [&](int slot, int j) { return m->token[slot][w * kKeysPerWarp + j]; };
     auto page_of = [&](int t) { return p.cache + (long long)(t >> 6) * p.page_stride; };
 
-    // fp8: tokens 4i + sub of the tile, and the codes of its first two parts,
-    // already in registers when the buffer falls free (the other two parts'
-    // follow into their place)
-    constexpr int kSteps = kKeysPerWarp / 4;
+    // fp8: four lanes take 64 codes of a token (one block of a part), the four
+    // next to them the other block of the token's neighbour: even and odd rows
+    // swizzle apart, so that the eight meet in no bank.  Step i: tokens 2p, 2p+1
+    // with p = sub + 4 (i / 2), changed over for odd i.  The codes of a tile's
+    // first two parts are in registers when the buffer falls free; the other
+    // two parts' follow into their place.
+    constexpr int kSteps = 4;
+    const int other = col >> 2;
+    auto step_token = [&](int i) { return 2 * (sub + 4 * (i >> 1)) + (other ^ (i & 1)); };
     uint4 codes[2][kSteps];
-    int tok[kSteps];
-    auto code_row = [&](int t) {
-      return (t >= 0 ? page_of(t) + (t & 63) * kLatent : reinterpret_cast<const uint8_t*>(g_zeros)) + col * 16;
-    };
+    const uint8_t* row[kSteps];
+    int rope_tok[kSteps];                          // rotated parts: tokens 4i + sub
     int4 tile = make_int4(0, 0, kEnd, 0);          // as the lookup warps found it
     auto fetch = [&](int it) {
       const int slot = it % kRing;
@@ -651,10 +689,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       tile = m->tile[slot];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        tok[i] = wait.ok ? token_at(slot, 4 * i + sub) : -1;
-        const uint8_t* row = code_row(tok[i]);
-#pragma unroll
-        for (int part = 0; part < 2; ++part) codes[part][i] = ld_stream(row + part * 128);
+        const int t = wait.ok ? token_at(slot, step_token(i)) : -1;
+        row[i] = (t >= 0 ? page_of(t) + (t & 63) * kLatent : reinterpret_cast<const uint8_t*>(g_zeros)) + col * 16;
+        codes[0][i] = ld_stream(row[i]);
+        codes[1][i] = ld_stream(row[i] + 128);
+        rope_tok[i] = wait.ok ? token_at(slot, 4 * i + sub) : -1;
       }
     };
     bool more = m->end > m->begin;
@@ -683,7 +722,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         if (it > 0) wait(&m->sfull, prev);
         // the first row's are the softmax warps' to bring: they have nothing
         // else to do then
-        if (it > 0 && wait.ok) load_queries<KV, 1>(p, tile.x, head0, heads, w * kHeadsPerWarp, kHeadsPerWarp, sbase, lane, m->mul[tile.w & 1]);
+        if (it > 0 && wait.ok)
+          load_queries<KV, 2>(p, tile.x, head0, heads, w * kHeadsPerWarp, kHeadsPerWarp, sbase, lane,
+                              m->mul[tile.w & 1]);
       }
       if (!kFp8) {
         // every address before the first part falls free
@@ -735,14 +776,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         if (wait.ok && deliver) warp_arrive(&m->full[kParts], lane);
       } else {
         uint2 ratio[kSteps];
+        uint32_t dst[kSteps];
         wait(&m->scale_full[slot], (it / kRing) & 1);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) ratio[i] = m->ratio[slot][w * kKeysPerWarp + 4 * i + sub];
+        for (int i = 0; i < kSteps; ++i) {
+          const int r = w * kKeysPerWarp + step_token(i);
+          ratio[i] = m->ratio[slot][r];
+          dst[i] = sbase + other * kBlockBytes + r * 128 + (((2 * (col & 3)) ^ (r & 7)) << 4);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&m->look_empty[slot]);
-        // lanes 4-7 of eight take their halves in the other order: no two
-        // lanes of a store meet in a bank
-        const int flip = col >> 2, c = (col & 3) * 2;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -754,18 +797,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
               for (int i = 0; i < kSteps; ++i) {
                 const uint32_t two = half ? ratio[i].y : ratio[i].x;
                 const uint32_t f = __byte_perm(two, two, odd ? 0x3232 : 0x1010);
-                const uint4 c4 = codes[odd][i];
-                const uint4 a = widen8(flip ? c4.z : c4.x, flip ? c4.w : c4.y, f);
-                const uint4 b = widen8(flip ? c4.x : c4.z, flip ? c4.y : c4.w, f);
-                const int r = w * kKeysPerWarp + 4 * i + sub;
-                const uint32_t row = sbase + part * kPartBytes + flip * kBlockBytes + r * 128;
-                st_shared_v4(row + (((c + flip) ^ (r & 7)) << 4), a);
-                st_shared_v4(row + (((c + 1 - flip) ^ (r & 7)) << 4), b);
+                st_shared_v4(dst[i] + part * kPartBytes, widen8(codes[odd][i].x, codes[odd][i].y, f));
+                st_shared_v4((dst[i] ^ 16) + part * kPartBytes, widen8(codes[odd][i].z, codes[odd][i].w, f));
               }
             }
             if (half == 0) {
 #pragma unroll
-              for (int i = 0; i < kSteps; ++i) codes[odd][i] = ld_stream(code_row(tok[i]) + (odd + 2) * 128);
+              for (int i = 0; i < kSteps; ++i) codes[odd][i] = ld_stream(row[i] + (odd + 2) * 128);
             }
             if (wait.ok && deliver) warp_arrive(&m->full[part], lane);
           }
@@ -773,9 +811,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         if (wait.ok && mine_used) {
 #pragma unroll
           for (int i = 0; i < kSteps; ++i) {
-            const int t = max(tok[i], 0);
+            const int t = max(rope_tok[i], 0);
             cp_async16(sbase + kOffP + (w * kKeysPerWarp + 4 * i + sub) * 128 + ((col ^ ((4 * i + sub) & 7)) << 4),
-                       page_of(t) + kRopeOffsetFp8 + (t & 63) * (kRope * 2) + col * 16, tok[i] < 0 ? 0u : 16u);
+                       page_of(t) + kRopeOffsetFp8 + (t & 63) * (kRope * 2) + col * 16, rope_tok[i] < 0 ? 0u : 16u);
           }
         }
         cp_async_wait_all();
@@ -966,7 +1004,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     const int hbase = half * 32, bar_half = 2 + half;
     const uint32_t my_tmem = tmem + ((uint32_t)(quarter * 32) << 16) + hbase;
     const int key = quarter * 32 + lane;
-    float sum[32];
+    F2 sum[16];
     // rows and parts come as the lookup warps found them: no walk of its own
     bool bad = false, fresh = true, more = m->end > m->begin;  // fresh: some head has no reference yet
     uint32_t piece = 0;
@@ -986,7 +1024,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       more = !(flags & kEnd);
       if (flags & kFirst) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sum[j] = 0.f;
+        for (int j = 0; j < 16; ++j) sum[j] = 0ull;
         bad = false;
         fresh = true;
       }
@@ -1001,6 +1039,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       // weights in log2 units over the reference, e = score - reference
       float e[32];
       const float key_log = kFp8 ? __log2f(key_scale) : 0.f;
+      const F2 ks2 = pair(key_scale, key_scale), sl2 = pair(p.scale_log2, p.scale_log2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t x[8], y[8];
@@ -1012,20 +1051,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           tmem_ld_wait8(x);
         }
 #pragma unroll
-        for (int j4 = 0; j4 < 8; j4 += 4) {
-          const float4 n4 = *reinterpret_cast<const float4*>(&m->nref[hbase + 8 * i + j4]);
-          const float nref[4] = {n4.x, n4.y, n4.z, n4.w};
-          float mul[4] = {p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2};
+        for (int j = 0; j < 8; j += 4) {
+          const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(&m->nref[hbase + 8 * i + j]);
+          F2 u0 = pair(x[j], x[j + 1]), u1 = pair(x[j + 2], x[j + 3]);
           if (kFp8) {
-            const float4 m4 = *reinterpret_cast<const float4*>(&m->mul[piece & 1][hbase + 8 * i + j4]);
-            mul[0] = m4.x, mul[1] = m4.y, mul[2] = m4.z, mul[3] = m4.w;
+            const ulonglong2 m2 = *reinterpret_cast<const ulonglong2*>(&m->mul[piece & 1][hbase + 8 * i + j]);
+            u0 = fma2(fma2(u0, ks2, pair(y[j], y[j + 1])), m2.x, n2.x);
+            u1 = fma2(fma2(u1, ks2, pair(y[j + 2], y[j + 3])), m2.y, n2.y);
+          } else {
+            u0 = fma2(u0, sl2, n2.x);
+            u1 = fma2(u1, sl2, n2.y);
           }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float v = __uint_as_float(x[j4 + u]);
-            if (kFp8) v = fmaf(v, key_scale, __uint_as_float(y[j4 + u]));
-            e[8 * i + j4 + u] = fmaf(v, mul[u], nref[u]);
-          }
+          unpair(u0, e[8 * i + j], e[8 * i + j + 1]);
+          unpair(u1, e[8 * i + j + 2], e[8 * i + j + 3]);
         }
       }
       if (!valid)
@@ -1066,7 +1104,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         if (!(flags & kFirst)) {
           // the scores' commit covers the last value product: O^T is at rest
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sum[j] *= m->keep[hbase + j];
+          for (int j = 0; j < 16; ++j)
+            sum[j] = mul2(sum[j], *reinterpret_cast<const F2*>(&m->keep[hbase + 2 * j]));
 #pragma unroll 1
           for (int i = 0; i < 4 * kParts; ++i) {
             uint32_t o[8];
@@ -1087,11 +1126,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         uint32_t w[4];
 #pragma unroll
         for (int u = 0; u < 8; u += 2) {
-          const float a = ex2(e[j8 + u]), b = ex2(e[j8 + u + 1]);
-          sum[j8 + u] += a;
-          sum[j8 + u + 1] += b;
+          float a = ex2(e[j8 + u]), b = ex2(e[j8 + u + 1]);
+          const F2 ab = pair(a, b);
+          sum[(j8 + u) / 2] = add2(sum[(j8 + u) / 2], ab);
           if (kFp8) {
-            const __half2 v = __floats2half2_rn(a * key_scale, b * key_scale);
+            unpair(mul2(ab, ks2), a, b);
+            const __half2 v = __floats2half2_rn(a, b);
             w[u / 2] = *reinterpret_cast<const uint32_t*>(&v);
           } else {
             const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
