@@ -87,7 +87,7 @@ constexpr int kRing = kLookWarps;
 constexpr int kKeysPerWarp = kTile / kLoadWarps;  // 16
 constexpr int kHeadsPerWarp = kAttnHeads / kLoadWarps;  // 8
 // Registers per thread: at launch (65,536 / 640 in steps of 8), then per role.
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsMisc = 64, kRegsLoad = 104;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsMisc = 72, kRegsLoad = 96;
 static_assert(kSoftmaxWarps * kRegsSoftmax + 4 * kRegsMisc + kLoadWarps * kRegsLoad <=
                   kAttnThreads / 32 * kRegsLaunch,
               "the roles' registers are those of the launch");
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     // with p = sub + 4 (i / 2), changed over for odd i.  The codes of a tile's
     // first two parts are in registers when the buffer falls free; the other
     // two parts' follow into their place.
-    constexpr int kSteps = 4;
+    constexpr int kSteps = kKeysPerWarp / 4;
     const int other = col >> 2;
     auto step_token = [&](int i) { return 2 * (sub + 4 * (i >> 1)) + (other ^ (i & 1)); };
     uint4 codes[2][kSteps];
