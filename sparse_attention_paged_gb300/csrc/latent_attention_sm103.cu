@@ -1164,7 +1164,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
             if (p.lse && h < heads)
               p.lse[(long long)what.x * p.H + head0 + h] = (max_h + log2f(total_h)) * 0.69314718055994531f;
           } else {
-            m->fac[h] = bad ? CUDART_NAN_F : 1.f;
             part_at[kAttnHeads * kLatent + h] = max_h;
             part_at[kAttnHeads * kLatent + kAttnHeads + h] = total_h;
           }
@@ -1172,7 +1171,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         }
         bar_sync(bar_half, 128);
         tc_fence_after();
-        // eight heads of a part at a time.  A warp's instructions come one in
+        // sixteen heads of a part at a time.  A warp's instructions come one in
         // about eight cycles here, so the loop is short rather than wide: bf16
         // pairs change lanes as one word, and pointers only move on
         const int odd = lane & 1, mine = heads - hbase;   // this half's heads
@@ -1183,31 +1182,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           uint16_t* dst = row + part * 128;
           float* sum_at = part_at + hbase * kLatent + part * 128 + key;
 #pragma unroll 1
-          for (int h0 = 0; h0 < min(32, mine); h0 += 8) {
-            uint32_t o[8];
-            tmem_ld_32x32b_x8(my_tmem + part * kAttnHeads + h0, o);
-            tmem_ld_wait8(o);
-            const float4 fa = *reinterpret_cast<const float4*>(&m->fac[hbase + h0]);
-            const float4 fb = *reinterpret_cast<const float4*>(&m->fac[hbase + h0 + 4]);
-            const float v[8] = {__uint_as_float(o[0]) * fa.x, __uint_as_float(o[1]) * fa.y,
-                                __uint_as_float(o[2]) * fa.z, __uint_as_float(o[3]) * fa.w,
-                                __uint_as_float(o[4]) * fb.x, __uint_as_float(o[5]) * fb.y,
-                                __uint_as_float(o[6]) * fb.z, __uint_as_float(o[7]) * fb.w};
+          for (int h0 = 0; h0 < min(32, mine); h0 += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(my_tmem + part * kAttnHeads + h0, o);
+            tmem_ld_wait(o);
             if (whole) {
               // two heads of a lane pair: each lane writes two values of one head
 #pragma unroll
-              for (int j = 0; j < 8; j += 2) {
-                const __nv_bfloat162 two = __floats2bfloat162_rn(v[j], v[j + 1]);
+              for (int j = 0; j < 16; j += 2) {
+                const float2 f = *reinterpret_cast<const float2*>(&m->fac[hbase + h0 + j]);
+                const __nv_bfloat162 two =
+                    __floats2bfloat162_rn(__uint_as_float(o[j]) * f.x, __uint_as_float(o[j + 1]) * f.y);
                 const uint32_t a = *reinterpret_cast<const uint32_t*>(&two);
                 const uint32_t c = __byte_perm(a, __shfl_xor_sync(0xffffffffu, a, 1), pick);
                 if (h0 + j + odd < mine) *reinterpret_cast<uint32_t*>(dst) = c;
                 dst += 2 * p.out_head;
               }
             } else {
+              // a part that went wrong has a total that is NaN: that is enough
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (h0 + j < mine) sum_at[j * kLatent] = v[j];
-              sum_at += 8 * kLatent;
+              for (int j = 0; j < 16; ++j)
+                if (h0 + j < mine) sum_at[j * kLatent] = __uint_as_float(o[j]);
+              sum_at += 16 * kLatent;
             }
           }
         }
@@ -1250,35 +1246,65 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial sums of one row that slices cut: grid (CTA whose piece
-// begins the row, four heads), a head per 128 threads.
-constexpr int kJoinHeads = 4;
-__global__ void __launch_bounds__(kJoinHeads * 128) latent_join_kernel(const LatentAttnParams p, int main_ctas) {
+// Joins the partial sums of the rows that slices cut: block (c, y) those of
+// the row that CTA c's slice begins and does not end (WIDE: of the c-th such row).  A thread has four values of a head; the pieces are read
+// four at a time, their loads together.  WIDE (few rows, so each may have
+// many pieces): a block has one head, and its four groups of 128 threads a
+// quarter of the pieces each.  Otherwise it has four heads.
+constexpr int kJoinThreads = 512;
+template <bool WIDE>
+__global__ void __launch_bounds__(kJoinThreads, 3) latent_join_kernel(const LatentAttnParams p, int main_ctas) {
+  __shared__ float4 sums[4][128];
+  __shared__ float2 stats[4][128];
   griddep_wait();
   griddep_launch_dependents();
-  const int* rec = reinterpret_cast<const int*>(p.ws + (long long)main_ctas * 2 * kPartialFloats) +
-                   (long long)blockIdx.x * kSplitInts;
-  const int row = rec[0], last = rec[1];
+  const int lane = threadIdx.x & 31, grp = blockIdx.x % p.groups;
+  const int* rec = reinterpret_cast<const int*>(p.ws + (long long)main_ctas * 2 * kPartialFloats) + grp * kSplitInts;
+  int cta = blockIdx.x / p.groups;
+  if (WIDE) {
+    // the CTA whose slice begins the row: the cta-th with a record
+    int want = cta;
+    cta = -1;
+    for (int c0 = 0; c0 < p.ctas && cta < 0; c0 += 160) {
+      uint32_t found[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const int c = c0 + 32 * i + lane;
+        found[i] = c < p.ctas && rec[(long long)c * p.groups * kSplitInts] >= 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        uint32_t f = __ballot_sync(0xffffffffu, found[i] != 0);
+        const int n = __popc(f);
+        if (cta < 0 && want < n) {
+          for (; want > 0; --want) f &= f - 1;
+          cta = c0 + 32 * i + __ffs(f) - 1;
+        }
+        want -= n;
+      }
+    }
+  }
+  if (cta < 0) return;
+  rec += (long long)cta * p.groups * kSplitInts;
+  const int row = rec[0], n = rec[1] - cta;      // n pieces after the first
   if (row < 0) return;
-  const int cta = blockIdx.x / p.groups, grp = blockIdx.x % p.groups;
-  const int h = blockIdx.y * kJoinHeads + threadIdx.x / 128, d = (threadIdx.x % 128) * 4;
+  const int part = threadIdx.x / 128, d = (threadIdx.x % 128) * 4;
+  const int h = WIDE ? blockIdx.y : blockIdx.y * 4 + part;
   const int head = grp * kAttnHeads + h;
-  if (head >= p.H) return;
+  if (head >= p.H) return;                       // WIDE: the whole block
   const long long step = (long long)p.groups * 2 * kPartialFloats;
-  const float* first = p.ws + ((long long)blockIdx.x * 2 + 1) * kPartialFloats;
-  // the later pieces lie in slot 0 of their CTAs
-  const float* rest = p.ws + (long long)blockIdx.x * 2 * kPartialFloats + step;
-  const int n = last - cta;
-  // pieces eight at a time, their loads together: piece -1 is the first
+  // the first piece lies in slot 1 of its CTA, the later ones in slot 0 of theirs
+  const float* rest = p.ws + ((long long)cta * p.groups + grp) * 2 * kPartialFloats + step;
+  const float* first = rest - step + kPartialFloats;
   float top = -CUDART_INF_F, total = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int i0 = -1; i0 < n; i0 += 8) {
-    float mx[8], sm[8];
-    float4 v[8];
+  for (int i0 = -1 + (WIDE ? part : 0); i0 < n; i0 += WIDE ? 16 : 4) {
+    float mx[4], sm[4];
+    float4 v[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u;
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * (WIDE ? 4 : 1);
       mx[u] = -CUDART_INF_F, sm[u] = 0.f, v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
         const float* s = i < 0 ? first : rest + i * step;
@@ -1289,19 +1315,44 @@ __global__ void __launch_bounds__(kJoinHeads * 128) latent_join_kernel(const Lat
     }
     float now = top;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) now = fmaxf(now, mx[u]);
+    for (int u = 0; u < 4; ++u) now = fmaxf(now, mx[u]);
     const float ref = now == -CUDART_INF_F ? 0.f : now;
     float wgt = ex2(top - ref);
     total *= wgt;
     acc.x *= wgt, acc.y *= wgt, acc.z *= wgt, acc.w *= wgt;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < 4; ++u) {
       wgt = ex2(mx[u] - ref);
       total = fmaf(sm[u], wgt, total);
       acc.x = fmaf(v[u].x, wgt, acc.x);
       acc.y = fmaf(v[u].y, wgt, acc.y);
       acc.z = fmaf(v[u].z, wgt, acc.z);
       acc.w = fmaf(v[u].w, wgt, acc.w);
+    }
+    top = now;
+  }
+  if (WIDE) {
+    sums[part][threadIdx.x % 128] = acc;
+    stats[part][threadIdx.x % 128] = make_float2(top, total);
+    __syncthreads();
+    if (part > 0) return;
+    float now = top;
+#pragma unroll
+    for (int u = 1; u < 4; ++u) now = fmaxf(now, stats[u][threadIdx.x].x);
+    const float ref = now == -CUDART_INF_F ? 0.f : now;
+    float wgt = ex2(top - ref);
+    total *= wgt;
+    acc.x *= wgt, acc.y *= wgt, acc.z *= wgt, acc.w *= wgt;
+#pragma unroll
+    for (int u = 1; u < 4; ++u) {
+      const float2 st = stats[u][threadIdx.x];
+      const float4 v = sums[u][threadIdx.x];
+      wgt = ex2(st.x - ref);
+      total = fmaf(st.y, wgt, total);
+      acc.x = fmaf(v.x, wgt, acc.x);
+      acc.y = fmaf(v.y, wgt, acc.y);
+      acc.z = fmaf(v.z, wgt, acc.z);
+      acc.w = fmaf(v.w, wgt, acc.w);
     }
     top = now;
   }
@@ -1332,11 +1383,20 @@ cudaError_t launch_t(LatentAttnParams p, int sms, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, latent_attention_kernel<KV>, p);
   if (e != cudaSuccess) return e;
+  // a slice cuts at most one row at its end: at most `cut` rows a head group
+  const int cut = p.rows < p.ctas ? p.rows : p.ctas, heads = p.H < kAttnHeads ? p.H : kAttnHeads;
+  // the wide join where a row may be in 16 pieces or more (one row of 131,072
+  // tokens, 128 heads: the call takes 72 us with it and 78 without; one row of
+  // 512 selected tokens, 8 pieces: 13.2 with it and 12.2 without)
+  const long long units = p.idx ? (p.k + kUnit - 1) / kUnit : p.W;
+  const bool wide = cut * p.groups <= 16 && min((long long)p.ctas, units * p.rows) >= 16LL * p.rows;
   cudaLaunchConfig_t join = cfg;
-  join.gridDim = dim3(p.ctas * p.groups, (min(p.H, kAttnHeads) + kJoinHeads - 1) / kJoinHeads);
-  join.blockDim = dim3(kJoinHeads * 128);
+  join.gridDim = dim3((wide ? cut : p.ctas) * p.groups, wide ? heads : (heads + 3) / 4);
+  join.blockDim = dim3(kJoinThreads);
   join.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&join, latent_join_kernel, p, (int)(p.ctas * p.groups));
+  const int main_ctas = p.ctas * p.groups;
+  return wide ? cudaLaunchKernelEx(&join, latent_join_kernel<true>, p, main_ctas)
+              : cudaLaunchKernelEx(&join, latent_join_kernel<false>, p, main_ctas);
 }
 
 }  // namespace
