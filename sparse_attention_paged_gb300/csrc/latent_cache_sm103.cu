@@ -16,10 +16,17 @@
 //
 // Load: a range of each request's tokens as packed bf16 rows.
 //
-// One warp per token in both: lane l holds values 16l .. 16l+15 and the
-// rotated values 2l, 2l+1; a group's maximum is a shuffle over eight lanes.
-// HBM-bound; a warp's 1,152 bytes are all in flight at once, so 64 warps an
-// SM cover the latency.
+// One warp per token in both, all of a token's loads at once; HBM-bound for
+// many tokens, by latency for few.  In the store lane l holds values
+// 16l .. 16l+15 and a group's maximum is a shuffle over eight lanes; in the
+// load it holds 8l .. 8l+7 and 256 + 8l .., so that a warp writes 512
+// adjacent bytes an instruction (4% faster than 32 bytes a lane).  Measured
+// out of HBM, one call after another: storing 65,536 tokens with the norm
+// and the rotation 29.1 us (fp8, 4.1 TB/s) and 28.9 us (bf16, 5.2 TB/s),
+// loading them 21.3 us (fp8, 5.6 TB/s) and 25.0 us (bf16, 6.0 TB/s); 1,024
+// tokens 2.5 us either way.  The store's work, about 250 instructions
+// a token and 64 passes of L1 for the weights, is what keeps it from the
+// load's rate.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -58,30 +65,17 @@ __device__ __forceinline__ int scale_exponent(float top) {
   return max(e, -126);
 }
 
+// One token's latent (r0, r1: this lane's 16 values; w: their weights) and
+// rotated part (rr: its two) into their place.
 template <int KV>
-__global__ void __launch_bounds__(kWarps * 32) latent_store_kernel(const LatentStoreParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * kWarps + warp;
-  sm100::griddep_wait();
-  sm100::griddep_launch_dependents();
-  if (i >= p.n) return;
-  const int at = __ldg(p.slots + i);
-  if (at < 0) return;                                          // warp-uniform
-  const uint4* src = reinterpret_cast<const uint4*>(p.latent + i * p.latent_stride) + lane * 2;
-  const uint4 r0 = __ldg(src), r1 = __ldg(src + 1);
-  const uint32_t rr = __ldg(reinterpret_cast<const uint32_t*>(p.rope + i * p.rope_stride) + lane);
-  const int page = at / kPage, slot = at % kPage;
-  if (page >= p.num_pages) {
-    if (lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
-    return;
-  }
+__device__ __forceinline__ void store_token(const LatentStoreParams& p, int page, int slot, int pos, uint4 r0,
+                                            uint4 r1, uint32_t rr, const float (&w)[16], int lane) {
   uint8_t* pg = p.cache + (long long)page * p.page_stride;
 
   // the rotated part
   float a, b;
   unpack2(rr, a, b);
   if (p.positions != nullptr) {
-    const int pos = __ldg(p.positions + i);
     if (pos < 0 || pos >= p.max_pos) {
       if (lane == 0) raise_status(p.status, DSA_ERR_BAD_POSITION);
       a = b = CUDART_NAN_F;
@@ -122,15 +116,8 @@ __global__ void __launch_bounds__(kWarps * 32) latent_store_kernel(const LatentS
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float r = rsqrtf(s * (1.f / kLatent) + p.eps);
-    const float4* w = reinterpret_cast<const float4*>(p.weight) + lane * 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 f = __ldg(w + j);
-      x[4 * j] = x[4 * j] * r * f.x;
-      x[4 * j + 1] = x[4 * j + 1] * r * f.y;
-      x[4 * j + 2] = x[4 * j + 2] * r * f.z;
-      x[4 * j + 3] = x[4 * j + 3] * r * f.w;
-    }
+    for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
   }
   if (KV == DSA_KV_BF16) {
     uint4* dst = reinterpret_cast<uint4*>(pg + slot * kTokenBytesBf16) + lane * 2;
@@ -162,6 +149,47 @@ __global__ void __launch_bounds__(kWarps * 32) latent_store_kernel(const LatentS
       make_uint4(codes[0], codes[1], codes[2], codes[3]);
   if ((lane & 7) == 0)
     reinterpret_cast<float*>(pg + kScaleOffsetFp8)[slot * kLatentGroups + lane / 8] = pow2(e);
+}
+
+template <int KV, int TOK>
+__global__ void __launch_bounds__(kWarps * 32) latent_store_kernel(const LatentStoreParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long i0 = ((long long)blockIdx.x * kWarps + warp) * TOK;
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  int at[TOK], pos[TOK];
+  uint4 r0[TOK], r1[TOK];
+  uint32_t rr[TOK];
+#pragma unroll
+  for (int u = 0; u < TOK; ++u) {
+    const long long i = i0 + u;
+    at[u] = -1, pos[u] = 0;
+    if (i >= p.n) continue;
+    at[u] = __ldg(p.slots + i);
+    if (p.positions != nullptr) pos[u] = __ldg(p.positions + i);
+    const uint4* src = reinterpret_cast<const uint4*>(p.latent + i * p.latent_stride) + lane * 2;
+    r0[u] = __ldg(src), r1[u] = __ldg(src + 1);
+    rr[u] = __ldg(reinterpret_cast<const uint32_t*>(p.rope + i * p.rope_stride) + lane);
+  }
+  float w[16];
+  if (p.weight != nullptr) {
+    const float4* src = reinterpret_cast<const float4*>(p.weight) + lane * 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 f = __ldg(src + j);
+      w[4 * j] = f.x, w[4 * j + 1] = f.y, w[4 * j + 2] = f.z, w[4 * j + 3] = f.w;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < TOK; ++u) {
+    if (at[u] < 0) continue;                                   // warp-uniform, as all below
+    const int page = at[u] / kPage;
+    if (page >= p.num_pages) {
+      if (lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
+      continue;
+    }
+    store_token<KV>(p, page, at[u] % kPage, pos[u], r0[u], r1[u], rr[u], w, lane);
+  }
 }
 
 // The request of output row i: the last r < n_req with cu[r] <= i (0 if
@@ -205,14 +233,16 @@ __global__ void __launch_bounds__(kWarps * 32) latent_load_kernel(const LatentLo
       const uint8_t* pg = p.cache + (long long)page * p.page_stride;
       const int slot = (int)(pos % kPage);
       if (KV == DSA_KV_BF16) {
-        const uint4* src = reinterpret_cast<const uint4*>(pg + slot * kTokenBytesBf16) + lane * 2;
-        o0 = src[0], o1 = src[1];
+        const uint4* src = reinterpret_cast<const uint4*>(pg + slot * kTokenBytesBf16) + lane;
+        o0 = src[0], o1 = src[32];
         orope = reinterpret_cast<const uint32_t*>(pg + slot * kTokenBytesBf16 + kLatent * 2)[lane];
       } else {
-        const uint4 c = reinterpret_cast<const uint4*>(pg + slot * kLatent)[lane];
-        const float s = reinterpret_cast<const float*>(pg + kScaleOffsetFp8)[slot * kLatentGroups + lane / 8];
+        const uint2* src = reinterpret_cast<const uint2*>(pg + slot * kLatent) + lane;
+        const uint2 c0 = src[0], c1 = src[32];
+        const float* scale = reinterpret_cast<const float*>(pg + kScaleOffsetFp8) + slot * kLatentGroups + lane / 16;
+        const float s0 = scale[0], s1 = scale[2];
         orope = reinterpret_cast<const uint32_t*>(pg + kRopeOffsetFp8 + slot * (kRope * 2))[lane];
-        const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+        const uint32_t u[4] = {c0.x, c0.y, c1.x, c1.y};
         uint32_t o[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -220,6 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32) latent_load_kernel(const LatentLo
           for (int h = 0; h < 2; ++h) {
             const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[j] >> (16 * h)), __NV_E4M3);
             const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+            const float s = j < 2 ? s0 : s1;
             o[2 * j + h] = pack2(v.x * s, v.y * s);
           }
         o0 = make_uint4(o[0], o[1], o[2], o[3]);
@@ -228,15 +259,21 @@ __global__ void __launch_bounds__(kWarps * 32) latent_load_kernel(const LatentLo
     }
   }
   uint16_t* out = p.out + i * p.out_stride;
-  reinterpret_cast<uint4*>(out)[lane * 2] = o0;
-  reinterpret_cast<uint4*>(out)[lane * 2 + 1] = o1;
+  reinterpret_cast<uint4*>(out)[lane] = o0;
+  reinterpret_cast<uint4*>(out)[lane + 32] = o1;
   reinterpret_cast<uint32_t*>(out + kLatent)[lane] = orope;
 }
 
+// From this many tokens on a warp stores kManyTok of them and loads their
+// weights once: 4,096 tokens 4.3 us for 4.8, 22,528 12.3 for 13.0, 65,536
+// 29.1 for 33.3 (fp8).  Below, latency counts: 1,024 tokens 3.2 us for 2.5.
+// Four or eight a warp are slower than two at 22,528 tokens.
+constexpr int kMany = 4096, kManyTok = 2;
+
 template <typename P>
-cudaError_t launch(void (*kernel)(P), const P& p, cudaStream_t stream) {
+cudaError_t launch(void (*kernel)(P), const P& p, int tok, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)p.n + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3((unsigned)(((long long)p.n + kWarps * tok - 1) / (kWarps * tok)));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -250,13 +287,16 @@ cudaError_t launch(void (*kernel)(P), const P& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_latent_store(const LatentStoreParams& p, int kv_dtype, cudaStream_t stream) {
-  if (kv_dtype == DSA_KV_BF16) return launch(latent_store_kernel<DSA_KV_BF16>, p, stream);
-  return launch(latent_store_kernel<DSA_KV_FP8_E4M3>, p, stream);
+  if (p.n >= kMany)
+    return kv_dtype == DSA_KV_BF16 ? launch(latent_store_kernel<DSA_KV_BF16, kManyTok>, p, kManyTok, stream)
+                                   : launch(latent_store_kernel<DSA_KV_FP8_E4M3, kManyTok>, p, kManyTok, stream);
+  return kv_dtype == DSA_KV_BF16 ? launch(latent_store_kernel<DSA_KV_BF16, 1>, p, 1, stream)
+                                 : launch(latent_store_kernel<DSA_KV_FP8_E4M3, 1>, p, 1, stream);
 }
 
 cudaError_t launch_latent_load(const LatentLoadParams& p, int kv_dtype, cudaStream_t stream) {
-  if (kv_dtype == DSA_KV_BF16) return launch(latent_load_kernel<DSA_KV_BF16>, p, stream);
-  return launch(latent_load_kernel<DSA_KV_FP8_E4M3>, p, stream);
+  return kv_dtype == DSA_KV_BF16 ? launch(latent_load_kernel<DSA_KV_BF16>, p, 1, stream)
+                                 : launch(latent_load_kernel<DSA_KV_FP8_E4M3>, p, 1, stream);
 }
 
 }  // namespace dsa
