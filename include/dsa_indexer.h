@@ -409,7 +409,12 @@ int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_page
  *             current device, 16-byte aligned; calls that may overlap need
  *             one each.
  * The softmax and all sums are fp32; the weights of the value product are
- * rounded to bf16.  The launch shape depends on H alone, so a captured call
+ * rounded to bf16.  With an fp8 cache latent queries, weights and tokens are
+ * fp16 under scales of their own (a power of two per head, the largest of a
+ * token's four scales per token): exact for scales that are powers of two
+ * within 2^15 of the token's largest; another scale is rounded as a ratio of
+ * the largest and so are its products (2^-11 each), and what falls below
+ * 2^-24 of the largest scale is lost.  The launch shape depends on H alone, so a captured call
  * may be replayed with other lengths, lists and tables.  Two kernel launches.
  * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
  * visible position without a page in the pool a NaN row and
