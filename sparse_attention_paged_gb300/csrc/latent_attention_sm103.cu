@@ -50,6 +50,17 @@
 // three tiles ahead and ask L2 for the tokens' bytes, which keeps HBM busy
 // whatever the tile buffer does.  The loaders copy (bf16) or convert (fp8) 16
 // bytes at a time; masked tokens are not read, their rows are zeros.
+//
+// Measured (whole call, 64 heads where not said otherwise): 64 rows of 2,048
+// selected tokens each, bf16, 65.5 us; 64 rows of 512 to 32,768 tokens, fp8,
+// 145 us; one row of 131,072 bf16 tokens and 128 heads 72 us (151 MB, 2.1
+// TB/s); 1,024 fp8 prefill rows of 2,048 selected tokens 497 us (590
+// TFLOP/s); one row of 512 and 16 heads 12 us.  What bounds it: a tile's chain of loads, scores,
+// softmax and values, 7,300 to 8,800 cycles per 128 fp8 tokens, of which
+// shared memory is busy for 4,400 (both products' operands and the loaders'
+// stores) and the softmax for 1,450 to 2,100.  Tiles of 64 tokens in two
+// buffers overlapped more but ran their products at half rate: the prefill
+// took 1,316 us, the ragged rows 366.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
