@@ -1282,7 +1282,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
 // quarter of the pieces each.  Otherwise it has four heads.
 constexpr int kJoinThreads = 512;
 template <bool WIDE>
-__global__ void __launch_bounds__(kJoinThreads, 3) latent_join_kernel(const LatentAttnParams p, int main_ctas) {
+__global__ void __launch_bounds__(kJoinThreads, WIDE ? 2 : 3) latent_join_kernel(const LatentAttnParams p, int main_ctas) {
   __shared__ float4 sums[4][128];
   __shared__ float2 stats[4][128];
   griddep_wait();
