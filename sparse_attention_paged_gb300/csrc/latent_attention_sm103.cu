@@ -448,10 +448,17 @@ __device__ __forceinline__ float sum_columns(const F2 (&pairs)[16], int lane) {
   return v[0];
 }
 
-// Which row a CTA's slice leaves unfinished (-1: none), and the CTA with its
-// last unit.
-__device__ __forceinline__ int* split_record(const LatentAttnParams& p) {
-  return reinterpret_cast<int*>(p.ws + (long long)gridDim.x * 2 * kPartialFloats) + (long long)blockIdx.x * kSplitInts;
+// The split records, {row or -1, CTA with its last unit, CTA with its first, 0}:
+// one per row where there are no more rows than CTAs (-1: nothing to join),
+// else one per CTA, for the row that its slice begins and does not end.
+__device__ __forceinline__ bool records_by_row(const LatentAttnParams& p) { return p.rows <= p.ctas; }
+
+__device__ __forceinline__ void record_split(const LatentAttnParams& p, int row, bool split, int last) {
+  const int grp = blockIdx.x % p.groups, cta = blockIdx.x / p.groups;
+  if (!split && !records_by_row(p)) return;       // the CTA's -1 is there from the start
+  reinterpret_cast<int4*>(p.ws + (long long)gridDim.x * 2 * kPartialFloats)[(records_by_row(p) ? row : cta) * p.groups +
+                                                                            grp] =
+      make_int4(split ? row : -1, last, cta, 0);
 }
 
 // What a masked token's codes are read from.
@@ -594,6 +601,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     auto clear = [&](int row, int first, int step) {
       const bool bad = __ldg(p.seqlens + row) > 0;
       if (bad && first == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
+      if (first == 0) record_split(p, row, false, 0);
       const uint32_t v = bad ? 0x7fff7fffu : 0u;
 #pragma unroll 1
       for (int j = first; j < heads * (kLatent / 8); j += step)
@@ -677,7 +685,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     }
     if (tid == 0) {
       m->begin = begin, m->end = end, m->total = total, m->ctas = ctas;
-      split_record(p)[0] = -1;
+      if (!records_by_row(p))
+        reinterpret_cast<int4*>(p.ws + (long long)gridDim.x * 2 * kPartialFloats)[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
     walk.start(p, m->start_row, m->start_unit, end - begin);
@@ -895,11 +904,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           if (walk.first) {
             const bool begins = walk.u == 0, whole = begins && walk.left >= walk.units();
             m->piece[walk.piece & 7] = make_int4(walk.row, (begins ? kBegins : 0) | (whole ? kWhole : 0), 0, 0);
-            if (begins && !whole) {
-              // the row goes on in later CTAs
+            if (begins) {
+              // where the row ends, should it go on in later CTAs
               const long long last_unit = (long long)m->end - walk.left + walk.units() - 1;
-              split_record(p)[0] = walk.row;
-              split_record(p)[1] = (int)(((last_unit + 1) * m->ctas - 1) / m->total);
+              record_split(p, walk.row, !whole, whole ? 0 : (int)(((last_unit + 1) * m->ctas - 1) / m->total));
             }
           }
         }
@@ -1261,10 +1269,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
             part_at[kAttnHeads * kLatent + kAttnHeads + h] = CUDART_NAN_F;
           }
         }
-        if (begins && !whole && tid == 0) {
+        if (begins && tid == 0) {
           const long long last_unit = (long long)m->end - walk.left + walk.units() - 1;
-          split_record(p)[0] = walk.row;
-          split_record(p)[1] = (int)(((last_unit + 1) * m->ctas - 1) / m->total);
+          record_split(p, walk.row, !whole, whole ? 0 : (int)(((last_unit + 1) * m->ctas - 1) / m->total));
         }
       }
     }
@@ -1275,9 +1282,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial sums of the rows that slices cut: block (c, y) those of
-// the row that CTA c's slice begins and does not end (WIDE: of the c-th such row).  A thread has four values of a head; the pieces are read
-// four at a time, their loads together.  WIDE (few rows, so each may have
+// Joins the partial sums of the rows that slices cut, a block (record, heads).
+// A thread has four values of a head; the pieces are read four at a time,
+// their loads together.  WIDE (few rows, so each may have
 // many pieces): a block has one head, and its four groups of 128 threads a
 // quarter of the pieces each.  Otherwise it has four heads.
 constexpr int kJoinThreads = 512;
@@ -1287,35 +1294,9 @@ __global__ void __launch_bounds__(kJoinThreads, WIDE ? 2 : 3) latent_join_kernel
   __shared__ float2 stats[4][128];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, grp = blockIdx.x % p.groups;
-  const int* rec = reinterpret_cast<const int*>(p.ws + (long long)main_ctas * 2 * kPartialFloats) + grp * kSplitInts;
-  int cta = blockIdx.x / p.groups;
-  if (WIDE) {
-    // the CTA whose slice begins the row: the cta-th with a record
-    int want = cta;
-    cta = -1;
-    for (int c0 = 0; c0 < p.ctas && cta < 0; c0 += 160) {
-      uint32_t found[5];
-#pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        const int c = c0 + 32 * i + lane;
-        found[i] = c < p.ctas && rec[(long long)c * p.groups * kSplitInts] >= 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        uint32_t f = __ballot_sync(0xffffffffu, found[i] != 0);
-        const int n = __popc(f);
-        if (cta < 0 && want < n) {
-          for (; want > 0; --want) f &= f - 1;
-          cta = c0 + 32 * i + __ffs(f) - 1;
-        }
-        want -= n;
-      }
-    }
-  }
-  if (cta < 0) return;
-  rec += (long long)cta * p.groups * kSplitInts;
-  const int row = rec[0], n = rec[1] - cta;      // n pieces after the first
+  const int grp = blockIdx.x % p.groups;
+  const int4 rec = reinterpret_cast<const int4*>(p.ws + (long long)main_ctas * 2 * kPartialFloats)[blockIdx.x];
+  const int row = rec.x, n = rec.y - rec.z;      // n pieces after the first
   if (row < 0) return;
   const int part = threadIdx.x / 128, d = (threadIdx.x % 128) * 4;
   const int h = WIDE ? blockIdx.y : blockIdx.y * 4 + part;
@@ -1323,7 +1304,7 @@ __global__ void __launch_bounds__(kJoinThreads, WIDE ? 2 : 3) latent_join_kernel
   if (head >= p.H) return;                       // WIDE: the whole block
   const long long step = (long long)p.groups * 2 * kPartialFloats;
   // the first piece lies in slot 1 of its CTA, the later ones in slot 0 of theirs
-  const float* rest = p.ws + ((long long)cta * p.groups + grp) * 2 * kPartialFloats + step;
+  const float* rest = p.ws + ((long long)rec.z * p.groups + grp) * 2 * kPartialFloats + step;
   const float* first = rest - step + kPartialFloats;
   float top = -CUDART_INF_F, total = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1412,15 +1393,14 @@ cudaError_t launch_t(LatentAttnParams p, int sms, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, latent_attention_kernel<KV>, p);
   if (e != cudaSuccess) return e;
-  // a slice cuts at most one row at its end: at most `cut` rows a head group
-  const int cut = p.rows < p.ctas ? p.rows : p.ctas, heads = p.H < kAttnHeads ? p.H : kAttnHeads;
-  // the wide join where a row may be in 16 pieces or more (one row of 131,072
-  // tokens, 128 heads: the call takes 72 us with it and 78 without; one row of
-  // 512 selected tokens, 8 pieces: 13.2 with it and 12.2 without)
-  const long long units = p.idx ? (p.k + kUnit - 1) / kUnit : p.W;
-  const bool wide = cut * p.groups <= 16 && min((long long)p.ctas, units * p.rows) >= 16LL * p.rows;
+  const int records = p.rows < p.ctas ? p.rows : p.ctas, heads = p.H < kAttnHeads ? p.H : kAttnHeads;
+  // The wide join, a block per head, while that is no more than five blocks an
+  // SM.  fp8 calls of 64 heads over 2,048 tokens, wide and not: 2 rows 15.1 and
+  // 22.8 us, 8 rows 17.6 and 20.4, 16 rows (1,024 blocks) 25.1 and 24.1, 48
+  // rows 50.2 and 40.9; one row of 131,072 bf16 tokens and 128 heads 58 and 77.
+  const bool wide = (long long)records * p.groups * heads <= 5LL * sms;
   cudaLaunchConfig_t join = cfg;
-  join.gridDim = dim3((wide ? cut : p.ctas) * p.groups, wide ? heads : (heads + 3) / 4);
+  join.gridDim = dim3(records * p.groups, wide ? heads : (heads + 3) / 4);
   join.blockDim = dim3(kJoinThreads);
   join.dynamicSmemBytes = 0;
   const int main_ctas = p.ctas * p.groups;
