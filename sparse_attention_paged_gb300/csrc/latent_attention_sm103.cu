@@ -39,7 +39,8 @@
 // product of the next tile takes them in the same order as they arrive.  P
 // lies where the rotated part was, which only the score product reads.
 //
-// Persistent: the call's 64-token units (per head group of 64) are cut into
+// Persistent: the call's 128-token units (per head group of 64; 64-token where
+// a few short rows have no more than one for each CTA) are cut into
 // equal slices, one per CTA, rows in order.  A row that a slice cuts leaves
 // unnormalised partial sums in the workspace, and a second kernel joins
 // them, so one long row or a few short ones spread over every SM, and a
@@ -83,8 +84,10 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kUnit = 64;                       // tokens per unit of the split
-constexpr int kTile = 128;                      // tokens per tile
+constexpr int kTileShift = 7, kTile = 1 << kTileShift;  // tokens per tile, and per unit of the split
+// Few rows that have no more than half tiles enough for every CTA are cut
+// into those: one row of 512 tokens then runs on eight CTAs.
+constexpr int kFewRows = 32;
 constexpr int kParts = 4;                       // latent parts of 128 values; the rotated part follows
 constexpr int kBlockBytes = kTile * 128;        // 64 values of a tile's tokens
 constexpr int kPartBytes = 2 * kBlockBytes;
@@ -123,7 +126,7 @@ struct Misc {
   uint64_t look_full[kRing], look_empty[kRing], scale_full[kRing];
   uint64_t done;
   uint32_t tmem;
-  int start_row, start_unit, nzero;
+  int start_row, start_unit, nzero, shift;
   int begin, end, total, ctas; // the slice's units, the call's units, the CTAs that have one
   int scan[kAttnThreads / 32];
   alignas(16) uint2 ratio[kRing][kTile];  // fp8: each part's scale over s(t), fp16
@@ -307,29 +310,29 @@ __device__ __forceinline__ int row_entries(const LatentAttnParams& p, int row, i
   return p.idx ? min(L, p.k) : L;
 }
 
+// Units of 2^shift tokens; entries >= 0.
+__device__ __forceinline__ int units_of(int entries, int shift) { return ((entries - 1) >> shift) + 1; }
+
 __device__ __forceinline__ int row_units(const LatentAttnParams& p, int row) {
   int len;
-  return (row_entries(p, row, &len) + kUnit - 1) / kUnit;
+  return units_of(row_entries(p, row, &len), kTileShift);
 }
 
 // Walks the tiles of a CTA's slice, row by row; rows without units are passed.
-// A tile is up to two units of one row.
+// A tile is a unit of one row: kTile tokens or half of that.
 struct TileWalk {
-  int row, u, n, len, left, piece;
+  int row, u, n, len, left, piece, shift = kTileShift;
   bool first;
-  __device__ __forceinline__ int units() const { return (n + kUnit - 1) / kUnit; }
-  __device__ __forceinline__ int count() const { return min(2, min(left, units() - u)); }
-  __device__ __forceinline__ int tokens() const { return min(n - u * kUnit, count() * kUnit); }
-  __device__ __forceinline__ bool last() const { return left == count() || u + count() == units(); }
+  __device__ __forceinline__ int units() const { return units_of(n, shift); }
+  __device__ __forceinline__ int tokens() const { return min(n - (u << shift), 1 << shift); }
+  __device__ __forceinline__ bool last() const { return left == 1 || u + 1 == units(); }
   __device__ __forceinline__ void start(const LatentAttnParams& p, int row0, int unit0, int units) {
     row = row0, u = unit0, left = units, piece = 0, first = true, n = 0, len = 0;
     if (left > 0) n = row_entries(p, row, &len);
   }
   __device__ __forceinline__ void step(const LatentAttnParams& p) {
-    const int c = count();
-    left -= c;
-    if (left <= 0) return;
-    u += c;
+    if (--left <= 0) return;
+    ++u;
     first = false;
     if (u < units()) return;
     do {
@@ -610,9 +613,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       for (int h = first; p.lse && h < heads; h += step)
         p.lse[(long long)row * p.H + head0 + h] = bad ? CUDART_NAN_F : -CUDART_INF_F;
     };
-    if (p.rows <= 32) {
+    if (p.rows <= kFewRows) {
       // few rows: every warp scans them for itself
-      const int mine = lane < p.rows ? row_units(p, lane) : 0;
+      int len;
+      const int entries = lane < p.rows ? row_entries(p, lane, &len) : 0;
+      // (the bound keeps the sum from wrapping)
+      const uint32_t halves = __reduce_add_sync(0xffffffffu, (uint32_t)min(units_of(entries, kTileShift - 1), 1 << 20));
+      if (halves <= (uint32_t)p.ctas) walk.shift = kTileShift - 1;
+      const int mine = units_of(entries, walk.shift);
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -684,7 +692,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       }
     }
     if (tid == 0) {
-      m->begin = begin, m->end = end, m->total = total, m->ctas = ctas;
+      m->begin = begin, m->end = end, m->total = total, m->ctas = ctas, m->shift = walk.shift;
       if (!records_by_row(p))
         reinterpret_cast<int4*>(p.ws + (long long)gridDim.x * 2 * kPartialFloats)[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
@@ -865,7 +873,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     for (int it = 0; walk.left > 0; ++it) {
       if (it % kLookWarps == slot) {
         const int n = walk.tokens();
-        const int flags = (walk.first ? kFirst : 0) | (walk.last() ? kLast : 0) | (walk.left == walk.count() ? kEnd : 0);
+        const int flags = (walk.first ? kFirst : 0) | (walk.last() ? kLast : 0) | (walk.left == 1 ? kEnd : 0);
         int tok[4];
         bool bad = false;
 #pragma unroll
@@ -873,7 +881,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           const int j = i * 32 + lane;
           tok[i] = -1;                             // first the position
           if (j < n) {
-            const int e = walk.u * kUnit + j;
+            const int e = (walk.u << walk.shift) + j;
             tok[i] = p.idx ? __ldg(p.idx + walk.row * p.idx_stride + e) : e;
           }
           if (tok[i] >= walk.len) tok[i] = -1;
@@ -945,7 +953,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
           // may give up.
           for (int n = 0; n < 500 && !mbar_test_wait(&m->full[0], (it - 1) & 1); ++n) __nanosleep(40);
           if (p.idx == nullptr) {
-            // whole pages: the two units' first tokens
+            // whole pages: the first tokens of both
             const int t0 = __shfl_sync(0xffffffffu, tok[0], 0), t1 = __shfl_sync(0xffffffffu, tok[2], 0);
             const int t = lane == 0 ? t0 : lane == 1 ? t1 : -1;
             if (t >= 0)
@@ -1253,6 +1261,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
     }
     if (more) {
       // a wait ran out: the rows and parts from this one on are NaN
+      walk.shift = m->shift;
       walk.start(p, m->start_row, m->start_unit, m->end - m->begin);
       for (uint32_t i = 0; walk.left > 0; walk.step(p)) {
         if (!walk.first) continue;

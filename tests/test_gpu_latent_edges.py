@@ -176,3 +176,20 @@ def test_captured_store_attention_load(kv):
             assert torch.equal(a, b)
         if kv == lib.KV_BF16:
             assert torch.equal(back, torch.cat([lat, rope], -1))
+
+
+@pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("rows,length", [(19, 512), (20, 512), (32, 257), (33, 64), (40, 129), (160, 100), (3, 3201)])
+def test_rows_and_lengths_around_the_split(kv, rows, length):
+    """Half tiles or whole ones, records by row or by CTA, joins of both kinds."""
+    lens = [length + (r % 3) - 1 for r in range(rows)]
+    lens[rows // 2] = 0
+    Case(lens, 5, kv, seed=rows + length).run().check()
+
+
+@pytest.mark.parametrize("kv", KVS)
+def test_joined_rows_do_not_keep_an_earlier_calls_records(kv):
+    """The same workspace for calls whose rows are cut, whole and empty in turn."""
+    work = torch.full((lib.dsa_latent_attention_workspace(),), math.nan, device="cuda")
+    for lens in ([4000, 4000], [60, 0], [0, 9000], [130] * 30, [0] * 3 + [2000], [70] * 200, [500, 1]):
+        Case(lens, 7, kv, seed=len(lens)).run(workspace=work).check()
