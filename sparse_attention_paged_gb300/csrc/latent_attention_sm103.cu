@@ -48,20 +48,24 @@
 //
 // Warps: 0-7 softmax and output, 8 MMA issue, 9-11 token lookup, 12-19
 // loaders.  The lookup warps go through selection list and block table up to
-// three tiles ahead and ask L2 for the tokens' bytes, which keeps HBM busy
-// whatever the tile buffer does.  The loaders copy (bf16) or convert (fp8) 16
+// three tiles ahead and ask L2 for a tile's bytes when the tile before it
+// arrives, which keeps HBM busy whatever the tile buffer does (152 rows of
+// 8,192 fp8 tokens 264 us, 335 without).  The loaders copy (bf16) or convert (fp8) 16
 // bytes at a time; masked tokens are not read, their rows are zeros.
 //
 // Measured (whole call, 64 heads where not said otherwise): 64 rows of 2,048
-// selected tokens each, bf16, 65.5 us; 64 rows of 512 to 32,768 tokens, fp8,
-// 145 us; one row of 131,072 bf16 tokens and 128 heads 72 us (151 MB, 2.1
-// TB/s); 1,024 fp8 prefill rows of 2,048 selected tokens 497 us (590
-// TFLOP/s); one row of 512 and 16 heads 12 us.  What bounds it: a tile's chain of loads, scores,
-// softmax and values, 7,300 to 8,800 cycles per 128 fp8 tokens, of which
-// shared memory is busy for 4,400 (both products' operands and the loaders'
-// stores) and the softmax for 1,450 to 2,100.  Tiles of 64 tokens in two
-// buffers overlapped more but ran their products at half rate: the prefill
-// took 1,316 us, the ragged rows 366.
+// selected tokens each, bf16, 48 us; 64 rows of 512 to 32,768 tokens, fp8, 137
+// us; one row of 131,072 bf16 tokens and 128 heads 58 us; 1,024 fp8 prefill
+// rows of 2,048 selected tokens 480 us (610 TFLOP/s); 152 rows of 8,192 tokens
+// 264 us in either type (5.5 and 3.1 TB/s); one row of 512 and 16 heads 11 us.
+// What bounds it: a tile's chain.  Value product (1,536 cycles of operand
+// reads), the next tile's scores (1,728) and softmax (1,150 to 1,600) follow
+// one another, since only one tile fits: 5,750 cycles a bf16 tile, 6,000 to
+// 7,000 an fp8 tile, whose conversion stores share shared memory with the
+// products.  Few rows: 6 us from the launch to the first tokens' addresses
+// (lengths, list and table, one DRAM trip each), the first tile, the join.
+// Tiles of 64 tokens in two buffers overlapped more but ran their products at
+// half rate: the prefill took 1,316 us, the ragged rows 366.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
