@@ -13,7 +13,10 @@
 // four loads are in flight and the token's cosines and sines are read once
 // for them.  Both values of a pair lie in one lane: where the half layout
 // pairs values that are rot/2 apart, a lane takes four from either end.
-// Measured: 4,096 tokens of 64 + 1 heads of 128 bf16 values 31.8 us (4.3 TB/s
+// Values are read evict-first, as nothing else reads them.  Writing them so as
+// well takes another 5 to 10% off this kernel's time and adds it to that of
+// the next one, which reads them.
+// Measured: 4,096 tokens of 64 + 1 heads of 128 bf16 values 31 us (4.4 TB/s
 // of 136 MB), with 61% of the issue slots taken, so that HBM and instructions
 // bound it together; 1,337 tokens of 24 + 8 heads of 192 fp16 values 7.6 us
 // (4.3 TB/s) in a graph; 64 tokens 2.6 us, one DRAM round trip and the launch.
@@ -30,7 +33,9 @@ namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Blocks of 128: 4,096 tokens of 65 heads 31.5 us for 32.2 with 256 (a wave's
+// end is cut finer).
+constexpr int kThreads = 128;
 constexpr int kChunk = 8;  // values a lane holds
 
 // Two floats in one 64-bit register pair: half the instructions of the sums
@@ -70,14 +75,14 @@ __device__ __forceinline__ float sum2(F2 a) {
 template <typename T>
 struct Raw4 {
   uint2 r;
-  __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void load(const T* p) { r = __ldcs(reinterpret_cast<const uint2*>(p)); }
   __device__ __forceinline__ void zero() { r = make_uint2(0u, 0u); }
 };
 
 template <>
 struct Raw4<float> {
   float4 r;
-  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void load(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
   __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
 };
 
@@ -132,9 +137,10 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // LANES: lanes per row (8 * LANES >= dim; FULL: equal); HEADS: heads a group
-// takes; INTER: interleaved pairs.  The loads stay packed until their head's turn, so that three blocks fit an SM.
+// takes; INTER: interleaved pairs.  The loads stay packed until their head's turn, so that
+// 32 warps fit an SM (16-bit types).
 template <typename T, int LANES, int HEADS, bool INTER, bool FULL>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 8) norm_rope_kernel(const NormRopeParams p) {
   const long long unit = ((long long)blockIdx.x * kThreads + threadIdx.x) / LANES;
   const int c = threadIdx.x % LANES;
   const int units_q = (p.heads[0] + HEADS - 1) / HEADS;
