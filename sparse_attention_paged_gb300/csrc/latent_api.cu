@@ -90,7 +90,7 @@ int dsa_qk_norm_rope(const void* q, long long q_token_stride, long long q_head_s
     return DSA_ERR_MISALIGNED;
   if (T == 0 || Hq + (long long)Hk == 0) return DSA_OK;
   // at most one unit of 32 lanes per head: the grid stays below 2^31 blocks
-  if ((double)T * ((double)Hq + Hk) >= 1.6e10) return DSA_ERR_UNSUPPORTED;
+  if ((double)T * ((double)Hq + Hk) >= 8e9) return DSA_ERR_UNSUPPORTED;
   dsa::NormRopeParams p = {};
   p.x[0] = q, p.x[1] = k, p.y[0] = q_out, p.y[1] = k_out;
   p.xt[0] = q_token_stride, p.xt[1] = k_token_stride;
