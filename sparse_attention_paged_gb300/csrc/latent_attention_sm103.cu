@@ -953,9 +953,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
         if (it > 0) {
           // The first tile is loaded at once; the later ones wait for its place.
           // Asked for when the tile before has begun to arrive: earlier costs
-          // 2 to 5% (the place in L2).  Late would only cost time, so the wait
-          // may give up.
-          for (int n = 0; n < 500 && !mbar_test_wait(&m->full[0], (it - 1) & 1); ++n) __nanosleep(40);
+          // 2 to 5% (the place in L2).  Late, or after a whole phase that was
+          // missed, it would hold up the next tiles' lookup: the wait is short.
+          for (int n = 0; n < 100 && !mbar_test_wait(&m->full[0], (it - 1) & 1); ++n) __nanosleep(40);
           if (p.idx == nullptr) {
             // whole pages: the first tokens of both
             const int t0 = __shfl_sync(0xffffffffu, tok[0], 0), t1 = __shfl_sync(0xffffffffu, tok[2], 0);
