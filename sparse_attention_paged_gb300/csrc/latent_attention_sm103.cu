@@ -109,6 +109,8 @@ constexpr int kRegsLaunch = 96, kRegsSoftmax = 104, kRegsMisc = 72, kRegsLoad = 
 static_assert(kSoftmaxWarps * kRegsSoftmax + 4 * kRegsMisc + kLoadWarps * kRegsLoad <=
                   kAttnThreads / 32 * kRegsLaunch,
               "the roles' registers are those of the launch");
+static_assert(kSoftmaxWarps % 4 == 0 && kMmaWarp % 4 == 0 && kLoadWarp0 % 4 == 0 && kLoadWarps % 4 == 0,
+              "a register count holds for a warpgroup of four warps");
 // The reference (log2 units): a new one is set ref_below under the largest
 // weight, and holds until a weight is ref_limit above it.
 constexpr float ref_below(int kv) { return kv == DSA_KV_BF16 ? 0.f : 6.f; }
@@ -883,182 +885,185 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
       }
     }
     cp_async_wait_all();
-  } else if (warp >= kLookWarp0) {
-    // ---- token lookup ----------------------------------------------------------
+  } else if (warp >= kMmaWarp) {
+    // warps 8-11 are one warpgroup, and all of a warpgroup have to run the same
+    // setmaxnreg: before its roles part
     fewer_registers<kRegsMisc>();
-    // tile i by warp i % 3: list and block table to token, and L2 asked for it
-    const int slot = warp - kLookWarp0;
-    for (int it = 0; walk.left > 0; ++it) {
-      if (it % kLookWarps == slot) {
-        const int n = walk.tokens();
-        const int flags = (walk.first ? kFirst : 0) | (walk.last() ? kLast : 0) | (walk.left == 1 ? kEnd : 0);
-        int tok[4];
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = i * 32 + lane;
-          tok[i] = -1;                             // first the position
-          if (j < n) {
-            const int e = (walk.u << walk.shift) + j;
-            tok[i] = p.idx ? __ldg(p.idx + walk.row * p.idx_stride + e) : e;
-          }
-          if (tok[i] >= walk.len) tok[i] = -1;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (tok[i] < 0) {
-            tok[i] = -1;
-            continue;
-          }
-          const int page = __ldg(p.block_table + walk.row * p.bt_stride + tok[i] / kPage);
-          const bool in = page >= 0 && page < p.num_pages;
-          tok[i] = in ? page * kPage + tok[i] % kPage : -1;
-          bad |= !in;
-        }
-        if (it >= kRing) wait(&m->look_empty[slot], (it / kRing - 1) & 1);
-        const bool any_bad = __any_sync(0xffffffffu, bad);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t v = __ballot_sync(0xffffffffu, tok[i] >= 0);
-          if (wait.ok) {
-            m->token[slot][i * 32 + lane] = tok[i];
-            if (lane == 0) m->mask[slot][i] = v;
-          }
-        }
-        if (wait.ok && lane == 0) {
-          m->tile[slot] = make_int4(walk.row, n, flags | (any_bad ? kBad : 0), walk.piece);
-          if (walk.first) {
-            const bool begins = walk.u == 0, whole = begins && walk.left >= walk.units();
-            m->piece[walk.piece & 7] = make_int4(walk.row, (begins ? kBegins : 0) | (whole ? kWhole : 0), 0, 0);
-            if (begins) {
-              // where the row ends, should it go on in later CTAs
-              const long long last_unit = (long long)m->end - walk.left + walk.units() - 1;
-              record_split(p, walk.row, !whole, whole ? 0 : (int)(((last_unit + 1) * m->ctas - 1) / m->total));
-            }
-          }
-        }
-        if (any_bad && lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
-        __syncwarp();
-        if (wait.ok && lane == 0) mbar_arrive(&m->look_full[slot]);
-        if (kFp8) {
-          float4 sc[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = max(tok[i], 0);
-            sc[i] = __ldg(reinterpret_cast<const float4*>(p.cache + (long long)(t >> 6) * p.page_stride +
-                                                          kScaleOffsetFp8) + (t & 63));
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float most = fmaxf(fmaxf(fmaxf(sc[i].x, sc[i].y), fmaxf(sc[i].z, sc[i].w)), kSmallestScale);
-            const float inv = __frcp_rn(most);
-            const __half2 a = __floats2half2_rn(sc[i].x * inv, sc[i].y * inv);
-            const __half2 b = __floats2half2_rn(sc[i].z * inv, sc[i].w * inv);
-            const bool in = tok[i] >= 0;           // a masked token: zeros times zero
-            if (wait.ok) {
-              m->ratio[slot][i * 32 + lane] = make_uint2(in ? *reinterpret_cast<const uint32_t*>(&a) : 0u,
-                                                         in ? *reinterpret_cast<const uint32_t*>(&b) : 0u);
-              m->key_scale[slot][i * 32 + lane] = in ? most : 1.f;
-            }
-          }
-          __syncwarp();
-          if (wait.ok && lane == 0) mbar_arrive(&m->scale_full[slot]);
-        }
-        if (it > 0) {
-          // The first tile is loaded at once; the later ones wait for its place.
-          // Asked for when the tile before has begun to arrive: earlier costs
-          // 2 to 5% (the place in L2).  Late, or after a whole phase that was
-          // missed, it would hold up the next tiles' lookup: the wait is short.
-          for (int n = 0; n < 100 && !mbar_test_wait(&m->full[0], (it - 1) & 1); ++n) __nanosleep(40);
-          if (p.idx == nullptr) {
-            // whole pages: the first tokens of both
-            const int t0 = __shfl_sync(0xffffffffu, tok[0], 0), t1 = __shfl_sync(0xffffffffu, tok[2], 0);
-            const int t = lane == 0 ? t0 : lane == 1 ? t1 : -1;
-            if (t >= 0)
-              l2_prefetch_bulk(p.cache + (long long)(t >> 6) * p.page_stride,
-                               (uint32_t)(kFp8 ? kPageBytesFp8 : kPageBytesBf16));
-          } else {
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              const int t = i == 0 ? tok[0] : i == 1 ? tok[1] : i == 2 ? tok[2] : tok[3];
-              if (t < 0) continue;
-              const uint8_t* pg = p.cache + (long long)(t >> 6) * p.page_stride;
-              const int s = t & 63;
-              const uint8_t* row = pg + s * (kFp8 ? kLatent : kTokenBytesBf16);
-              l2_prefetch_bulk(row, kFp8 ? kLatent : kTokenBytesBf16);
-              if (kFp8) l2_prefetch(pg + kRopeOffsetFp8 + s * (kRope * 2));
-            }
-          }
-          if (walk.first)
-#pragma unroll 1
-            for (int h = lane; h < heads; h += 32) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                l2_prefetch(p.ql + walk.row * p.ql_row + (head0 + h) * p.ql_head + j * 64);
-              l2_prefetch(p.qr + walk.row * p.qr_row + (head0 + h) * p.qr_head);
-            }
-        }
-      }
-      walk.step(p);
-    }
-  } else if (warp == kMmaWarp) {
-    // ---- MMA issue -----------------------------------------------------------
-    fewer_registers<kRegsMisc>();
-    if (elect_one()) {
-      Waiter<false> wait{p.status, true};
-      if (walk.left > 0) wait(&m->qfirst, 0);
+    if (warp >= kLookWarp0) {
+      // ---- token lookup ----------------------------------------------------------
+      // tile i by warp i % 3: list and block table to token, and L2 asked for it
+      const int slot = warp - kLookWarp0;
       for (int it = 0; walk.left > 0; ++it) {
-        // eight MMAs to a step of these loops: all 68 in a row push the other
-        // roles out of the instruction cache, four leave the tensor pipe idle
-        uint64_t a_d = smem_desc_sw128(sbase, 1024), b_d = smem_desc_sw128(sbase + kOffQ, 1024);
+        if (it % kLookWarps == slot) {
+          const int n = walk.tokens();
+          const int flags = (walk.first ? kFirst : 0) | (walk.last() ? kLast : 0) | (walk.left == 1 ? kEnd : 0);
+          int tok[4];
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = i * 32 + lane;
+            tok[i] = -1;                             // first the position
+            if (j < n) {
+              const int e = (walk.u << walk.shift) + j;
+              tok[i] = p.idx ? __ldg(p.idx + walk.row * p.idx_stride + e) : e;
+            }
+            if (tok[i] >= walk.len) tok[i] = -1;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (tok[i] < 0) {
+              tok[i] = -1;
+              continue;
+            }
+            const int page = __ldg(p.block_table + walk.row * p.bt_stride + tok[i] / kPage);
+            const bool in = page >= 0 && page < p.num_pages;
+            tok[i] = in ? page * kPage + tok[i] % kPage : -1;
+            bad |= !in;
+          }
+          if (it >= kRing) wait(&m->look_empty[slot], (it / kRing - 1) & 1);
+          const bool any_bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v = __ballot_sync(0xffffffffu, tok[i] >= 0);
+            if (wait.ok) {
+              m->token[slot][i * 32 + lane] = tok[i];
+              if (lane == 0) m->mask[slot][i] = v;
+            }
+          }
+          if (wait.ok && lane == 0) {
+            m->tile[slot] = make_int4(walk.row, n, flags | (any_bad ? kBad : 0), walk.piece);
+            if (walk.first) {
+              const bool begins = walk.u == 0, whole = begins && walk.left >= walk.units();
+              m->piece[walk.piece & 7] = make_int4(walk.row, (begins ? kBegins : 0) | (whole ? kWhole : 0), 0, 0);
+              if (begins) {
+                // where the row ends, should it go on in later CTAs
+                const long long last_unit = (long long)m->end - walk.left + walk.units() - 1;
+                record_split(p, walk.row, !whole, whole ? 0 : (int)(((last_unit + 1) * m->ctas - 1) / m->total));
+              }
+            }
+          }
+          if (any_bad && lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
+          __syncwarp();
+          if (wait.ok && lane == 0) mbar_arrive(&m->look_full[slot]);
+          if (kFp8) {
+            float4 sc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = max(tok[i], 0);
+              sc[i] = __ldg(reinterpret_cast<const float4*>(p.cache + (long long)(t >> 6) * p.page_stride +
+                                                            kScaleOffsetFp8) + (t & 63));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float most = fmaxf(fmaxf(fmaxf(sc[i].x, sc[i].y), fmaxf(sc[i].z, sc[i].w)), kSmallestScale);
+              const float inv = __frcp_rn(most);
+              const __half2 a = __floats2half2_rn(sc[i].x * inv, sc[i].y * inv);
+              const __half2 b = __floats2half2_rn(sc[i].z * inv, sc[i].w * inv);
+              const bool in = tok[i] >= 0;           // a masked token: zeros times zero
+              if (wait.ok) {
+                m->ratio[slot][i * 32 + lane] = make_uint2(in ? *reinterpret_cast<const uint32_t*>(&a) : 0u,
+                                                           in ? *reinterpret_cast<const uint32_t*>(&b) : 0u);
+                m->key_scale[slot][i * 32 + lane] = in ? most : 1.f;
+              }
+            }
+            __syncwarp();
+            if (wait.ok && lane == 0) mbar_arrive(&m->scale_full[slot]);
+          }
+          if (it > 0) {
+            // The first tile is loaded at once; the later ones wait for its place.
+            // Asked for when the tile before has begun to arrive: earlier costs
+            // 2 to 5% (the place in L2).  Late, or after a whole phase that was
+            // missed, it would hold up the next tiles' lookup: the wait is short.
+            for (int n = 0; n < 100 && !mbar_test_wait(&m->full[0], (it - 1) & 1); ++n) __nanosleep(40);
+            if (p.idx == nullptr) {
+              // whole pages: the first tokens of both
+              const int t0 = __shfl_sync(0xffffffffu, tok[0], 0), t1 = __shfl_sync(0xffffffffu, tok[2], 0);
+              const int t = lane == 0 ? t0 : lane == 1 ? t1 : -1;
+              if (t >= 0)
+                l2_prefetch_bulk(p.cache + (long long)(t >> 6) * p.page_stride,
+                                 (uint32_t)(kFp8 ? kPageBytesFp8 : kPageBytesBf16));
+            } else {
 #pragma unroll 1
-        for (int part = 0; part < kParts; ++part) {
-          wait(&m->full[part], it & 1);
-          tc_fence_after();
-          if (wait.ok)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16(tmem + kTmemS, a_d + (((k / 4) * kBlockBytes + (k % 4) * 32) >> 4),
-                      b_d + (((k / 4) * kQBlockBytes + (k % 4) * 32) >> 4), idesc_s(KV), k > 0 || part > 0);
-          a_d += kPartBytes >> 4;
-          b_d += 2 * kQBlockBytes >> 4;
-        }
-        wait(&m->full[kParts], it & 1);
-        tc_fence_after();
-        if (wait.ok)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16(tmem + (kFp8 ? kTmemR : kTmemS), a_d + (k * 32 >> 4), b_d + (k * 32 >> 4),
-                    kFp8 ? kIdescRope : idesc_s(KV), !kFp8 || k > 0);
-        if (wait.ok) mma_commit(&m->sfull);
-        const int steps = (walk.tokens() + 15) / 16;
-        const uint32_t keep = walk.first ? 0u : 1u;
-        wait(&m->pfull, it & 1);
-        if (walk.first && walk.piece > 0) wait(&m->ofree, (walk.piece - 1) & 1);
-        tc_fence_after();
-        if (wait.ok) {
-          a_d = smem_desc_mn_sw128(sbase, kBlockBytes, 1024);
-          b_d = smem_desc_mn_sw128(sbase + kOffP, kBlockBytes, 1024);
+              for (int i = 0; i < 4; ++i) {
+                const int t = i == 0 ? tok[0] : i == 1 ? tok[1] : i == 2 ? tok[2] : tok[3];
+                if (t < 0) continue;
+                const uint8_t* pg = p.cache + (long long)(t >> 6) * p.page_stride;
+                const int s = t & 63;
+                const uint8_t* row = pg + s * (kFp8 ? kLatent : kTokenBytesBf16);
+                l2_prefetch_bulk(row, kFp8 ? kLatent : kTokenBytesBf16);
+                if (kFp8) l2_prefetch(pg + kRopeOffsetFp8 + s * (kRope * 2));
+              }
+            }
+            if (walk.first)
 #pragma unroll 1
-          for (int part = 0; part < kParts; ++part) {
+              for (int h = lane; h < heads; h += 32) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              if (k < steps)
-                mma_f16(tmem + part * kAttnHeads, a_d + (k * 2048 >> 4), b_d + (k * 2048 >> 4), idesc_o(KV),
-                        k > 0 ? 1u : keep);
-            mma_commit(&m->empty[part]);
-            a_d += kPartBytes >> 4;
+                for (int j = 0; j < 8; ++j)
+                  l2_prefetch(p.ql + walk.row * p.ql_row + (head0 + h) * p.ql_head + j * 64);
+                l2_prefetch(p.qr + walk.row * p.qr_row + (head0 + h) * p.qr_head);
+              }
           }
         }
         walk.step(p);
       }
-      if (!wait.ok) {
-        // what was issued still runs: wait for it before TMEM is given back
-        mma_commit(&m->done);
-        mbar_wait_bounded(&m->done, 0, kWaitLimit);
+    } else {
+      // ---- MMA issue -----------------------------------------------------------
+      if (elect_one()) {
+        Waiter<false> wait{p.status, true};
+        if (walk.left > 0) wait(&m->qfirst, 0);
+        for (int it = 0; walk.left > 0; ++it) {
+          // eight MMAs to a step of these loops: all 68 in a row push the other
+          // roles out of the instruction cache, four leave the tensor pipe idle
+          uint64_t a_d = smem_desc_sw128(sbase, 1024), b_d = smem_desc_sw128(sbase + kOffQ, 1024);
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+            wait(&m->full[part], it & 1);
+            tc_fence_after();
+            if (wait.ok)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_f16(tmem + kTmemS, a_d + (((k / 4) * kBlockBytes + (k % 4) * 32) >> 4),
+                        b_d + (((k / 4) * kQBlockBytes + (k % 4) * 32) >> 4), idesc_s(KV), k > 0 || part > 0);
+            a_d += kPartBytes >> 4;
+            b_d += 2 * kQBlockBytes >> 4;
+          }
+          wait(&m->full[kParts], it & 1);
+          tc_fence_after();
+          if (wait.ok)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16(tmem + (kFp8 ? kTmemR : kTmemS), a_d + (k * 32 >> 4), b_d + (k * 32 >> 4),
+                      kFp8 ? kIdescRope : idesc_s(KV), !kFp8 || k > 0);
+          if (wait.ok) mma_commit(&m->sfull);
+          const int steps = (walk.tokens() + 15) / 16;
+          const uint32_t keep = walk.first ? 0u : 1u;
+          wait(&m->pfull, it & 1);
+          if (walk.first && walk.piece > 0) wait(&m->ofree, (walk.piece - 1) & 1);
+          tc_fence_after();
+          if (wait.ok) {
+            a_d = smem_desc_mn_sw128(sbase, kBlockBytes, 1024);
+            b_d = smem_desc_mn_sw128(sbase + kOffP, kBlockBytes, 1024);
+#pragma unroll 1
+            for (int part = 0; part < kParts; ++part) {
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                if (k < steps)
+                  mma_f16(tmem + part * kAttnHeads, a_d + (k * 2048 >> 4), b_d + (k * 2048 >> 4), idesc_o(KV),
+                          k > 0 ? 1u : keep);
+              mma_commit(&m->empty[part]);
+              a_d += kPartBytes >> 4;
+            }
+          }
+          walk.step(p);
+        }
+        if (!wait.ok) {
+          // what was issued still runs: wait for it before TMEM is given back
+          mma_commit(&m->done);
+          mbar_wait_bounded(&m->done, 0, kWaitLimit);
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ---- softmax and output --------------------------------------------------
     more_registers<kRegsSoftmax>();
