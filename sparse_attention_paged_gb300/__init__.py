@@ -55,6 +55,39 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+class _AllocateOn:
+    """Allocations for a call on `stream` (None: torch's current one; 0: the default stream).
+
+    Within, torch allocates on that stream: the allocator then takes no memory that other streams
+    may still be using, and once the call has dropped its own it goes to later work of that stream
+    only.  ``returned`` marks an output, which leaves for a program on the current stream.
+    """
+
+    def __init__(self, stream, like):
+        self.scope = self.current = None
+        if stream is not None and like.is_cuda:
+            import torch
+            if isinstance(stream, int):
+                stream = (torch.cuda.ExternalStream(stream, device=like.device) if stream
+                          else torch.cuda.default_stream(like.device))
+            self.current = torch.cuda.current_stream(like.device)
+            self.scope = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.scope is not None:
+            self.scope.__enter__()
+        return self
+
+    def __exit__(self, *error):
+        if self.scope is not None:
+            self.scope.__exit__(*error)
+
+    def returned(self, x):
+        if self.current is not None:
+            x.record_stream(self.current)
+        return x
+
+
 def dsa_status_string(status: int) -> str:
     return _native.load().dsa_status_string(int(status)).decode()
 
@@ -163,7 +196,8 @@ def indexer_logits(kind: str, q, w, kcache, kscale, page_stride_bytes, num_pages
     import torch
     rows = int(seqlens.shape[0])
     if out is None:
-        out = torch.empty((rows, W * PAGE), dtype=torch.float32, device=seqlens.device)
+        with _AllocateOn(stream, seqlens) as on:
+            out = on.returned(seqlens.new_empty((rows, W * PAGE), dtype=torch.float32))
     fn = dsa_indexer_logits_decode if kind == "decode" else dsa_indexer_logits_prefill
     st = fn(q, w, kcache, kscale, page_stride_bytes, num_pages, kv_dtype, block_table,
             bt_stride, seqlens, rows, H, D, PAGE, W, out, out.stride(0), dev_status, stream)
@@ -251,6 +285,11 @@ def _tensor_calls():
     return _calls
 
 
+# The tensor-level calls run on torch's current stream unless `stream` names another (a
+# torch.cuda.Stream, or a cudaStream_t as an int).  What they allocate belongs to that stream; the
+# order between it and the streams of the tensors that are given, and those tensors' lives, are
+# the caller's to keep.
+
 def _stream_address(stream):
     return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
@@ -275,10 +314,12 @@ def qk_norm_rope(q, k, positions=None, table=None, *, rot_dims=None, rot_offset=
     """
     if rot_dims is not None and table is not None and rot_dims != table.shape[1]:
         raise ValueError("rot_dims: the table's width")
-    if q_out is None:
-        q_out = q.new_empty(q.shape)
-    if k_out is None and k is not None:
-        k_out = k.new_empty(k.shape)
+    if q_out is None or (k_out is None and k is not None):
+        with _AllocateOn(stream, q) as on:
+            if q_out is None:
+                q_out = on.returned(q.new_empty(q.shape))
+            if k_out is None and k is not None:
+                k_out = on.returned(k.new_empty(k.shape))
     status = (_calls or _tensor_calls()).qk_norm_rope(
         q, k, positions, table, rot_offset, interleaved, norm, q_weight, k_weight, q_bias, k_bias,
         eps, q_out, k_out, dev_status, _stream_address(stream))
@@ -311,7 +352,8 @@ def latent_load(cache, kv_dtype, block_table, cu_rows, n, *, starts=None, out=No
     """
     if out is None:
         import torch
-        out = torch.empty((n, LATENT + ROPE), dtype=torch.bfloat16, device=cache.device)
+        with _AllocateOn(stream, cache) as on:
+            out = on.returned(cache.new_empty((n, LATENT + ROPE), dtype=torch.bfloat16))
     status = (_calls or _tensor_calls()).latent_load(
         cache, kv_dtype, block_table, cu_rows, n, starts, out, dev_status, _stream_address(stream))
     if status:
@@ -327,12 +369,14 @@ def latent_attention(q_latent, q_rope, cache, kv_dtype, block_table, seqlens, sc
     as the top-k calls write them).  Returns out, bf16 [rows, H, 512]; ``lse`` (fp32 [rows, H])
     is written when given.  Raises DsaError on a host-side error.
     """
-    if out is None:
-        out = q_latent.new_empty(q_latent.shape)
-    if workspace is None:
+    if out is None or workspace is None:
         import torch
-        workspace = torch.empty(max(dsa_latent_attention_workspace(), 0), dtype=torch.float32,
-                                device=q_latent.device)
+        with _AllocateOn(stream, q_latent) as on:
+            if out is None:
+                out = on.returned(q_latent.new_empty(q_latent.shape))
+            if workspace is None:
+                workspace = q_latent.new_empty(max(dsa_latent_attention_workspace(), 0),
+                                               dtype=torch.float32)
     status = (_calls or _tensor_calls()).latent_attention(
         q_latent, q_rope, cache, kv_dtype, block_table, seqlens, scale, idx, out, lse, workspace,
         dev_status, _stream_address(stream))
