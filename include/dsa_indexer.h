@@ -407,7 +407,9 @@ int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_page
  *             all rows share row 0).
  *   workspace fp32, at least dsa_latent_attention_workspace() floats for the
  *             current device, 16-byte aligned; calls that may overlap need
- *             one each.
+ *             one each.  What another call or kernel writes to it meanwhile
+ *             leaves the results undefined, without an access out of range;
+ *             where it is noticed the status is DSA_ERR_INVALID_ARG.
  * The softmax and all sums are fp32; the weights of the value product are
  * rounded to bf16.  With an fp8 cache latent queries, weights and tokens are
  * fp16 under scales of their own (a power of two per head, the largest of a

@@ -1330,7 +1330,11 @@ __global__ void __launch_bounds__(kJoinThreads, WIDE ? 2 : 3) latent_join_kernel
   const int grp = blockIdx.x % p.groups;
   const int4 rec = reinterpret_cast<const int4*>(p.ws + (long long)main_ctas * 2 * kPartialFloats)[blockIdx.x];
   const int row = rec.x, n = rec.y - rec.z;      // n pieces after the first
-  if (row < 0) return;
+  if (row == -1) return;
+  if (!split_record_ok(row, rec.y, rec.z, p.rows, p.ctas)) {  // another call wrote to this workspace
+    if (threadIdx.x == 0) raise_status(p.status, DSA_ERR_INVALID_ARG);
+    return;
+  }
   const int part = threadIdx.x / 128, d = (threadIdx.x % 128) * 4;
   const int h = WIDE ? blockIdx.y : blockIdx.y * 4 + part;
   const int head = grp * kAttnHeads + h;

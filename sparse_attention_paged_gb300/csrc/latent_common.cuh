@@ -102,4 +102,10 @@ constexpr int kPartialFloats = kAttnHeads * kLatent + 2 * kAttnHeads;
 constexpr int kSplitInts = 4;
 constexpr long long latent_ws_floats(long long sms) { return sms * (2LL * kPartialFloats + kSplitInts); }
 
+// A split record {row, CTA with its last unit, CTA with its first, 0} that names rows and CTAs of
+// this call.  The join takes addresses from it, and the workspace is the caller's memory.
+__host__ __device__ constexpr bool split_record_ok(int row, int last, int first, int rows, int ctas) {
+  return row >= 0 && row < rows && first >= 0 && first <= last && last < ctas;
+}
+
 }  // namespace dsa
