@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -147,14 +148,32 @@ Table table_of(const at::Tensor* t, int64_t rows) {
   return Table{static_cast<const int*>(ptr(t)), t->stride(0), W};
 }
 
+// Every CUDA tensor among the arguments is on the current device, whose
+// streams and SM count the library uses: an address of another device would
+// fault in a kernel.  (Tensors of the host are refused by `launch`.)
+void one_device(PyObject* const* a, Py_ssize_t n) {
+  int first = -1;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    // numbers and None first: the general test of a type takes 40 ns
+    if (a[i] == Py_None || PyLong_Check(a[i]) || PyFloat_Check(a[i]) || !THPVariable_Check(a[i])) continue;
+    const at::Device d = THPVariable_Unpack(a[i]).device();
+    if (!d.is_cuda()) continue;
+    need(first < 0 || d.index() == first, "the tensors are on more than one CUDA device");
+    first = d.index();
+  }
+  need(first < 0 || first == c10::cuda::current_device(),
+       "the tensors are not on the current CUDA device (torch.cuda.set_device, or `with torch.cuda.device`)");
+}
+
 template <typename F>
-PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
+PyObject* guarded(PyObject* const* a, Py_ssize_t n, Py_ssize_t want, F f) {
   if (n != want) {
     PyErr_Format(PyExc_TypeError, "%zd arguments expected, %zd given", want, n);
     return nullptr;
   }
   try {
     all_on_gpu = true;
+    one_device(a, n);
     return PyLong_FromLong(f());
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
@@ -167,7 +186,7 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
 // q, k, positions, table, rot_offset, interleaved, norm, q_weight, k_weight,
 // q_bias, k_bias, eps, q_out, k_out, dev_status, stream
 PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 16, [&] {
+  return guarded(a, n, 16, [&] {
     const at::Tensor *q = tensor(a[0], "q"), *k = tensor(a[1], "k");
     const at::Tensor *qo = tensor(a[12], "q_out"), *ko = tensor(a[13], "k_out");
     need(q && q->dim() == 3, "q: [T, Hq, D] expected");
@@ -207,7 +226,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // latent, rope, slot_mapping, cache, kv_dtype, norm_weight, eps, positions,
 // rope_table, interleaved, dev_status, stream
 PyObject* latent_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 12, [&] {
+  return guarded(a, n, 12, [&] {
     long long ls, rs;
     const at::Tensor* latent = tensor(a[0], "latent");
     void* c = rows_bf16(latent, "latent: bfloat16 [n, 512], rows contiguous", -1, 512, &ls);
@@ -233,7 +252,7 @@ PyObject* latent_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // cache, kv_dtype, block_table, cu_rows, n, starts, out, dev_status, stream
 PyObject* latent_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 9, [&] {
+  return guarded(a, n, 9, [&] {
     const at::Tensor* cu = tensor(a[3], "cu_rows");
     const int* cu_rows = ints(cu, "cu_rows", -1);
     need(cu_rows && cu->size(0) >= 1, "cu_rows: int32 [requests + 1] expected");
@@ -252,7 +271,7 @@ PyObject* latent_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // q_latent, q_rope, cache, kv_dtype, block_table, seqlens, scale, idx, out,
 // lse, workspace, dev_status, stream
 PyObject* latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 13, [&] {
+  return guarded(a, n, 13, [&] {
     const at::Tensor *ql = tensor(a[0], "q_latent"), *qr = tensor(a[1], "q_rope"), *idx = tensor(a[7], "idx");
     const at::Tensor *out = tensor(a[8], "out"), *ws = tensor(a[10], "workspace");
     need(ql && ql->scalar_type() == at::kBFloat16 && ql->dim() == 3 && ql->size(2) == 512 && ql->stride(2) == 1,
