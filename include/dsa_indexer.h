@@ -395,7 +395,7 @@ int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_page
  * with c[t] the 512 latent values and k[t] the rotated part of position t of
  * the row's block-table row.  The visible positions are t < seqlens[r]
  * (idx NULL), or those of the row's selection list: entries idx[r * idx_stride
- * + j], j < min(k, seqlens[r]), that are not negative and below seqlens[r]
+ * + j], j < min(k, seqlens[r]), k >= 1, that are not negative and below seqlens[r]
  * (the lists that the top-k calls write: valid entries first, then -1; an
  * entry that is repeated counts as often).  A row without a visible position
  * gives zeros and lse = -inf.

@@ -366,7 +366,8 @@ def latent_attention(q_latent, q_rope, cache, kv_dtype, block_table, seqlens, sc
     """Attention of [rows, H] query heads over the latent cache, in the absorbed form.
 
     Over every position below ``seqlens``, or over the selection lists ``idx`` (int32 [rows, k],
-    as the top-k calls write them).  Returns out, bf16 [rows, H, 512]; ``lse`` (fp32 [rows, H])
+    k >= 1, as the top-k calls write them; a row whose entries are all -1 gives zeros and lse
+    -inf).  Returns out, bf16 [rows, H, 512]; ``lse`` (fp32 [rows, H])
     is written when given.  Raises DsaError on a host-side error.
     """
     if out is None or workspace is None:

@@ -286,6 +286,8 @@ PyObject* latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (idx) {
       need(idx->scalar_type() == at::kInt && idx->dim() == 2 && idx->size(0) == rows && idx->stride(1) == 1,
            "idx: int32 [rows, k]");
+      // an empty tensor has no address, and no address stands for "no lists"
+      need(idx->size(1) > 0 || rows == 0, "idx: lists of at least one entry (None: every position)");
       k = idx->size(1), idx_stride = rows > 1 ? idx->stride(0) : k;
     }
     need(out && out->scalar_type() == at::kBFloat16 && out->dim() == 3 && out->sizes() == ql->sizes() &&

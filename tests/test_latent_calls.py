@@ -82,3 +82,14 @@ def test_allocations_of_the_current_stream(calls, name):
     x, made = calls
     CALLS[name](x, None)
     assert made and all(t.made_on == "current" and not t.users for t in made)
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("sliced", [False, True])
+def test_lists_without_entries_are_refused(rows, sliced):
+    """An empty list is not "every position": it has no address, as no list has none."""
+    ql, qr = torch.zeros((rows, 8, 512), dtype=torch.bfloat16), torch.zeros((rows, 8, 64), dtype=torch.bfloat16)
+    pool, lens = torch.zeros((2, 41984), dtype=torch.uint8), torch.ones(rows, dtype=torch.int32)
+    idx = torch.zeros((rows, 5), dtype=torch.int32)[:, :0] if sliced else torch.zeros((rows, 0), dtype=torch.int32)
+    with pytest.raises(ValueError, match="at least one entry"):
+        lib.latent_attention(ql, qr, pool, lib.KV_FP8_E4M3, torch.zeros((1, 2), dtype=torch.int32), lens, 0.1, idx=idx)
