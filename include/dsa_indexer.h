@@ -412,12 +412,15 @@ int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_page
  *             where it is noticed the status is DSA_ERR_INVALID_ARG.
  * The softmax and all sums are fp32; the weights of the value product are
  * rounded to bf16.  With an fp8 cache latent queries, weights and tokens are
- * fp16 under scales of their own (a power of two per head, the largest of a
- * token's four scales per token): exact for scales that are powers of two
- * within 2^15 of the token's largest; another scale is rounded as a ratio of
- * the largest and so are its products (2^-11 each), and what falls below
- * 2^-24 of the largest scale is lost.  The launch shape depends on H alone, so a captured call
- * may be replayed with other lengths, lists and tables.  Two kernel launches.
+ * fp16 under scales of their own (a power of two per head, one per token from
+ * its four scales, groups of zeros left out): exact for scales that are powers
+ * of two within 2^22 of the token's largest; another scale is rounded as a
+ * ratio and so are its products (2^-11 each); what lies further down is rounded
+ * to 2^-32 of the largest scale, and a group whose scale is 2^-32 of it or less
+ * counts as zeros.  Weights round by 2^-11 of themselves, and by 2^-31 of the
+ * row's largest weight * scale where theirs is below 2^-20 of it.  The launch
+ * shape depends on H alone, so a captured call may be replayed with other
+ * lengths, lists and tables.  Two kernel launches.
  * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
  * visible position without a page in the pool a NaN row and
  * DSA_ERR_BAD_PAGE; a wait that runs out DSA_ERR_TIMEOUT and NaN rows.
