@@ -32,9 +32,9 @@
 // For scales that are powers of two the tile is exact down to 2^-22 of the
 // token's largest scale, rounded to 2^-32 of it below, and a group of 2^-32 of it
 // or less counts as zeros; a group that does hold zeros has no say in s(t).  A
-// head's queries are scaled by a power of two to bring their largest below
-// 2^15, so that any bf16 range fits; the rotated part stays bf16 in an
-// accumulator of its own.  The reference is kept on w * s(t): the largest lie
+// head's queries are scaled by a power of two that brings the largest of the
+// latent part below 2^15 and of the rotated part below 2^61, so that any finite
+// bf16 values fit; the rotated part stays bf16 in an accumulator of its own.  The reference is kept on w * s(t): the largest lie
 // between 2^6 and 2^15, what is 2^-20 of them is still a normal number, and
 // what is below is rounded to 2^-31 of them.
 //
@@ -123,6 +123,9 @@ constexpr float ref_limit(int kv) { return kv == DSA_KV_BF16 ? 8.f : 15.f; }
 constexpr uint32_t kUnset = 0x80000000u;        // bits of -reference (-0) before the first visible token
 // s(t) over the largest of a token's scales at least, and over the smallest
 constexpr float kScaleBelowTop = 1.f / 128, kScaleAboveLow = 16.f;
+// A head's rotated queries may be up to 2^46 of its latent ones under the power
+// of two that suits those: 2^61, far from bf16's limit and that of the sums.
+constexpr float kRopeRoom = 1.4210854715202004e-14f;  // 2^-46
 constexpr float kSmallestScale = 7.8886090522101181e-31f;  // 2^-100: keeps 1 / s and the sums in range
 
 // Shared memory, from a 1,024-byte boundary.
@@ -449,6 +452,16 @@ __device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8]) {
   }
 }
 
+// The largest magnitude of eight bf16 values; NaN does not count.
+__device__ __forceinline__ float largest8(const uint4& r) {
+  auto size = [](uint32_t u) {
+    u &= 0x7fff7fffu;
+    return *reinterpret_cast<const __nv_bfloat162*>(&u);
+  };
+  const __nv_bfloat162 m = __hmax2(__hmax2(size(r.x), size(r.y)), __hmax2(size(r.z), size(r.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
 // The largest value of a warp's lanes; NaN does not count.
 __device__ __forceinline__ float warp_max(float v) {
   float r;
@@ -519,7 +532,8 @@ __device__ const uint4 g_zeros[kLatent / 16] = {};
 // Brings `count` heads' queries of a row to their place, head by head, UNROLL
 // heads' loads at a time.  bf16: as they are (cp.async; the caller waits for
 // them).  fp8: the latent part as fp16, both parts times a power of two that
-// brings the head's largest into [2^14, 2^15), and the factor that takes the
+// brings the head's largest into [2^14, 2^15) (the rotated part counted as
+// kRopeRoom of itself; values below 2^-86 times 2^100), and the factor that takes the
 // scores back into `mul`.  Heads past `heads` are zeros.
 template <int KV, int UNROLL>
 __device__ __forceinline__ void load_queries(const LatentAttnParams& p, int row, int head0, int heads, int first,
@@ -561,11 +575,11 @@ __device__ __forceinline__ void load_queries(const LatentAttnParams& p, int row,
         float x[8], y[8];
         unpack8(a[u], x);
         unpack8(b[u], y);
-        float top = 0.f;
+        float top = largest8(r[u]) * kRopeRoom;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
         top = warp_max(top);
-        const int n = top > 0.f ? min(max(127 + 14 - (int)(__float_as_uint(top) >> 23), -100), 100) : 0;
+        const int n = top > 0.f ? min(127 + 14 - (int)(__float_as_uint(top) >> 23), 100) : 0;
         const float f = __uint_as_float((uint32_t)(n + 127) << 23);
         uint32_t o[8];
 #pragma unroll

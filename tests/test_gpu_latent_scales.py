@@ -89,3 +89,20 @@ def test_groups_of_far_smaller_scales(smaller):
     x[:, 384:512] *= 2.0 ** -(smaller // 2)
     tokens = attend(x.to(torch.bfloat16), q, 0.1)
     assert (tokens[:, 128:256] != 0).any()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 60, 2.0 ** 100, 2.0 ** 117, 2.0 ** 124])
+def test_large_queries(size):
+    """Every finite bf16 query has its place in fp16 under its head's power of two."""
+    x, q = inputs(150, 6, 3, 1.0, 1.0)
+    q = (q.double() * size).to(torch.bfloat16)
+    attend(x.to(torch.bfloat16), q, 0.07 / size)
+
+
+@pytest.mark.parametrize("latent,rotated", [(1e-30, 2.0 ** 30), (1e-37, 1.0), (1e-20, 2.0 ** 100), (0.0, 2.0 ** 120),
+                                            (2.0 ** -126, 1e-30), (1.0, 2.0 ** 40)])
+def test_query_parts_of_far_sizes(latent, rotated):
+    """The head's power of two suits its rotated part too."""
+    x, q = inputs(150, 6, 4, 1.0, 1.0)
+    q = torch.cat([q[:, :512].double() * latent, q[:, 512:].double() * rotated], -1).to(torch.bfloat16)
+    attend(x.to(torch.bfloat16), q, 0.1 / max(rotated, 22 * latent))
