@@ -18,7 +18,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD, "libdsa_indexer.so")
-CALLS_PATH = os.path.join(BUILD, "_dsa_torch.so")      # the tensor-level calls (torch_calls.cpp)
 CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "nvcc")
 
@@ -50,10 +49,21 @@ def _deps():
     return files
 
 
+def calls_path() -> str:
+    """The CPython module of the tensor-level calls (torch_calls.cpp).  It reads tensors by the
+    layout of the torch that it was compiled with, so its name carries that torch's version and
+    commit, and Python's version and machine: another torch has a file of its own."""
+    import sysconfig
+    import torch
+    commit = (torch.version.git_version or "")[:10]
+    return os.path.join(BUILD, f"_dsa_torch-{torch.__version__}-{commit}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
+    calls = calls_path()
+    if not os.path.exists(LIB_PATH) or not os.path.exists(calls):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(calls))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
@@ -117,11 +127,11 @@ def _compile_calls() -> str:
 
 def _link_calls(obj):
     import torch
-    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    tmp = calls_path() + f".tmp{os.getpid()}"
     _run([CXX, "-shared", obj, "-o", tmp, "-L" + BUILD, "-l:libdsa_indexer.so", "-Wl,-rpath,$ORIGIN",
           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
           "-lc10", "-lc10_cuda"], "linking the tensor-level calls")
-    os.replace(tmp, CALLS_PATH)
+    os.replace(tmp, calls_path())
 
 
 _calls = None
@@ -135,7 +145,7 @@ def load_calls():
         import importlib.machinery
         import importlib.util
         import torch  # noqa: F401  (its libraries are the module's)
-        loader = importlib.machinery.ExtensionFileLoader("_dsa_torch", CALLS_PATH)
+        loader = importlib.machinery.ExtensionFileLoader("_dsa_torch", calls_path())
         spec = importlib.util.spec_from_loader("_dsa_torch", loader)
         _calls = importlib.util.module_from_spec(spec)
         loader.exec_module(_calls)
