@@ -1,7 +1,8 @@
 """Build and load libdsa_indexer.so (the sm_103a CUDA library) in-tree.
 
 The library is compiled with nvcc for ``sm_103a`` only and loaded with
-ctypes.  There is no fallback: if the library cannot be built or loaded the
+ctypes; the tensor-level calls over it are a CPython module, compiled with
+g++ when one of them is first made.  There is no fallback: if the library cannot be built or loaded the
 calls raise.
 """
 from __future__ import annotations
@@ -44,9 +45,13 @@ def _sources():
 
 def _deps():
     files = _sources()
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
+    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     return files
+
+
+def _older(path, files) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(f) > os.path.getmtime(path) for f in files)
 
 
 def calls_path() -> str:
@@ -60,16 +65,15 @@ def calls_path() -> str:
 
 
 def is_stale() -> bool:
-    calls = calls_path()
-    if not os.path.exists(LIB_PATH) or not os.path.exists(calls):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(calls))
-    return any(os.path.getmtime(f) > t for f in _deps())
+    return _older(LIB_PATH, _deps())
+
+
+def calls_stale() -> bool:
+    return _older(calls_path(), [os.path.join(CSRC, "torch_calls.cpp"), os.path.join(INCLUDE, "dsa_indexer.h")])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu under csrc/ for sm_103a and link the shared library; compile the
-    CPython module of the tensor-level calls against it."""
+    """Compile every .cu under csrc/ for sm_103a and link the shared library."""
     if not force and not is_stale():
         return LIB_PATH
     os.makedirs(BUILD, exist_ok=True)
@@ -86,10 +90,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        calls = ex.submit(_compile_calls)
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         results = list(ex.map(compile_one, srcs))
-        calls_obj = calls.result()
     for obj, log in results:
         objs.append(obj)
         if verbose and log:
@@ -100,8 +102,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_calls(calls_obj)
     return LIB_PATH
+
+
+def build_calls(force: bool = False, compiled: str | None = None) -> str:
+    """Compile the CPython module of the tensor-level calls (g++, torch's and Python's headers) and
+    link it to the shared library, which is built first.  ``compiled``: its object file."""
+    if force or compiled or calls_stale():
+        build()
+        _link_calls(compiled or _compile_calls())
+    return calls_path()
+
+
+def build_all(force: bool = False, verbose: bool = False) -> None:
+    """Both, compiled side by side."""
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(_compile_calls) if force or calls_stale() else None
+        build(force, verbose)
+        build_calls(compiled=calls.result() if calls else None)
 
 
 def _run(cmd, what):
@@ -117,6 +135,7 @@ def _compile_calls() -> str:
     include = [INCLUDE, base, os.path.join(base, "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"],
                os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    os.makedirs(BUILD, exist_ok=True)
     obj = os.path.join(BUILD, "torch_calls.o")
     _run([CXX, "-O2", "-std=c++17", "-fPIC",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -142,6 +161,7 @@ def load_calls():
     global _calls
     if _calls is None:
         load()
+        build_calls()
         import importlib.machinery
         import importlib.util
         import torch  # noqa: F401  (its libraries are the module's)

@@ -2,6 +2,7 @@
 import os
 import shutil
 import sysconfig
+import types
 
 import pytest
 import torch
@@ -22,8 +23,33 @@ def built():
     (sysconfig, "get_config_var", lambda name: ".cpython-399-other.so")])
 def test_another_torch_or_python_has_its_own_module(built, monkeypatch, where, name, value):
     """A module that was compiled against another torch's tensors is not loaded."""
-    assert not _native.is_stale()
+    assert not _native.calls_stale()
     here = _native.calls_path()
     monkeypatch.setattr(where, name, value)
     assert _native.calls_path() != here
+    assert _native.calls_stale() and not _native.is_stale()
+
+
+def test_c_library_needs_no_torch_headers(monkeypatch, tmp_path):
+    """The library is built and loaded where the module of the tensor-level calls cannot be."""
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    def no_headers(*a):
+        raise RuntimeError("torch/csrc/autograd/python_variable.h: no such file")
+    monkeypatch.setattr(_native, "BUILD", str(tmp_path))
+    monkeypatch.setattr(_native, "LIB_PATH", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(_native, "_lib", None)
+    monkeypatch.setattr(_native, "_calls", None)
+    monkeypatch.setattr(_native, "_compile_calls", no_headers)
+    monkeypatch.setattr(_native.subprocess, "run", run)
     assert _native.is_stale()
+    _native.build()
+    assert not _native.is_stale() and ran and all(cmd[0] == _native.NVCC for cmd in ran)
+    with pytest.raises(RuntimeError, match="python_variable"):
+        _native.build_calls()
