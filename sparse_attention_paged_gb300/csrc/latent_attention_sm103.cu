@@ -997,40 +997,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attention_kernel(const
                                                             kScaleOffsetFp8) + (t & 63));
             }
             // A group of scale 1 holds zeros (latent_store gives those 1) or values
-            // up to 448.  Zeros have no say in s(t), or they would push groups of
-            // far smaller scales out of fp16.  (Where every scale is 1 the look
-            // at the codes takes 3 to 5%: the prefill 515 us for 488.)
-            uint32_t ones = 0;
+            // up to 448.  Where 1 is a token's largest, zeros must not count, or
+            // they would push groups of far smaller scales out of fp16.  (Where
+            // every scale is 1 the look at the codes takes up to 10%: the prefill 533
+            // us for 484.)
+            float top[4];
+            bool ones = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (tok[i] >= 0)
-                ones |= ((sc[i].x == 1.f ? 1u : 0u) | (sc[i].y == 1.f ? 2u : 0u) | (sc[i].z == 1.f ? 4u : 0u) |
-                         (sc[i].w == 1.f ? 8u : 0u)) << (4 * i);
-            if (__any_sync(0xffffffffu, ones != 0)) {
-              uint32_t zeros = 0;
-#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              top[i] = fmaxf(fmaxf(sc[i].x, sc[i].y), fmaxf(sc[i].z, sc[i].w));
+              ones |= tok[i] >= 0 && top[i] == 1.f;
+            }
+            if (__any_sync(0xffffffffu, ones)) {
+#pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t ask = (ones >> (4 * i)) & 15u;
-                const int t = i == 0 ? tok[0] : i == 1 ? tok[1] : i == 2 ? tok[2] : tok[3];
-                if (ask) zeros |= zero_groups(p.cache + (long long)(t >> 6) * p.page_stride + (t & 63) * kLatent, ask)
-                                  << (4 * i);
+                const int t = tok[i];
+                if (t < 0 || top[i] != 1.f) continue;
+                const uint32_t zeros = zero_groups(
+                    p.cache + (long long)(t >> 6) * p.page_stride + (t & 63) * kLatent,
+                    (sc[i].x == 1.f ? 1u : 0u) | (sc[i].y == 1.f ? 2u : 0u) | (sc[i].z == 1.f ? 4u : 0u) |
+                        (sc[i].w == 1.f ? 8u : 0u));
+                if (zeros & 1u) sc[i].x = 0.f;
+                if (zeros & 2u) sc[i].y = 0.f;
+                if (zeros & 4u) sc[i].z = 0.f;
+                if (zeros & 8u) sc[i].w = 0.f;
+                top[i] = fmaxf(fmaxf(sc[i].x, sc[i].y), fmaxf(sc[i].z, sc[i].w));
               }
               __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((zeros >> (4 * i)) & 1u) sc[i].x = 0.f;
-                if ((zeros >> (4 * i)) & 2u) sc[i].y = 0.f;
-                if ((zeros >> (4 * i)) & 4u) sc[i].z = 0.f;
-                if ((zeros >> (4 * i)) & 8u) sc[i].w = 0.f;
-              }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float4 c = sc[i];
-              const float top = fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w));
-              const float low = fminf(fminf(c.x > 0.f ? c.x : top, c.y > 0.f ? c.y : top),
-                                      fminf(c.z > 0.f ? c.z : top, c.w > 0.f ? c.w : top));
-              const float most = fmaxf(fmaxf(kScaleBelowTop * top, kScaleAboveLow * low), kSmallestScale);
+              const float low = fminf(fminf(c.x > 0.f ? c.x : top[i], c.y > 0.f ? c.y : top[i]),
+                                      fminf(c.z > 0.f ? c.z : top[i], c.w > 0.f ? c.w : top[i]));
+              const float most = fmaxf(fmaxf(kScaleBelowTop * top[i], kScaleAboveLow * low), kSmallestScale);
               const float inv = __frcp_rn(most);
               const __half2 a = __floats2half2_rn(sc[i].x * inv, sc[i].y * inv);
               const __half2 b = __floats2half2_rn(sc[i].z * inv, sc[i].w * inv);
