@@ -1,6 +1,7 @@
 """One decode step of a sparse latent attention layer, with this library's calls in their order:
 
-    norm + rotation of the indexer's queries and keys, rotation of the attention's queries
+    norm + rotation of the indexer's queries and keys (with queries that are rotated only it would
+    be a call for each), rotation of the attention's queries
     the new tokens' keys into the indexer's cache, their latents into the latent cache
     the indexer's logits and the k best positions of every request
     attention over those positions

@@ -324,7 +324,7 @@ typedef enum { DSA_NORM_NONE = 0, DSA_NORM_RMS = 1, DSA_NORM_LAYER = 2 } dsa_nor
  * then values [rot_offset, rot_offset + rot_dims) are rotated by
  * positions[t].  weight, bias: fp32 [D] per side, nullable (1 and 0).
  * positions NULL: no rotation.  Hq or Hk may be 0 (that side's pointers are
- * not used).  8 <= D <= 256, a multiple of 8; rot_dims a multiple of 16
+ * not used); sides of different norms take a call each.  8 <= D <= 256, a multiple of 8; rot_dims a multiple of 16
  * (interleaved: of 8), rot_offset of 8 (DSA_ERR_UNSUPPORTED).  Arrays and
  * rows 16-byte aligned, weights, biases and rope_table too
  * (DSA_ERR_MISALIGNED).  A position
@@ -404,7 +404,8 @@ int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_page
  *   out       bf16 [rows, H, 512] through its strides; lse fp32 [rows, H]
  *             contiguous, nullable.
  *   block_table, bt_stride, seqlens  as for the indexer calls (bt_stride = 0:
- *             all rows share row 0).
+ *             all rows share row 0, a prompt of one request; prompts of several
+ *             requests repeat a request's row for each of its query tokens).
  *   workspace fp32, at least dsa_latent_attention_workspace() floats for the
  *             current device, 16-byte aligned; calls that may overlap need
  *             one each.  What another call or kernel writes to it meanwhile
@@ -420,9 +421,9 @@ int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_page
  * counts as zeros.  Weights round by 2^-11 of themselves, and by 2^-31 of the
  * row's largest weight * scale where theirs is below 2^-20 of it.  A head's
  * latent queries are exact down to 2^-29 of its largest, but for steps of
- * 2^-125 and of 2^-85 of its largest rotated one.  The launch shape depends on H
- * alone, so a captured call may be replayed with other
- * lengths, lists and tables.  Two kernel launches.
+ * 2^-125 and of 2^-85 of its largest rotated one.  Two kernel launches, whose
+ * shapes depend on rows and H, not on lengths, lists or tables: a captured call
+ * may be replayed with others of those.
  * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
  * visible position without a page in the pool a NaN row and
  * DSA_ERR_BAD_PAGE; a wait that runs out DSA_ERR_TIMEOUT and NaN rows.

@@ -308,9 +308,10 @@ def qk_norm_rope(q, k, positions=None, table=None, *, rot_dims=None, rot_offset=
                  k_bias=None, eps=1e-6, q_out=None, k_out=None, dev_status=None, stream=None):
     """Norm and rotate queries [T, Hq, D] and keys [T, Hk, D] per head, in one kernel.
 
-    The last dimension is contiguous, the others may be strided; ``k`` may be None.  ``table``
-    as ``rope_table`` makes it.  Outputs are allocated unless given (in place: pass q and k).
-    Returns (q_out, k_out).  Raises DsaError on a host-side error.
+    The last dimension is contiguous, the others may be strided; ``k`` may be None.  One ``norm``
+    for both: with different ones, a call for each.  ``table`` as ``rope_table`` makes it.
+    Outputs are allocated unless given (in place: pass q and k).  Returns (q_out, k_out).  Raises
+    DsaError on a host-side error.
     """
     if rot_dims is not None and table is not None and rot_dims != table.shape[1]:
         raise ValueError("rot_dims: the table's width")
@@ -368,7 +369,8 @@ def latent_attention(q_latent, q_rope, cache, kv_dtype, block_table, seqlens, sc
     Over every position below ``seqlens``, or over the selection lists ``idx`` (int32 [rows, k],
     k >= 1, as the top-k calls write them; a row whose entries are all -1 gives zeros and lse
     -inf).  Returns out, bf16 [rows, H, 512]; ``lse`` (fp32 [rows, H])
-    is written when given.  Raises DsaError on a host-side error.
+    is written when given.  ``block_table`` has a row per query row, or one for all; a prompt's
+    tokens of one of several requests repeat its row.  Raises DsaError on a host-side error.
     """
     if out is None or workspace is None:
         import torch

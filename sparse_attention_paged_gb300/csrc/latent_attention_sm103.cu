@@ -58,11 +58,13 @@
 // 8,192 fp8 tokens 264 us, 335 without).  The loaders copy (bf16) or convert (fp8) 16
 // bytes at a time; masked tokens are not read, their rows are zeros.
 //
-// Measured (whole call, 64 heads where not said otherwise): 64 rows of 2,048
-// selected tokens each, bf16, 48 us; 64 rows of 512 to 32,768 tokens, fp8, 137
-// us; one row of 131,072 bf16 tokens and 128 heads 58 us; 1,024 fp8 prefill
-// rows of 2,048 selected tokens 480 us (610 TFLOP/s); 152 rows of 8,192 tokens
-// 264 us in either type (5.5 and 3.1 TB/s); one row of 512 and 16 heads 11 us.
+// Measured (both kernels; 64 heads where not said otherwise; in a captured graph
+// with warm inputs, and as single calls with inputs out of L2): 64 rows of 2,048
+// selected tokens each, bf16, 49 and 53 us; 64 rows of 512 to 32,768 tokens, fp8,
+// 138 both; one row of 131,072 bf16 tokens and 128 heads 58 and 63; 1,024 fp8
+// prefill rows of 2,048 selected tokens 478 and 485 (610 TFLOP/s); one row of 512
+// and 16 heads 11.4 and 11.6; 152 rows of 8,192 tokens 262 in either type (5.5
+// and 3.1 TB/s).
 // What bounds it: a tile's chain.  Value product (1,536 cycles of operand
 // reads), the next tile's scores (1,728) and softmax (1,150 to 1,600) follow
 // one another, since only one tile fits: 5,750 cycles a bf16 tile, 6,000 to

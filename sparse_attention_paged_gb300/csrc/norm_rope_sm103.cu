@@ -17,8 +17,11 @@
 // well takes another 5 to 10% off this kernel's time and adds it to that of
 // the next one, which reads them.
 // Measured: 4,096 tokens of 64 + 1 heads of 128 bf16 values 31 us (4.4 TB/s
-// of 136 MB), with 61% of the issue slots taken, so that HBM and instructions
-// bound it together; 1,337 tokens of 24 + 8 heads of 192 fp16 values 7.6 us
+// of 136 MB, 0.64 of a copy's rate, with 61% of the issue slots taken: neither
+// is full).  What holds it: a block has no loads in flight while it computes and
+// stores, and an access is 8 bytes a lane (16 for fp32), which fills whole
+// sectors in a part rotated by halves only; elsewhere neighbouring lanes are 16
+// bytes apart, and an instruction takes half of each sector.  1,337 tokens of 24 + 8 heads of 192 fp16 values 7.6 us
 // (4.3 TB/s) in a graph; 64 tokens 2.6 us, one DRAM round trip and the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
