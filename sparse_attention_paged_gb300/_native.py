@@ -7,7 +7,9 @@ calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import fcntl
 import os
 import subprocess
 import threading
@@ -72,11 +74,25 @@ def calls_stale() -> bool:
     return _older(calls_path(), [os.path.join(CSRC, "torch_calls.cpp"), os.path.join(INCLUDE, "dsa_indexer.h")])
 
 
+@contextlib.contextmanager
+def _one_builder():
+    """Processes that find the build stale at the same time take turns: they share its files."""
+    os.makedirs(BUILD, exist_ok=True)
+    with open(os.path.join(BUILD, "lock"), "w") as f:
+        fcntl.flock(f, fcntl.LOCK_EX)
+        yield
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every .cu under csrc/ for sm_103a and link the shared library."""
-    if not force and not is_stale():
-        return LIB_PATH
-    os.makedirs(BUILD, exist_ok=True)
+    if force or is_stale():
+        with _one_builder():
+            if force or is_stale():
+                _build(verbose)
+    return LIB_PATH
+
+
+def _build(verbose: bool = False) -> None:
     objs = []
 
     def compile_one(src):
@@ -102,24 +118,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
-def build_calls(force: bool = False, compiled: str | None = None) -> str:
+def build_calls(force: bool = False) -> str:
     """Compile the CPython module of the tensor-level calls (g++, torch's and Python's headers) and
-    link it to the shared library, which is built first.  ``compiled``: its object file."""
-    if force or compiled or calls_stale():
+    link it to the shared library, which is built first."""
+    if force or calls_stale():
         build()
-        _link_calls(compiled or _compile_calls())
+        with _one_builder():
+            if force or calls_stale():
+                _link_calls(_compile_calls())
     return calls_path()
 
 
 def build_all(force: bool = False, verbose: bool = False) -> None:
     """Both, compiled side by side."""
-    with ThreadPoolExecutor(max_workers=1) as ex:
+    if not (force or is_stale() or calls_stale()):
+        return
+    with _one_builder(), ThreadPoolExecutor(max_workers=1) as ex:
         calls = ex.submit(_compile_calls) if force or calls_stale() else None
-        build(force, verbose)
-        build_calls(compiled=calls.result() if calls else None)
+        if force or is_stale():
+            _build(verbose)
+        if calls:
+            _link_calls(calls.result())
 
 
 def _run(cmd, what):
@@ -135,7 +156,6 @@ def _compile_calls() -> str:
     include = [INCLUDE, base, os.path.join(base, "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"],
                os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
-    os.makedirs(BUILD, exist_ok=True)
     obj = os.path.join(BUILD, "torch_calls.o")
     _run([CXX, "-O2", "-std=c++17", "-fPIC",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",

@@ -1,6 +1,8 @@
 """What is compiled for whom (no GPU, and nothing is compiled here)."""
 import os
 import shutil
+import subprocess
+import sys
 import sysconfig
 import types
 
@@ -53,3 +55,33 @@ def test_c_library_needs_no_torch_headers(monkeypatch, tmp_path):
     assert not _native.is_stale() and ran and all(cmd[0] == _native.NVCC for cmd in ran)
     with pytest.raises(RuntimeError, match="python_variable"):
         _native.build_calls()
+
+
+BUILDER = """
+import os, subprocess, sys, time, types
+sys.path.insert(0, sys.argv[2])
+from sparse_attention_paged_gb300 import _native
+_native.BUILD = sys.argv[1]
+_native.LIB_PATH = os.path.join(sys.argv[1], "lib.so")
+_native._sources = lambda: [os.path.join(_native.CSRC, "dsa_api.cu")]
+
+def run(cmd, **kw):
+    out = cmd[cmd.index("-o") + 1]
+    with open(os.path.join(sys.argv[1], "ran"), "a") as f:
+        f.write("x")
+    with open(out, "w"):
+        time.sleep(0.3)
+    return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+_native.subprocess = types.SimpleNamespace(run=run)
+_native.build()
+assert not _native.is_stale()
+"""
+
+
+def test_processes_do_not_build_at_once(tmp_path):
+    """Three that find the build missing: one compiles and links, the others wait and take its files."""
+    args = [sys.executable, "-c", BUILDER, str(tmp_path), _native.ROOT]
+    running = [subprocess.Popen(args) for _ in range(3)]
+    assert [p.wait(timeout=60) for p in running] == [0, 0, 0]
+    assert (tmp_path / "ran").read_text() == "xx"
