@@ -417,11 +417,11 @@ int dsa_latent_load(const void* cache, long long page_stride_bytes, int num_page
  * its four scales, groups of zeros left out): exact for scales that are powers
  * of two within 2^22 of the token's largest; another scale is rounded as a
  * ratio and so are its products (2^-11 each); what lies further down is rounded
- * to 2^-32 of the largest scale, and a group whose scale is 2^-32 of it or less
- * counts as zeros.  Weights round by 2^-11 of themselves, and by 2^-31 of the
- * row's largest weight * scale where theirs is below 2^-20 of it.  A head's
- * latent queries are exact down to 2^-29 of its largest, but for steps of
- * 2^-125 and of 2^-85 of its largest rotated one.  Two kernel launches, whose
+ * to 2^-32 of the largest scale or to 2^-125, and a group whose scale is 2^-32
+ * of it or less counts as zeros.  Weights round by 2^-11 of themselves, and by
+ * 2^-31 of the row's largest weight * scale where theirs is below 2^-20 of it.
+ * A head's latent queries are exact down to 2^-29 of its largest, but for steps
+ * of 2^-125 and of 2^-85 of its largest rotated one.  Two kernel launches, whose
  * shapes depend on rows and H, not on lengths, lists or tables: a captured call
  * may be replayed with others of those.
  * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
