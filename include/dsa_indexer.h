@@ -93,7 +93,8 @@ extern "C" {
 
 typedef enum {
   DSA_KV_FP8_E4M3 = 0,
-  DSA_KV_BF16 = 1
+  DSA_KV_BF16 = 1,
+  DSA_KV_FP16 = 2  /* the paged cache of keys and values only */
 } dsa_kv_dtype_t;
 
 typedef enum {
@@ -444,6 +445,164 @@ int dsa_latent_attention(const void* q_latent, long long ql_row_stride, long lon
  * (two partial rows of 64 heads and a split record per SM); -1 when there is
  * no device. */
 long long dsa_latent_attention_workspace(void);
+
+/*
+ * ---- A paged cache of keys and values with grouped heads -------------------
+ *
+ * The common rules hold as for the calls above.  Hq query heads share Hkv key
+ * and value heads (query head h reads head h / (Hq / Hkv)); D is 64 or 128,
+ * page_size 64, and Hq a multiple of Hkv.  A pool of keys or values holds
+ * num_pages pages of 64 slots and Hkv heads: slot s of head h in page p starts
+ * at element p * page_stride + s * slot_stride + h * head_stride and has D
+ * adjacent values, so that token-major and head-major pages are both at hand.
+ * Strides are at least D and, like the pool, on 16 bytes (those of a single
+ * page or head are not used).  kv_dtype: DSA_KV_BF16 or DSA_KV_FP16 (then
+ * queries, keys and values are of that type, DSA_ERR_UNSUPPORTED otherwise), or
+ * DSA_KV_FP8_E4M3 with fp32 scales k_scale and v_scale [num_pages, Hkv, 64],
+ * contiguous, 16-byte aligned: value = code * scale, scale >= 0.  dtype:
+ * DSA_BF16 or DSA_FP16.
+ */
+
+/*
+ * Block tables and slots from the requests' lengths.  Request b holds
+ * lengths[b] tokens in the first ceil(lengths[b] / 64) pages of its table row
+ * and gets new_tokens[b] more, for which it takes as many pages as it still
+ * needs from free_pages (n_free page ids), requests in order; the pages' ids
+ * are entered into its row.  Its tokens are rows cu_rows[b] up to cu_rows[b+1]
+ * of the outputs:
+ *   slots      [n]: page * 64 + slot, -1 for the rows behind the last token
+ *   positions  [n], nullable: the token's position, 0 behind the last
+ *   seqlens    [n_req], nullable: lengths + new_tokens (not lengths or
+ *              new_tokens itself)
+ *   cu_rows    [n_req + 1], nullable: sums of new_tokens
+ *   used       [1], nullable: pages taken
+ * No other entry of the table is written.  Arrays must not overlap.
+ * Data errors: a request with a negative length or more than W * 64 tokens
+ * (DSA_ERR_BAD_SEQLEN), or for whose pages the free list is too short
+ * (DSA_ERR_BAD_PAGE), takes none; its tokens have slot -1 and position 0, its
+ * seqlens is 0.  A page whose slots would pass 32 bits, or a negative one,
+ * gives slot -1 and DSA_ERR_BAD_PAGE.  More than n tokens: those past n have no
+ * row, and a fresh page that begins there is not entered, DSA_ERR_BAD_SEQLEN.
+ * bt_stride may be 0 for one request only.
+ */
+int dsa_request_slots(const int* lengths, const int* new_tokens, int n_req,
+                      const int* free_pages, int n_free, int* block_table, long long bt_stride,
+                      int W, int page_size, int n, int* slots, int* positions, int* seqlens,
+                      int* cu_rows, int* used, int* dev_status, void* stream);
+
+/*
+ * Store: n new tokens into their slots (slot_mapping as for dsa_kcache_store:
+ * negative = skip, past the pool = skipped with DSA_ERR_BAD_PAGE, equal slots
+ * race).  Key of token i, head h: D values at k + i * k_token_stride + h *
+ * k_head_stride, v alike (16-byte aligned).  fp8: per token and head the scale
+ * is 2^e with the smallest e >= -126 for which the largest finite magnitude is
+ * at most 448 * 2^e (2^-126 for zeros); codes round to nearest even,
+ * infinities become +-448 and NaN stays NaN.
+ */
+int dsa_kv_store(const void* k, long long k_token_stride, long long k_head_stride, const void* v,
+                 long long v_token_stride, long long v_head_stride, int n, int Hkv, int D,
+                 int dtype, const int* slot_mapping, void* k_cache, long long kc_page_stride,
+                 long long kc_slot_stride, long long kc_head_stride, void* v_cache,
+                 long long vc_page_stride, long long vc_slot_stride, long long vc_head_stride,
+                 float* k_scale, float* v_scale, int num_pages, int kv_dtype, int page_size,
+                 int* dev_status, void* stream);
+
+/*
+ * Boxes around the keys of pages: for every request the pages that hold its
+ * positions starts[r] (NULL: 0; negative: 0) up to seqlens[r] - 1, each with all
+ * its positions below seqlens[r].  bounds: int8 [num_pages, Hkv, 2, D],
+ * contiguous, 16-byte aligned: the largest keys' codes, then the smallest ones';
+ * bound_scale: fp32 [num_pages, Hkv].  With e >= -126 the smallest for which no
+ * key's magnitude is above 127 * 2^e: scale 2^e, codes ceil(largest / 2^e) and
+ * floor(smallest / 2^e).  NaN keys are passed over (a channel without a number:
+ * 0), infinities count as the largest float.  max_tokens: how many positions a
+ * request has from starts[r] on; it shapes the launch, and more are taken all
+ * the same, but for 0, which launches nothing.
+ * Data errors: seqlens[r] > W * 64 leaves the request out (DSA_ERR_BAD_SEQLEN),
+ * a page outside the pool itself (DSA_ERR_BAD_PAGE).
+ */
+int dsa_block_bounds(const void* k_cache, long long kc_page_stride, long long kc_slot_stride,
+                     long long kc_head_stride, const float* k_scale, int num_pages, int kv_dtype,
+                     int Hkv, int D, int page_size, const int* block_table, long long bt_stride,
+                     int W, const int* starts, const int* seqlens, int n_req, int max_tokens,
+                     signed char* bounds, float* bound_scale, int* dev_status, void* stream);
+
+/*
+ * The k pages of every row and key head that may hold the largest scores:
+ * blocks[r, h, :] (int32 [rows, Hkv, k], contiguous) are places in the row's
+ * block table, ascending, then -1.  A row of ceil(seqlens[r] / 64) <= k pages
+ * has them all.  Else the first `first` and the last `last` pages are taken
+ * (first + last <= k), and of the others those with the largest
+ *     score = (sum_d p_d high_d - n_d low_d) * scale
+ * over the page's box as dsa_block_bounds writes it, equal ones from the front.
+ * p and n are the group's queries' positive and negative parts: with 2^x above
+ * the group's largest |q|, i = round(q * 2^(20 - x)) (to even), P and N the sums
+ * of the positive and of the negated negative i over the group's heads, s >= 0
+ * the smallest with max(P, N) <= 127 * 2^s over all d, p = ceil(P / 2^s),
+ * n = ceil(N / 2^s).  So the score bounds the sum over the group's heads of the
+ * largest product with a key of the page, up to one factor per row and head and
+ * the queries' rounding.  It is exact, past the largest float that; NaN queries
+ * count as 0, infinities as the largest float.
+ * q: [rows, Hq, D] through its strides, 16-byte aligned; Hq / Hkv <= 1024 and W
+ * <= 32768 (DSA_ERR_UNSUPPORTED).
+ * Data errors: seqlens[r] > W * 64 (DSA_ERR_BAD_SEQLEN) or a page outside the
+ * pool among the row's (DSA_ERR_BAD_PAGE) gives a list of -1.
+ */
+int dsa_block_select(const void* q, long long q_row_stride, long long q_head_stride, int rows,
+                     int Hq, int Hkv, int D, int dtype, const signed char* bounds,
+                     const float* bound_scale, int num_pages, const int* block_table,
+                     long long bt_stride, int W, int page_size, const int* seqlens, int k,
+                     int first, int last, int* blocks, int* dev_status, void* stream);
+
+/*
+ * Attention of one query token per row (a decode request, or a prefill token
+ * with its causal length) over its cached tokens:
+ *     s[t] = scale * q[r, h] . k[t],  out[r, h] = sum_t softmax(s)[t] v[t],
+ *     lse[r, h] = log sum_t exp(s[t])
+ * The visible tokens are t < seqlens[r] (blocks NULL), or those of them in the
+ * pages that the list blocks[r * blocks_row_stride + (h / group) *
+ * blocks_head_stride + j], j < k, names (places in the row's block table; the
+ * lists that dsa_block_select writes, or one for all heads with head stride 0).
+ * Entries that are negative or past the row's pages are passed over, and a
+ * page that is named twice counts twice.  A row without a visible token gives
+ * zeros and lse = -inf.
+ *   q, out    [rows, Hq, D] through their strides, 16-byte aligned, of dtype.
+ *   lse       fp32 [rows, Hq] contiguous, nullable.
+ *   block_table, bt_stride, seqlens  as for the indexer calls (bt_stride = 0:
+ *             all rows share row 0).
+ *   workspace fp32, at least dsa_paged_attention_workspace() floats, 16-byte
+ *             aligned; calls that may overlap need one each.  What another call
+ *             or kernel writes to it meanwhile leaves the results undefined,
+ *             without an access out of range.
+ * Softmax and sums are fp32.  The weights of the value product are rounded to
+ * the cache's type.  With an fp8 cache the codes are taken as fp16 (exact); a
+ * head's queries as fp16 under a power of two, exact down to 2^-28 of the
+ * head's largest and to 2^-39 of it below; weights times the tokens' value
+ * scales as fp16, rounded by 2^-11 of themselves and by 2^-38 of the row's
+ * largest where they are below 2^-27 of it.  The same call gives the same bits.
+ * Two kernel launches, whose shapes depend on Hq / Hkv and D only: a captured
+ * call may be replayed with other lengths, lists and tables.
+ * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
+ * visible token without a page in the pool NaN for the heads that see it and
+ * DSA_ERR_BAD_PAGE; a wait that runs out DSA_ERR_TIMEOUT and NaN rows.
+ * rows * Hkv * ceil(Hq / Hkv / 32) * (blocks ? k : W) must be below 2^31.
+ */
+int dsa_paged_attention(const void* q, long long q_row_stride, long long q_head_stride, int rows,
+                        int Hq, int Hkv, int D, int dtype, float scale, const void* k_cache,
+                        long long kc_page_stride, long long kc_slot_stride,
+                        long long kc_head_stride, const void* v_cache, long long vc_page_stride,
+                        long long vc_slot_stride, long long vc_head_stride, const float* k_scale,
+                        const float* v_scale, int num_pages, int kv_dtype, int page_size,
+                        const int* block_table, long long bt_stride, int W, const int* seqlens,
+                        const int* blocks, long long blocks_row_stride,
+                        long long blocks_head_stride, int k, void* out, long long out_row_stride,
+                        long long out_head_stride, float* lse, float* workspace,
+                        long long workspace_floats, int* dev_status, void* stream);
+
+/* Floats of workspace that dsa_paged_attention needs on the current device
+ * (two partial results and a split record per CTA); -1 for shapes that it does
+ * not take or without a device. */
+long long dsa_paged_attention_workspace(int Hq, int Hkv, int D);
 
 /* A static, human-readable name for a status code. */
 const char* dsa_status_string(int status);

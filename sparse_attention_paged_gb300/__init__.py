@@ -18,6 +18,7 @@ from . import _native
 
 KV_FP8_E4M3 = 0
 KV_BF16 = 1
+KV_FP16 = 2                    # the paged cache of keys and values only
 H = 64
 D = 128
 PAGE = 64
@@ -275,6 +276,70 @@ def dsa_latent_attention_workspace() -> int:
     return int(_native.load().dsa_latent_attention_workspace())
 
 
+def dsa_request_slots(lengths, new_tokens, n_req, free_pages, n_free, block_table, bt_stride, W,
+                      page_size, n, slots, positions, seqlens, cu_rows, used, dev_status=None,
+                      stream=None) -> int:
+    """C ``dsa_request_slots``; returns its status code."""
+    return _native.load().dsa_request_slots(
+        _p(lengths), _p(new_tokens), n_req, _p(free_pages), n_free, _p(block_table), bt_stride, W,
+        page_size, n, _p(slots), _p(positions), _p(seqlens), _p(cu_rows), _p(used),
+        _p(dev_status), _stream(stream))
+
+
+def dsa_kv_store(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, n, Hkv, D,
+                 dtype, slot_mapping, k_cache, kc_page_stride, kc_slot_stride, kc_head_stride,
+                 v_cache, vc_page_stride, vc_slot_stride, vc_head_stride, k_scale, v_scale,
+                 num_pages, kv_dtype, page_size, dev_status=None, stream=None) -> int:
+    """C ``dsa_kv_store``; returns its status code."""
+    return _native.load().dsa_kv_store(
+        _p(k), k_token_stride, k_head_stride, _p(v), v_token_stride, v_head_stride, n, Hkv, D,
+        dtype, _p(slot_mapping), _p(k_cache), kc_page_stride, kc_slot_stride, kc_head_stride,
+        _p(v_cache), vc_page_stride, vc_slot_stride, vc_head_stride, _p(k_scale), _p(v_scale),
+        num_pages, kv_dtype, page_size, _p(dev_status), _stream(stream))
+
+
+def dsa_block_bounds(k_cache, kc_page_stride, kc_slot_stride, kc_head_stride, k_scale, num_pages,
+                     kv_dtype, Hkv, D, page_size, block_table, bt_stride, W, starts, seqlens,
+                     n_req, max_tokens, bounds, bound_scale, dev_status=None, stream=None) -> int:
+    """C ``dsa_block_bounds``; returns its status code."""
+    return _native.load().dsa_block_bounds(
+        _p(k_cache), kc_page_stride, kc_slot_stride, kc_head_stride, _p(k_scale), num_pages,
+        kv_dtype, Hkv, D, page_size, _p(block_table), bt_stride, W, _p(starts), _p(seqlens),
+        n_req, max_tokens, _p(bounds), _p(bound_scale), _p(dev_status), _stream(stream))
+
+
+def dsa_block_select(q, q_row_stride, q_head_stride, rows, Hq, Hkv, D, dtype, bounds, bound_scale,
+                     num_pages, block_table, bt_stride, W, page_size, seqlens, k, first, last,
+                     blocks, dev_status=None, stream=None) -> int:
+    """C ``dsa_block_select``; returns its status code."""
+    return _native.load().dsa_block_select(
+        _p(q), q_row_stride, q_head_stride, rows, Hq, Hkv, D, dtype, _p(bounds), _p(bound_scale),
+        num_pages, _p(block_table), bt_stride, W, page_size, _p(seqlens), k, first, last,
+        _p(blocks), _p(dev_status), _stream(stream))
+
+
+def dsa_paged_attention(q, q_row_stride, q_head_stride, rows, Hq, Hkv, D, dtype, scale, k_cache,
+                        kc_page_stride, kc_slot_stride, kc_head_stride, v_cache, vc_page_stride,
+                        vc_slot_stride, vc_head_stride, k_scale, v_scale, num_pages, kv_dtype,
+                        page_size, block_table, bt_stride, W, seqlens, blocks, blocks_row_stride,
+                        blocks_head_stride, k, out, out_row_stride, out_head_stride, lse,
+                        workspace, workspace_floats, dev_status=None, stream=None) -> int:
+    """C ``dsa_paged_attention``; returns its status code."""
+    return _native.load().dsa_paged_attention(
+        _p(q), q_row_stride, q_head_stride, rows, Hq, Hkv, D, dtype, scale, _p(k_cache),
+        kc_page_stride, kc_slot_stride, kc_head_stride, _p(v_cache), vc_page_stride,
+        vc_slot_stride, vc_head_stride, _p(k_scale), _p(v_scale), num_pages, kv_dtype, page_size,
+        _p(block_table), bt_stride, W, _p(seqlens), _p(blocks), blocks_row_stride,
+        blocks_head_stride, k, _p(out), out_row_stride, out_head_stride, _p(lse), _p(workspace),
+        workspace_floats, _p(dev_status), _stream(stream))
+
+
+def dsa_paged_attention_workspace(Hq, Hkv, D) -> int:
+    """C ``dsa_paged_attention_workspace``: floats for the current device, -1 without one or for
+    shapes that the call does not take."""
+    return int(_native.load().dsa_paged_attention_workspace(Hq, Hkv, D))
+
+
 _calls = None
 
 
@@ -383,6 +448,116 @@ def latent_attention(q_latent, q_rope, cache, kv_dtype, block_table, seqlens, sc
     status = (_calls or _tensor_calls()).latent_attention(
         q_latent, q_rope, cache, kv_dtype, block_table, seqlens, scale, idx, out, lse, workspace,
         dev_status, _stream_address(stream))
+    if status:
+        raise DsaError(status)
+    return out
+
+
+# ---- a paged cache of keys and values with grouped heads ----
+#
+# Hq query heads share Hkv key and value heads, D is 64 or 128.  A cache is a tensor [pages, 64, Hkv,
+# D] of the tokens' type or float8_e4m3fn, values of a head adjacent and everything else strided: a
+# head-major pool [pages, Hkv, 64, D] goes in as pool.transpose(1, 2).  An fp8 cache has fp32 scales
+# [pages, Hkv, 64] beside it.
+
+def request_slots(lengths, new_tokens, free_pages, block_table, n, *, slots=None, positions=None,
+                  seqlens=None, cu_rows=None, used=None, dev_status=None, stream=None):
+    """Pages for new tokens into the block table, and the tokens' slots, from the requests' lengths.
+
+    Request b holds ``lengths[b]`` tokens and gets ``new_tokens[b]``, for which it takes pages of
+    ``free_pages`` in order (int32, ``used`` says how many); ``block_table`` [requests, W] is updated
+    in place.  ``n``: rows of the outputs, at least the new tokens in all; the rest has slot -1.
+    Outputs are allocated unless given.  Returns (slots [n], positions [n], seqlens [requests],
+    cu_rows [requests + 1], used [1]), int32.  Raises DsaError on a host-side error.
+    """
+    if slots is None or positions is None or seqlens is None or cu_rows is None or used is None:
+        requests = lengths.shape[0]
+        with _AllocateOn(stream, lengths) as on:
+            def made(x, size):
+                return on.returned(lengths.new_empty((size,))) if x is None else x
+            slots, positions = made(slots, n), made(positions, n)
+            seqlens, cu_rows, used = made(seqlens, requests), made(cu_rows, requests + 1), made(used, 1)
+    status = (_calls or _tensor_calls()).request_slots(
+        lengths, new_tokens, free_pages, block_table, n, slots, positions, seqlens, cu_rows, used,
+        dev_status, _stream_address(stream))
+    if status:
+        raise DsaError(status)
+    return slots, positions, seqlens, cu_rows, used
+
+
+def kv_store(k, v, slot_mapping, k_cache, v_cache, *, k_scale=None, v_scale=None, dev_status=None,
+             stream=None):
+    """Write n tokens' keys and values [n, Hkv, D] (bf16 or fp16) into their slots of the caches.
+
+    Tokens and heads may be strided.  An fp8 cache takes codes, and ``k_scale`` and ``v_scale`` the
+    scales.  Raises DsaError on a host-side error.
+    """
+    status = (_calls or _tensor_calls()).kv_store(
+        k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, dev_status, _stream_address(stream))
+    if status:
+        raise DsaError(status)
+    return k_cache, v_cache
+
+
+def block_bounds(k_cache, block_table, starts, seqlens, max_tokens, bounds, bound_scale, *,
+                 k_scale=None, dev_status=None, stream=None):
+    """Boxes around the keys of the pages that hold the positions from ``starts`` (None: 0) up to
+    ``seqlens`` of each request, for ``block_select``.
+
+    ``bounds`` int8 [pages, Hkv, 2, D] and ``bound_scale`` fp32 [pages, Hkv] are updated in place.
+    ``max_tokens``: a request's positions from ``starts`` on, at most.  Raises DsaError on a
+    host-side error.
+    """
+    status = (_calls or _tensor_calls()).block_bounds(
+        k_cache, block_table, starts, seqlens, max_tokens, bounds, bound_scale, k_scale, dev_status,
+        _stream_address(stream))
+    if status:
+        raise DsaError(status)
+    return bounds, bound_scale
+
+
+def block_select(q, bounds, bound_scale, block_table, seqlens, k, *, first=1, last=1, out=None,
+                 dev_status=None, stream=None):
+    """The k pages of every row and key head whose boxes allow the largest scores of the group's
+    queries [rows, Hq, D], the ``first`` and the ``last`` ones always among them.
+
+    Returns int32 [rows, Hkv, k]: places in the row's block table, ascending, then -1, as
+    ``paged_attention`` takes them.  ``block_table`` has a row per query row, or one for all.
+    Raises DsaError on a host-side error.
+    """
+    if out is None:
+        import torch
+        with _AllocateOn(stream, q) as on:
+            out = on.returned(q.new_empty((q.shape[0], bounds.shape[1], k), dtype=torch.int32))
+    status = (_calls or _tensor_calls()).block_select(
+        q, bounds, bound_scale, block_table, seqlens, k, first, last, out, dev_status,
+        _stream_address(stream))
+    if status:
+        raise DsaError(status)
+    return out
+
+
+def paged_attention(q, k_cache, v_cache, block_table, seqlens, scale, *, blocks=None, k_scale=None,
+                    v_scale=None, out=None, lse=None, workspace=None, dev_status=None, stream=None):
+    """Attention of one query token per row, [rows, Hq, D], over its cached keys and values.
+
+    Over every position below ``seqlens``, or over those in the pages that ``blocks`` names (int32
+    [rows, Hkv, k], as ``block_select`` writes it; a list for all heads goes in expanded).  A row
+    without a visible token gives zeros and lse -inf.  Returns out, like q; ``lse`` (fp32 [rows,
+    Hq]) is written when given.  ``block_table`` has a row per query row, or one for all; a prompt's
+    tokens of one of several requests repeat its row.  Raises DsaError on a host-side error.
+    """
+    if out is None or workspace is None:
+        import torch
+        with _AllocateOn(stream, q) as on:
+            if out is None:
+                out = on.returned(q.new_empty(q.shape))
+            if workspace is None:
+                floats = dsa_paged_attention_workspace(q.shape[1], k_cache.shape[2], q.shape[2])
+                workspace = q.new_empty(max(floats, 0), dtype=torch.float32)
+    status = (_calls or _tensor_calls()).paged_attention(
+        q, k_cache, v_cache, block_table, seqlens, scale, blocks, k_scale, v_scale, out, lse,
+        workspace, dev_status, _stream_address(stream))
     if status:
         raise DsaError(status)
     return out

@@ -35,6 +35,8 @@ EXPORTS = ("dsa_indexer_logits_decode", "dsa_indexer_logits_prefill",
            "dsa_indexer_topk_decode_static", "dsa_kcache_store",
            "dsa_qk_norm_rope", "dsa_latent_store", "dsa_latent_load",
            "dsa_latent_attention", "dsa_latent_attention_workspace",
+           "dsa_request_slots", "dsa_kv_store", "dsa_block_bounds", "dsa_block_select",
+           "dsa_paged_attention", "dsa_paged_attention_workspace",
            "dsa_status_string", "dsa_indexer_abi_version")
 
 _lib = None
@@ -239,6 +241,24 @@ def load() -> ctypes.CDLL:
                                              ll, vp, vp]
         lib.dsa_latent_attention_workspace.restype = ll
         lib.dsa_latent_attention_workspace.argtypes = []
+        lib.dsa_request_slots.restype = ci
+        lib.dsa_request_slots.argtypes = [vp, vp, ci, vp, ci, vp, ll, ci, ci, ci, vp, vp, vp, vp, vp,
+                                          vp, vp]
+        lib.dsa_kv_store.restype = ci
+        lib.dsa_kv_store.argtypes = [vp, ll, ll, vp, ll, ll, ci, ci, ci, ci, vp, vp, ll, ll, ll, vp, ll,
+                                     ll, ll, vp, vp, ci, ci, ci, vp, vp]
+        lib.dsa_block_bounds.restype = ci
+        lib.dsa_block_bounds.argtypes = [vp, ll, ll, ll, vp, ci, ci, ci, ci, ci, vp, ll, ci, vp, vp, ci,
+                                         ci, vp, vp, vp, vp]
+        lib.dsa_block_select.restype = ci
+        lib.dsa_block_select.argtypes = [vp, ll, ll, ci, ci, ci, ci, ci, vp, vp, ci, vp, ll, ci, ci, vp,
+                                         ci, ci, ci, vp, vp, vp]
+        lib.dsa_paged_attention.restype = ci
+        lib.dsa_paged_attention.argtypes = [vp, ll, ll, ci, ci, ci, ci, ci, cf, vp, ll, ll, ll, vp, ll,
+                                            ll, ll, vp, vp, ci, ci, ci, vp, ll, ci, vp, vp, ll, ll, ci,
+                                            vp, ll, ll, vp, vp, ll, vp, vp]
+        lib.dsa_paged_attention_workspace.restype = ll
+        lib.dsa_paged_attention_workspace.argtypes = [ci, ci, ci]
         lib.dsa_status_string.restype = ctypes.c_char_p
         lib.dsa_status_string.argtypes = [ci]
         lib.dsa_indexer_abi_version.restype = ci

@@ -1,0 +1,991 @@
+// paged_attention_sm103.cu -- attention of one query token per row over a
+// paged cache of keys and values with grouped heads (Hq query heads share Hkv
+// key and value heads):
+//
+//   s[t]   = scale * q[r, h] . k[t, h / group]        t < seqlens[r], or the
+//   out    = sum_t softmax(s)[t] v[t, h / group]      tokens of the listed pages
+//   lse    = log sum_t exp(s[t])
+//
+// One pass over the tokens with a running maximum and sum per head.  A page of
+// 64 tokens of one key head, keys and values, is a stage of a ring in shared
+// memory that TMA fills through the pools' own strides; four warps take 16 of
+// its tokens each:
+//
+//   S [16 heads x 16 tokens] = Q (A) * K^T (B)        m16n8k16, fp32 sums
+//   O [16 heads x D]        += P (A) * V (B)
+//
+// Q's fragments stay in registers, and so does O; S becomes P in the registers
+// where it is.  The order of the values in a dot product is free: lane t of
+// four takes the 16-byte units 2t and 2t + 1 of a key's 128 bytes as they lie,
+// with the queries in the same order, so that keys are read 16 bytes at a
+// time without a bank conflict.  Each warp has a running maximum of its own;
+// the four meet once a row, in the row's last stage.
+//
+// Decode reads 2 D values per token for 4 D * group operations: 16 operations
+// a byte at 8 heads a group, where 285 would balance HBM and tensor cores.
+// Warp-level products leave S and P in registers; through tensor memory they
+// would take two more trips and barriers a page for tensor time that is not
+// missed.
+//
+// fp8 cache: codes become fp16, which holds e4m3 exactly.  A head's queries are
+// scaled to a largest magnitude below 2^14 by a power of two; scores take the
+// token's key scale; the weights take its value scale before they are rounded
+// to fp16, under a reference of their own that follows the largest weight *
+// scale: that is 2^13 to 2^14, and a token's weight is exact to 2^-11 of
+// itself down to 2^-27 of it, and to 2^-38 of it below.
+// 16-bit caches: the weights are rounded to the cache's type (2^-8 of
+// themselves for bf16, 2^-11 for fp16, 2^-25 of the largest where it is below
+// fp16's normal numbers), independently from token to token.
+//
+// Work: units of one page of one key head (a group of more than 32 query heads
+// is several), rows in order, cut into equal slices, one per CTA.  A row that a
+// slice cuts leaves partial sums in the workspace, joined by a second kernel in
+// the order of the slices: the same bits every time.
+//
+// Warps: the last one walks the slice (lengths, list, table; 32 pages at a
+// time) and issues TMA, the others compute.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "paged_common.cuh"
+#include "sm100_ptx.cuh"
+#include "tensor_maps.cuh"
+
+#ifndef DSA_WAIT_LIMIT_CYCLES
+#define DSA_WAIT_LIMIT_CYCLES 4000000000ll
+#endif
+
+namespace dsa {
+
+namespace {
+
+using namespace sm100;
+
+// at most about a second: the clock's low 32 bits are compared
+constexpr uint32_t kWaitLimit = DSA_WAIT_LIMIT_CYCLES < 2000000000ll ? DSA_WAIT_LIMIT_CYCLES : 2000000000ll;
+constexpr unsigned kAll = 0xffffffffu;
+
+// Shapes of one instance: cache type, values per head, tiles of 16 query heads.
+template <int KV, int D, int MT>
+struct Shape {
+  static constexpr bool kFp8 = KV == DSA_KV_FP8_E4M3;
+  static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
+  static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kBoxes = kRowBytes / kBoxBytes;
+  static constexpr int kBox = kPage * kBoxBytes;               // bytes of one box in shared memory
+  static constexpr int kSide = kPage * kRowBytes;              // keys or values of a page
+  static constexpr int kHeadsMax = 16 * MT;
+  static constexpr int kScaleBytes = kFp8 ? kPage * 4 : 0;
+  static constexpr int kOffScale = 2 * kSide;
+  static constexpr int kOffQ = kOffScale + 2 * kScaleBytes;
+  static constexpr int kStage = (kOffQ + kHeadsMax * D * 2 + 1023) / 1024 * 1024;
+  static constexpr int kCtas = MT == 1 ? 2 : 1;                // per SM
+  static constexpr int kConsumers = 4 * MT;                    // warps
+  static constexpr int kThreads = (kConsumers + 1) * 32;
+  static constexpr int kMisc = 4096;
+  static constexpr int kRoom = (233472 / kCtas - 1024 - 1024 - kMisc) / kStage;
+  static constexpr int kStages = kRoom < 8 ? kRoom : 8;
+  static constexpr int kSmem = kStages * kStage + kMisc + 1024;
+  // the four token slices of a row meet in a stage's keys and values, some columns at a time
+  static constexpr int kPasses = 4 * kHeadsMax * D * 4 / (2 * kSide) < 1 ? 1 : 4 * kHeadsMax * D * 4 / (2 * kSide);
+  static constexpr int kCols = D / kPasses;
+  static_assert(kStages >= 3 && kSmem <= 232448 && kCols >= 8 && kPasses * kCols == D, "shape");
+};
+
+struct Misc {
+  uint64_t full[8], empty[8];
+  uint64_t meet;                 // the consumer warps' own barrier
+  int4 meta[8];                  // per stage: row, tile, tokens | flags, last CTA of a row that is cut
+  int scan[16];
+  int begin, end, share, total;  // the slice, units per CTA, units in all
+  int row, tile, unit;           // the slice's first unit
+  // per consumer warp and head: maximum, reference of the sums, total.  Two of
+  // them in turn: a warp may reach the end of the next row while another still
+  // reads those of this one.
+  float stat[2][8][16][3];
+};
+static_assert(sizeof(Misc) <= 4096, "misc");
+// flags of a stage beside its tokens (0 to 64)
+constexpr int kBegin = 1 << 8;   // a row (or a piece of it) begins: reset, and queries come with it
+constexpr int kEnd = 1 << 9;     // ... ends
+constexpr int kWhole = 1 << 10;  // the piece is the whole row
+constexpr int kFirst = 1 << 11;  // the piece has the row's first unit
+constexpr int kBad = 1 << 12;    // a page that it needs is not in the pool
+constexpr int kDone = 1 << 13;   // the slice ends here: no unit
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// With results below 2^-126, down to 2^-149.
+__device__ __forceinline__ float ex2_small(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool FP16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (FP16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+
+// Two e4m3 codes as two fp16 values.
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  return (uint32_t)r.x | (uint32_t)r.y << 16;
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (FP16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                            int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// `bytes` (a multiple of 16, both addresses 16-byte aligned) to shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint64_t* bar, uint32_t bytes) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// A wait of a whole warp (every lane asks and gets the same answer).  After
+// one that ran out the rest return at once.
+struct Waiter {
+  int* status;
+  bool ok;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
+    if (!ok) return false;
+    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    const uint32_t t0 = (uint32_t)clock();
+#pragma unroll 1
+    do {
+      if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+      ok = !__any_sync(kAll, (uint32_t)clock() - t0 > kWaitLimit);
+    } while (ok);
+    raise_status(status, DSA_ERR_TIMEOUT);
+    return false;
+  }
+};
+
+// Units of a row: its pages, or its list's entries (those that name no page of
+// the row are passed over).  None for a row without tokens, or with more than
+// its table has room for.
+__device__ __forceinline__ int row_units(const PagedAttnParams& p, int len) {
+  if (len <= 0 || (long long)len > (long long)p.W * kPage) return 0;
+  return p.blocks ? p.k : (len - 1) / kPage + 1;
+}
+
+// Where the CTA's slice of the call's units begins and ends.  All threads.
+template <int THREADS>
+__device__ void find_slice(const PagedAttnParams& p, Misc* m) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_row = p.heads * p.tiles, each = (p.rows + THREADS - 1) / THREADS;
+  const int r0 = min((int)threadIdx.x * each, p.rows), r1 = min(r0 + each, p.rows);
+  int mine = 0;
+  for (int r = r0; r < r1; ++r) mine += row_units(p, __ldg(p.seqlens + r)) * per_row;
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) m->scan[warp] = before;
+  before -= mine;
+  __syncthreads();
+  int total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += m->scan[w];
+    total += m->scan[w];
+  }
+  const int share = max(1, (int)(((long long)total + gridDim.x - 1) / gridDim.x));
+  const int begin = (int)min((long long)blockIdx.x * share, (long long)total);
+  const int end = (int)min((long long)begin + share, (long long)total);
+  if (threadIdx.x == 0) m->begin = begin, m->end = end, m->share = share, m->total = total;
+  if (begin >= before && begin < before + mine) {
+    int at = before;
+    for (int r = r0; r < r1; ++r) {
+      const int n = row_units(p, __ldg(p.seqlens + r)), all = n * per_row;
+      if (begin < at + all) {
+        m->row = r, m->tile = (begin - at) / n, m->unit = (begin - at) % n;
+        break;
+      }
+      at += all;
+    }
+  }
+  __syncthreads();
+}
+
+// ---- the warp that loads ------------------------------------------------------
+
+template <int KV, int D, int MT>
+__device__ void produce(const PagedAttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, Misc* m,
+                        uint32_t stages) {
+  using S = Shape<KV, D, MT>;
+  const int lane = threadIdx.x & 31;
+  Waiter wait{p.status, true};
+  int stage = 0, issued = 0;
+  uint32_t phase = 1;                       // of the next empty wait: the first round passes
+  int left = m->end - m->begin;
+  if (left > 0) {
+    int row = m->row, tile = m->tile, unit = m->unit;
+    int len = __ldg(p.seqlens + row), n = row_units(p, len);
+    int at = m->begin;                      // index of `unit` among all
+    bool fresh = true;                      // the piece has had no stage yet
+    int bad = 0;
+    while (left > 0 && wait.ok) {
+      const int head = tile / p.tiles;
+      const int count = min(min(32, n - unit), left);
+      // 32 pages' places in the row, and their ids
+      int tokens = 0, page = -1;
+      if (lane < count) {
+        const int block = p.blocks ? __ldg(p.blocks + (long long)row * p.b_row + (long long)head * p.b_head + unit + lane)
+                                   : unit + lane;
+        if (block >= 0 && block <= (len - 1) / kPage) {
+          tokens = min(kPage, len - block * kPage);
+          page = __ldg(p.block_table + (long long)row * p.bt_stride + block);
+          if (page < 0 || page >= p.num_pages) page = -1;
+        }
+      }
+      if (__any_sync(kAll, tokens > 0 && page < 0)) bad = kBad;
+      const bool piece_ends = unit + count == n || count == left;
+      for (int i = 0; i < count; ++i) {
+        const int t = __shfl_sync(kAll, tokens, i), id = __shfl_sync(kAll, page, i);
+        const bool last = piece_ends && i + 1 == count, load = t > 0 && id >= 0;
+        if (!load && !last) continue;
+        if (!wait(&m->empty[stage], phase)) break;
+        if (lane == 0) {
+          int flags = (load ? t : 0) | (fresh ? kBegin : 0);
+          int last_cta = 0;
+          if (last) {
+            flags |= kEnd | bad;
+            const int first_unit = at - unit, end_unit = first_unit + n;
+            const bool begins = m->begin <= first_unit, ends = m->end >= end_unit;
+            if (begins) flags |= kFirst;
+            if (begins && ends) flags |= kWhole;
+            last_cta = (end_unit - 1) / m->share;
+          }
+          m->meta[stage] = make_int4(row, tile, flags, last_cta);
+          const uint32_t dst = stages + stage * S::kStage;
+          const int group0 = (tile % p.tiles) * S::kHeadsMax;
+          const int heads = min(S::kHeadsMax, p.group - group0);
+#ifdef DSA_TEST_SKIP_FIRST_TILE
+          const bool deliver = issued > 0;
+#else
+          constexpr bool deliver = true;
+#endif
+          uint32_t bytes = load ? 2 * S::kSide + 2 * S::kScaleBytes : 0;
+          if (load && fresh) bytes += heads * D * 2;
+          if (bytes && deliver) {
+            mbar_arrive_expect_tx(&m->full[stage], bytes);
+#pragma unroll
+            for (int b = 0; b < S::kBoxes; ++b) {
+              tma_load_4d(dst + b * S::kBox, kmap, &m->full[stage], b * 32, 0, head, id);
+              tma_load_4d(dst + S::kSide + b * S::kBox, vmap, &m->full[stage], b * 32, 0, head, id);
+            }
+            if (S::kFp8) {
+              const long long s = ((long long)id * p.heads + head) * kPage;
+              bulk_load(dst + S::kOffScale, p.k_scale + s, &m->full[stage], S::kScaleBytes);
+              bulk_load(dst + S::kOffScale + S::kScaleBytes, p.v_scale + s, &m->full[stage], S::kScaleBytes);
+            }
+            if (fresh) {
+              const uint16_t* q = p.q + (long long)row * p.q_row + (long long)(head * p.group + group0) * p.q_head;
+              if (p.q_head == D) {
+                bulk_load(dst + S::kOffQ, q, &m->full[stage], heads * D * 2);
+              } else {
+                for (int h = 0; h < heads; ++h)
+                  bulk_load(dst + S::kOffQ + h * D * 2, q + (long long)h * p.q_head, &m->full[stage], D * 2);
+              }
+            }
+          } else if (deliver) {
+            mbar_arrive(&m->full[stage]);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        fresh = false;
+        if (++stage == S::kStages) stage = 0, phase ^= 1;
+      }
+      unit += count, at += count, left -= count;
+      if (piece_ends && left > 0) {
+        unit = 0, fresh = true, bad = 0;
+        if (++tile == p.heads * p.tiles) {
+          tile = 0;
+          do {
+            len = __ldg(p.seqlens + ++row), n = row_units(p, len);
+          } while (n == 0 && row + 1 < p.rows);
+        }
+      }
+    }
+  }
+  // the end, for the consumers, in a stage that they have given back
+  const bool told = wait(&m->empty[stage], phase);
+  if (told && lane == 0) {
+    m->meta[stage] = make_int4(0, 0, kDone, 0);
+    mbar_arrive(&m->full[stage]);
+  }
+  // every copy has landed before the CTA's memory goes to another
+  Waiter landed{p.status, true};
+#ifdef DSA_TEST_SKIP_FIRST_TILE
+  const int first = 1;
+#else
+  const int first = 0;
+#endif
+  for (int i = max(first, issued - S::kStages + told); i < issued; ++i)
+    landed(&m->full[i % S::kStages], (i / S::kStages) & 1);
+}
+
+// ---- the warps that compute -----------------------------------------------------
+
+template <int KV, int D, int MT>
+struct Consumer {
+  using S = Shape<KV, D, MT>;
+  static constexpr bool kFp8 = S::kFp8;
+  static constexpr bool kHalf = KV != DSA_KV_BF16;    // the products' operands are fp16
+  static constexpr int kSteps = D / 16;               // k steps of S, and pairs of column tiles of O
+  static constexpr int kTiles = D / 8;                // column tiles of O
+
+  const PagedAttnParams& p;
+  Misc* m;
+  int warp, lane, g, t, slice, mt, heads;             // heads: of this warp's tile of 16
+  uint32_t qa[kSteps][4];
+  float o[kTiles][4];
+  float top[2], ref[2], sum[2], qf[2];                // rows g and g + 8
+  Waiter wait;
+  uint32_t meet_phase, turn;
+
+  __device__ Consumer(const PagedAttnParams& params, Misc* misc, int w, int l)
+      : p(params), m(misc), warp(w), lane(l), g(l >> 2), t(l & 3), slice(w & 3), mt(w >> 2), heads(0),
+        wait{params.status, true}, meet_phase(0), turn(0) {}
+
+  // All consumer warps.
+  __device__ __forceinline__ bool meet() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m->meet);
+    const bool r = wait(&m->meet, meet_phase);
+    meet_phase ^= 1;
+    return r;
+  }
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    top[0] = top[1] = ref[0] = ref[1] = -CUDART_INF_F;
+    sum[0] = sum[1] = 0.f;
+  }
+
+  // Queries of rows g and g + 8, in the order in which the keys are read.
+  __device__ __forceinline__ void load_queries(uint32_t q) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int row = mt * 16 + g + 8 * half;
+      const uint32_t at = q + row * (D * 2);
+      const bool there = g + 8 * half < heads;
+      if (!kFp8) {
+        // unit u = 2t + i of each 64 values: two steps
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 v = there ? lds128(at + b * 128 + (2 * t + i) * 16) : make_uint4(0, 0, 0, 0);
+            const int s = b * 4 + i * 2;
+            qa[s][half] = v.x, qa[s][half + 2] = v.y, qa[s + 1][half] = v.z, qa[s + 1][half + 2] = v.w;
+          }
+        continue;
+      }
+      // fp8: unit u of 16 values (2t + i of 8, or t of 4): four steps
+      constexpr int kUnits = D / 64;
+      uint32_t w[kUnits * 8];
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint4 v = there ? lds128(at + ((kUnits * t + i) * 2 + j) * 16) : make_uint4(0, 0, 0, 0);
+          const int k = i * 8 + j * 4;
+          w[k] = v.x, w[k + 1] = v.y, w[k + 2] = v.z, w[k + 3] = v.w;
+        }
+      auto low = [&](uint32_t u) {
+        return p.dtype == DSA_FP16 ? __half2float(__ushort_as_half((unsigned short)u)) : __uint_as_float(u << 16);
+      };
+      auto high = [&](uint32_t u) {
+        return p.dtype == DSA_FP16 ? __half2float(__ushort_as_half((unsigned short)(u >> 16)))
+                                   : __uint_as_float(u & 0xffff0000u);
+      };
+#pragma unroll
+      for (int k = 0; k < kUnits * 8; ++k) big = fmaxf(big, fmaxf(fabsf(low(w[k])), fabsf(high(w[k]))));
+      big = fmaxf(big, __shfl_xor_sync(kAll, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
+      // big < 2^x; queries times 2^(14 - x)
+      const int x = max((int)(__float_as_uint(big) >> 23) - 126, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - x) << 23);
+      qf[half] = __uint_as_float((uint32_t)(127 - 14 + x) << 23) * p.scale_log2;
+#pragma unroll
+      for (int k = 0; k < kUnits * 8; ++k) w[k] = pack2<true>(low(w[k]) * up, high(w[k]) * up);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) qa[s][half] = w[2 * s], qa[s][half + 2] = w[2 * s + 1];
+    }
+    if (!kFp8) qf[0] = qf[1] = p.scale_log2;
+  }
+
+  // S for the warp's 16 tokens: two column tiles of 8.
+  __device__ __forceinline__ void scores(uint32_t k, float (&s)[2][4]) {
+    float even[2][4], odd[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) even[j][c] = odd[j][c] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int token = slice * 16 + j * 8 + g;          // g: the column of a B fragment
+      if (!kFp8) {
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 v = lds128(k + b * S::kBox + token * 128 + (((2 * t + i) ^ (token & 7)) << 4));
+            const int st = b * 4 + i * 2;
+            mma16816<kHalf>(even[j], qa[st], v.x, v.y);
+            mma16816<kHalf>(odd[j], qa[st + 1], v.z, v.w);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const uint32_t at = D == 128 ? token * 128 + (((2 * t + i) ^ (token & 7)) << 4)
+                                       : token * 64 + ((t ^ ((token >> 1) & 3)) << 4);
+          const uint4 v = lds128(k + at);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float(&into)[4] = (c & 1) ? odd[j] : even[j];
+            mma16816<true>(into, qa[i * 4 + c], widen2(w[c] & 0xffffu), widen2(w[c] >> 16));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[j][c] = even[j][c] + odd[j][c];
+  }
+
+  // O += P * V; `keep`: masks of the tokens 2t, 2t + 1 (low and high half) and
+  // + 8 of a page that ends inside the warp's tokens.
+  template <bool CUT>
+  __device__ __forceinline__ void values(uint32_t v, const uint32_t (&pa)[4], uint32_t keep0, uint32_t keep1) {
+    if (!kFp8) {
+      // matrices of 8 tokens x 8 values: tokens 0-7 and 8-15 of two column tiles
+      const int token = slice * 16 + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < kTiles; j += 2) {
+        const int unit = j + (lane >> 4);                // of 16 bytes
+        uint32_t b[4];
+        ldmatrix_t(b, v + (unit >> 3) * S::kBox + token * 128 + (((unit & 7) ^ (token & 7)) << 4));
+        if (CUT) b[0] &= keep0, b[1] &= keep1, b[2] &= keep0, b[3] &= keep1;
+        mma16816<kHalf>(o[j], pa, b[0], b[1]);
+        mma16816<kHalf>(o[j + 1], pa, b[2], b[3]);
+      }
+      return;
+    }
+    // lane column g holds the D / 8 values from D / 8 * g on: one per column tile
+    constexpr int kWords = D / 32;
+    uint32_t w[4][kWords];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int token = slice * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+      if (D == 128) {
+        const uint4 x = lds128(v + token * 128 + ((g ^ (token & 7)) << 4));
+        w[i][0] = x.x, w[i][1] = x.y, w[i][kWords - 2] = x.z, w[i][kWords - 1] = x.w;
+      } else {
+        const uint2 x = lds64(v + token * 64 + (((g >> 1) ^ ((token >> 1) & 3)) << 4) + (g & 1) * 8);
+        w[i][0] = x.x, w[i][1] = x.y;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kWords; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // codes of two tokens side by side: (2t, 2t + 1) and (2t + 8, 2t + 9), two values each
+        const uint32_t a = __byte_perm(w[0][c], w[1][c], h ? 0x7362 : 0x5140);
+        const uint32_t b = __byte_perm(w[2][c], w[3][c], h ? 0x7362 : 0x5140);
+        uint32_t a0 = widen2(a & 0xffffu), a1 = widen2(a >> 16), b0 = widen2(b & 0xffffu), b1 = widen2(b >> 16);
+        if (CUT) a0 &= keep0, a1 &= keep0, b0 &= keep1, b1 &= keep1;
+        mma16816<true>(o[c * 4 + h * 2], pa, a0, b0);
+        mma16816<true>(o[c * 4 + h * 2 + 1], pa, a1, b1);
+      }
+  }
+
+  __device__ __forceinline__ void page(uint32_t stage, int tokens) {
+    if (tokens <= slice * 16) return;
+    float s[2][4];
+    scores(stage, s);
+    const int valid = tokens - slice * 16;               // of the warp's 16
+    // this lane's tokens: 8 j + 2 t and the next
+    float e[2][2], f[2][2];                              // fp8: exponent and mantissa of the value scales
+    if (kFp8) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t at = stage + S::kOffScale + (slice * 16 + 8 * j + 2 * t) * 4;
+        const uint2 ks = lds64(at), vs = lds64(at + S::kScaleBytes);
+        const uint32_t bits[2] = {vs.x, vs.y};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int x = (int)(bits[c] >> 23 & 255u);
+          e[j][c] = (float)(x - 127);
+          f[j][c] = x ? __uint_as_float((bits[c] & 0x807fffffu) | 0x3f800000u)
+                      : __uint_as_float(bits[c]) * 1.7014118346046923e38f;  // 2^127
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          s[j][c] = s[j][c] * qf[c >> 1] * __uint_as_float((c & 1) ? ks.y : ks.x);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[j][c] *= p.scale_log2;
+    }
+    if (valid < 16) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (8 * j + 2 * t + (c & 1) >= valid) s[j][c] = -CUDART_INF_F;
+    }
+    uint32_t pa[4];
+    float shrink[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int a = 2 * half, b = a + 1;
+      float big = fmaxf(fmaxf(s[0][a], s[0][b]), fmaxf(s[1][a], s[1][b]));
+      big = fmaxf(big, __shfl_xor_sync(kAll, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
+      const float now = fmaxf(top[half], big), base = now == -CUDART_INF_F ? 0.f : now;
+      const float p0 = ex2(s[0][a] - base), p1 = ex2(s[0][b] - base), p2 = ex2(s[1][a] - base),
+                  p3 = ex2(s[1][b] - base);
+      const float less = ex2(top[half] - base);
+      sum[half] = sum[half] * less + ((p0 + p1) + (p2 + p3));
+      top[half] = now;
+      if (!kFp8) {
+        shrink[half] = less;
+        pa[half] = pack2<kHalf>(p0, p1), pa[half + 2] = pack2<kHalf>(p2, p3);
+      } else {
+        const float y0 = s[0][a] + e[0][0], y1 = s[0][b] + e[0][1], y2 = s[1][a] + e[1][0], y3 = s[1][b] + e[1][1];
+        float high = fmaxf(fmaxf(y0, y1), fmaxf(y2, y3));
+        high = fmaxf(high, __shfl_xor_sync(kAll, high, 1));
+        high = fmaxf(high, __shfl_xor_sync(kAll, high, 2));
+        const float next = fmaxf(ref[half], high), from = (next == -CUDART_INF_F ? 0.f : next) - 13.f;
+        shrink[half] = ex2(ref[half] - (from + 13.f));
+        ref[half] = next;
+        pa[half] = pack2<true>(ex2(y0 - from) * f[0][0], ex2(y1 - from) * f[0][1]);
+        pa[half + 2] = pack2<true>(ex2(y2 - from) * f[1][0], ex2(y3 - from) * f[1][1]);
+      }
+    }
+    if (__any_sync(kAll, shrink[0] != 1.f || shrink[1] != 1.f)) {
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+        o[j][0] *= shrink[0], o[j][1] *= shrink[0], o[j][2] *= shrink[1], o[j][3] *= shrink[1];
+    }
+    if (valid >= 16) {
+      values<false>(stage + S::kSide, pa, 0, 0);
+    } else {
+      // masked tokens may hold anything, and 0 * NaN is NaN
+      auto mask = [&](int token) {
+        return (token < valid ? 0xffffu : 0u) | (token + 1 < valid ? 0xffff0000u : 0u);
+      };
+      values<true>(stage + S::kSide, pa, mask(2 * t), mask(2 * t + 8));
+    }
+  }
+
+  // Column of O's register c (0 or 1 of a row) of column tile j.
+  __device__ __forceinline__ int column(int j, int c) const {
+    return kFp8 ? (D / 8) * (2 * t + c) + j : 8 * j + 2 * t + c;
+  }
+
+  // A row's four slices of tokens meet in the stage; results or partial sums go out.
+  __device__ __forceinline__ void finish(uint8_t* stage, int4 meta) {
+    float(*stats)[16][3] = m->stat[turn];
+    turn ^= 1;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      sum[half] += __shfl_xor_sync(kAll, sum[half], 1);
+      sum[half] += __shfl_xor_sync(kAll, sum[half], 2);
+      if (!kFp8) ref[half] = top[half];
+      if (t == 0) {
+        float* s = stats[warp][g + 8 * half];
+        s[0] = top[half], s[1] = ref[half], s[2] = sum[half];
+      }
+    }
+    if (!meet()) return;
+    const int group0 = (meta.y % p.tiles) * S::kHeadsMax, key_head = meta.y / p.tiles;
+    const int all = min(S::kHeadsMax, p.group - group0);  // of the CTA
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float high = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) high = fmaxf(high, stats[mt * 4 + w][g + 8 * half][1]);
+      const float f = ref[half] == -CUDART_INF_F ? 0.f : ex2(ref[half] - high);
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) o[j][2 * half] *= f, o[j][2 * half + 1] *= f;
+    }
+    const bool whole = meta.z & kWhole;
+    const int piece = (meta.z & kFirst) ? 1 : 0;
+    const int hv = paged_cta_heads(p.group);
+    float* part = p.ws + ((long long)blockIdx.x * 2 + piece) * hv * (D + 4);
+    float* parts = reinterpret_cast<float*>(stage);
+#pragma unroll 1
+    for (int pass = 0; pass < S::kPasses; ++pass) {
+      // slices of a column chunk; groups of 8 columns are permuted by row against bank conflicts
+      auto place = [&](int col, int row) { return col ^ ((((row & 7) ^ ((col >> 5) & 3)) << 3) & (S::kCols - 1)); };
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = column(j, c & 1) - pass * S::kCols, row = mt * 16 + g + 8 * (c >> 1);
+          if (col >= 0 && col < S::kCols) parts[(slice * S::kHeadsMax + row) * S::kCols + place(col, row)] = o[j][c];
+        }
+      if (!meet()) return;
+      constexpr int kGroups = S::kCols / 8;
+      for (int i = warp * 32 + lane; i < all * kGroups; i += S::kConsumers * 32) {
+        const int row = i / kGroups, col = (i % kGroups) * 8;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4* from =
+              reinterpret_cast<const float4*>(parts + (w * S::kHeadsMax + row) * S::kCols + place(col, row));
+          const float4 a = from[0], b = from[1];
+          x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w, x[4] += b.x, x[5] += b.y, x[6] += b.z, x[7] += b.w;
+        }
+        const float(*st)[16][3] = stats + (row >> 4) * 4;
+        float big = -CUDART_INF_F, high = -CUDART_INF_F, total = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) big = fmaxf(big, st[w][row & 15][0]), high = fmaxf(high, st[w][row & 15][1]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float l = st[w][row & 15][2];
+          // a slice without tokens has no maximum; a NaN total stays one
+          total += st[w][row & 15][0] == -CUDART_INF_F ? l : l * ex2(st[w][row & 15][0] - big);
+        }
+        if (meta.z & kBad) total = CUDART_NAN_F;
+        const int c0 = pass * S::kCols + col;
+        if (!whole) {
+          float4* to = reinterpret_cast<float4*>(part + (long long)row * D + c0);
+          to[0] = make_float4(x[0], x[1], x[2], x[3]), to[1] = make_float4(x[4], x[5], x[6], x[7]);
+          if (c0 == 0)
+            *reinterpret_cast<float4*>(part + (long long)hv * D + row * 4) = make_float4(big, high, total, 0.f);
+          continue;
+        }
+        write_out(p, meta.x, key_head * p.group + group0 + row, c0, x, big, high, total);
+      }
+      if (pass + 1 < S::kPasses && !meet()) return;
+    }
+    if ((meta.z & kBad) && warp == 0 && lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
+    if (!whole && piece == 1 && warp == 0 && lane == 0) {
+      int4* record = reinterpret_cast<int4*>(p.ws + (long long)gridDim.x * 2 * hv * (D + 4)) + blockIdx.x;
+      *record = make_int4(meta.x, meta.y, meta.w, 0);
+    }
+  }
+
+  // Eight values of a head's result: the sums x under `high`, the total under `big`.
+  static __device__ __forceinline__ void write_out(const PagedAttnParams& p, int row, int head, int c0, float (&x)[8],
+                                                   float big, float high, float total) {
+    // no visible token: zeros, -inf
+    const float f = total == 0.f ? 0.f : (kFp8 ? 1.f / 8192.f : 1.f) / total;
+    const float unit = kFp8 ? ex2_small(high - big) : 1.f;  // of the size of the value scales
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = total == 0.f ? 0.f : x[2 * i] * f * unit, b = total == 0.f ? 0.f : x[2 * i + 1] * f * unit;
+      w[i] = p.dtype == DSA_FP16 ? pack2<true>(a, b) : pack2<false>(a, b);
+    }
+    *reinterpret_cast<uint4*>(p.out + (long long)row * p.out_row + (long long)head * p.out_head + c0) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+    if (c0 == 0 && p.lse)
+      p.lse[(long long)row * p.heads * p.group + head] =
+          total == 0.f ? -CUDART_INF_F : (big + log2f(total)) * 0.69314718055994531f;
+  }
+
+  // NaN or zeros into a row's heads [h0, h1), by `count` threads of which this one is `me`.
+  __device__ void fill(int row, int h0, int h1, bool nan, int me, int count) {
+    const uint32_t v = nan ? 0x7fff7fffu : 0u;           // NaN in either type
+    for (int i = h0 * (D / 8) + me; i < h1 * (D / 8); i += count) {
+      const int h = i / (D / 8), c0 = i % (D / 8) * 8;
+      *reinterpret_cast<uint4*>(p.out + (long long)row * p.out_row + (long long)h * p.out_head + c0) =
+          make_uint4(v, v, v, v);
+      if (c0 == 0 && p.lse) p.lse[(long long)row * p.heads * p.group + h] = nan ? CUDART_NAN_F : -CUDART_INF_F;
+    }
+  }
+
+  // Rows without units: zeros, or NaN where the length is past the table.
+  __device__ void empty_rows() {
+    for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
+      const int len = __ldg(p.seqlens + row);
+      if (row_units(p, len) > 0) continue;
+      const bool bad = len > 0;
+      if (bad && warp == 0 && lane == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
+      fill(row, 0, p.heads * p.group, bad, warp * 32 + lane, S::kConsumers * 32);
+    }
+  }
+
+  // After a wait that ran out: NaN for every row of the slice, and for its partial results.
+  __device__ void poison() {
+    const int hv = paged_cta_heads(p.group);
+    float* part = p.ws + (long long)blockIdx.x * 2 * hv * (D + 4);
+    for (int i = lane; i < 2 * hv; i += 32)
+      *reinterpret_cast<float4*>(part + (long long)(i / hv) * hv * (D + 4) + (long long)hv * D + (i % hv) * 4) =
+          make_float4(0.f, 0.f, CUDART_NAN_F, 0.f);
+    int left = m->end - m->begin, row = m->row, tile = m->tile, unit = m->unit;
+    while (left > 0) {
+      const int n = row_units(p, __ldg(p.seqlens + row));
+      if (n == 0) {
+        ++row;
+        continue;
+      }
+      const int group0 = (tile % p.tiles) * S::kHeadsMax, h0 = (tile / p.tiles) * p.group + group0;
+      fill(row, h0, h0 + min(S::kHeadsMax, p.group - group0), true, lane, 32);
+      left -= min(left, n - unit);
+      unit = 0;
+      if (++tile == p.heads * p.tiles) tile = 0, ++row;
+    }
+  }
+
+  __device__ void run(uint8_t* smem) {
+    if (warp == 0 && lane == 0) {
+      const int hv = paged_cta_heads(p.group);
+      reinterpret_cast<int4*>(p.ws + (long long)gridDim.x * 2 * hv * (D + 4))[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+    empty_rows();
+    int stage = 0;
+    uint32_t phase = 0;
+    reset();
+    while (wait(&m->full[stage], phase)) {
+      const int4 meta = m->meta[stage];
+      if (meta.z & kDone) return;
+      uint8_t* at = smem + stage * S::kStage;
+      const uint32_t base = smem_u32(at);
+      const int tokens = meta.z & 127;
+      if (meta.z & kBegin) {
+        reset();
+        heads = min(max(p.group - (meta.y % p.tiles) * S::kHeadsMax - mt * 16, 0), 16);
+        if (tokens) load_queries(base + S::kOffQ);
+      }
+      if (heads > 0) page(base, tokens);
+      if (meta.z & kEnd) {
+        finish(at, meta);
+        if (!wait.ok) break;
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m->empty[stage]);
+      if (++stage == S::kStages) stage = 0, phase ^= 1;
+    }
+    poison();
+  }
+};
+
+template <int KV, int D, int MT>
+__global__ void __launch_bounds__(Shape<KV, D, MT>::kThreads, Shape<KV, D, MT>::kCtas)
+    paged_attention_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap) {
+  using S = Shape<KV, D, MT>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  Misc* m = reinterpret_cast<Misc*>(smem + S::kStages * S::kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&m->full[i], 1);
+      mbar_init(&m->empty[i], S::kConsumers);
+    }
+    mbar_init(&m->meet, S::kConsumers);
+    fence_barrier_init();
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  find_slice<S::kThreads>(p, m);             // its barriers also publish the mbarriers
+  if (warp == S::kConsumers) {
+    produce<KV, D, MT>(p, &kmap, &vmap, m, smem_u32(smem));
+  } else {
+    Consumer<KV, D, MT> c(p, m, warp, lane);
+    c.run(smem);
+  }
+}
+
+// ---- the join -------------------------------------------------------------------
+
+constexpr int kJoinThreads = 128;
+
+// Block (c, h): head h of the row whose units CTA c begins and does not end.
+template <int KV, int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int ctas,
+                                                                  int heads_max) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  __shared__ float weight[kJoinThreads];
+  __shared__ float4 stat[kJoinThreads / 32];
+  __shared__ alignas(16) float sums[kGroups][D];
+  const int hv = paged_cta_heads(p.group), h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int4 record = *(reinterpret_cast<const int4*>(p.ws + (long long)ctas * 2 * hv * (D + 4)) + blockIdx.x);
+  const int first = blockIdx.x, row = record.x, tile = record.y, last = record.z;
+  // addresses come from it, and the workspace is the caller's
+  if (row < 0 || row >= p.rows || tile < 0 || tile >= p.heads * p.tiles || last <= first || last >= ctas) return;
+  const int group0 = (tile % p.tiles) * heads_max;
+  if (h >= p.group - group0) return;
+  const int pieces = last - first + 1;
+  auto part = [&](int i) { return p.ws + ((long long)(first + i) * 2 + (i == 0)) * hv * (D + 4); };
+  // the largest maximum and reference
+  float big = -CUDART_INF_F, high = -CUDART_INF_F;
+  for (int i = threadIdx.x; i < pieces; i += kJoinThreads) {
+    const float4 s = *reinterpret_cast<const float4*>(part(i) + (long long)hv * D + h * 4);
+    big = fmaxf(big, s.x), high = fmaxf(high, s.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    big = fmaxf(big, __shfl_xor_sync(kAll, big, o)), high = fmaxf(high, __shfl_xor_sync(kAll, high, o));
+  if (lane == 0) stat[warp] = make_float4(big, high, 0.f, 0.f);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) big = fmaxf(big, stat[w].x), high = fmaxf(high, stat[w].y);
+  // four columns a thread, several groups of pieces
+  const int col = threadIdx.x % kLanes * 4, group = threadIdx.x / kLanes;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+  for (int i0 = 0; i0 < pieces; i0 += kJoinThreads) {
+    const int n = min(kJoinThreads, pieces - i0);
+    __syncthreads();
+    if (threadIdx.x < n) {
+      const float4 s = *reinterpret_cast<const float4*>(part(i0 + threadIdx.x) + (long long)hv * D + h * 4);
+      weight[threadIdx.x] = s.y == -CUDART_INF_F ? 0.f : ex2(s.y - high);
+      total += s.x == -CUDART_INF_F ? s.z : s.z * ex2(s.x - big);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int i = group; i < n; i += kGroups) {
+      const float4 v = *reinterpret_cast<const float4*>(part(i0 + i) + (long long)h * D + col);
+      const float w = weight[i];
+      x.x += w * v.x, x.y += w * v.y, x.z += w * v.z, x.w += w * v.w;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  *reinterpret_cast<float4*>(&sums[group][col]) = x;
+  __syncthreads();
+  if (lane == 0) stat[warp].z = total;
+  __syncthreads();
+  total = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) total += stat[w].z;
+  if (threadIdx.x < D / 8) {
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int c0 = threadIdx.x * 8;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += sums[k][c0 + i];
+    Consumer<KV, D, 1>::write_out(p, row, (tile / p.tiles) * p.group + group0 + h, c0, y, big, high, total);
+  }
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int KV, int D, int MT>
+cudaError_t launch_t(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
+                     cudaStream_t stream) {
+  using S = Shape<KV, D, MT>;
+  static bool ready[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !ready[dev]) {
+    e = cudaFuncSetAttribute(paged_attention_kernel<KV, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ready[dev] = true;
+  }
+  const int ctas = sms * S::kCtas;
+  e = launch(paged_attention_kernel<KV, D, MT>, dim3(ctas), S::kThreads, S::kSmem, stream, p, kmap, vmap);
+  if (e != cudaSuccess) return e;
+  return launch(paged_join_kernel<KV, D>, dim3(ctas, paged_cta_heads(p.group)), kJoinThreads, 0, stream, p, ctas,
+                S::kHeadsMax);
+}
+
+template <int KV, int D>
+cudaError_t launch_d(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
+                     cudaStream_t stream) {
+  return paged_head_tiles(p.group) == 1 ? launch_t<KV, D, 1>(p, kmap, vmap, sms, stream)
+                                        : launch_t<KV, D, 2>(p, kmap, vmap, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attention(const PagedAttnParams& p, int dim, int kv_dtype, const CUtensorMap& kmap,
+                                   const CUtensorMap& vmap, int sms, cudaStream_t stream) {
+  if (kv_dtype == DSA_KV_BF16)
+    return dim == 128 ? launch_d<DSA_KV_BF16, 128>(p, kmap, vmap, sms, stream)
+                      : launch_d<DSA_KV_BF16, 64>(p, kmap, vmap, sms, stream);
+  if (kv_dtype == DSA_KV_FP16)
+    return dim == 128 ? launch_d<DSA_KV_FP16, 128>(p, kmap, vmap, sms, stream)
+                      : launch_d<DSA_KV_FP16, 64>(p, kmap, vmap, sms, stream);
+  return dim == 128 ? launch_d<DSA_KV_FP8_E4M3, 128>(p, kmap, vmap, sms, stream)
+                    : launch_d<DSA_KV_FP8_E4M3, 64>(p, kmap, vmap, sms, stream);
+}
+
+}  // namespace dsa

@@ -29,9 +29,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // everything the encoding reads; direct-mapped, guarded by a mutex.
 struct MapKey {
   const void* base;
-  unsigned long long dims[3], strides[2];
-  unsigned box[3];
-  int rank;
+  unsigned long long dims[4], strides[3];
+  unsigned box[4];
+  int rank, swizzle;
   bool operator==(const MapKey& o) const { return memcmp(this, &o, sizeof o) == 0; }
 };
 
@@ -52,13 +52,15 @@ int cache_slot(const MapKey& k) {
   return (int)(h % kMapCacheSize);
 }
 
-// Encode (or fetch) a 4-byte-unit, 128-byte-swizzle tiled map.
+// Encode (or fetch) a 4-byte-unit tiled map, 128-byte swizzle unless given.
 bool encode_cached(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims,
-                   const cuuint64_t* strides, const cuuint32_t* box) {
+                   const cuuint64_t* strides, const cuuint32_t* box,
+                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   MapKey k;
   memset(&k, 0, sizeof k);
   k.base = base;
   k.rank = rank;
+  k.swizzle = (int)swizzle;
   for (int i = 0; i < rank; ++i) {
     k.dims[i] = dims[i];
     k.box[i] = box[i];
@@ -74,9 +76,9 @@ bool encode_cached(CUtensorMap* m, int rank, const void* base, const cuuint64_t*
   }
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint32_t estr[3] = {1, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, rank, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
   std::lock_guard<std::mutex> g(g_cache_mutex);
@@ -117,6 +119,20 @@ bool encode_q_map(CUtensorMap* m, const RowsParams& p, int box_rows) {
   cuuint64_t strides[1] = {(cuuint64_t)kDim * 2};
   cuuint32_t box[2] = {32u, (cuuint32_t)box_rows};
   return encode_cached(m, 2, p.q, dims, strides, box);
+}
+
+// Pool of a key/value cache: dims {row bytes / 4, 64 slots, heads, pages}
+// through its strides, box = one head's 64 slots, 128 bytes of each (64 where
+// a row has no more, in the 64-byte swizzle).
+bool encode_kv_pool_map(CUtensorMap* m, const void* base, int row_bytes, long long slot_bytes,
+                        long long head_bytes, long long page_bytes, int heads, int num_pages) {
+  const int box_bytes = row_bytes < 128 ? row_bytes : 128;
+  cuuint64_t dims[4] = {(cuuint64_t)row_bytes / 4, (cuuint64_t)kPage, (cuuint64_t)heads,
+                        (cuuint64_t)num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)slot_bytes, (cuuint64_t)head_bytes, (cuuint64_t)page_bytes};
+  cuuint32_t box[4] = {(cuuint32_t)box_bytes / 4, (cuuint32_t)kPage, 1u, 1u};
+  return encode_cached(m, 4, base, dims, strides, box,
+                       box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace dsa

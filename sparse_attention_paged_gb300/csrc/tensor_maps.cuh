@@ -20,4 +20,9 @@ bool encode_kcache_map(CUtensorMap* m, const RowsParams& p);
 // 128-byte swizzle.
 bool encode_q_map(CUtensorMap* m, const RowsParams& p, int box_rows);
 
+// Pool of a key/value cache [pages, heads, 64 slots, row bytes] through its
+// strides (bytes); box = up to 128 bytes of one head's 64 slots of a page.
+bool encode_kv_pool_map(CUtensorMap* m, const void* base, int row_bytes, long long slot_bytes,
+                        long long head_bytes, long long page_bytes, int heads, int num_pages);
+
 }  // namespace dsa

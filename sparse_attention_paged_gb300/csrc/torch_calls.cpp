@@ -305,11 +305,218 @@ PyObject* latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---- the paged cache of keys and values with grouped heads ----
+
+int* writable(const int* p) { return const_cast<int*>(p); }
+
+int type16(const at::Tensor* t, const char* what) {
+  need(t && (t->scalar_type() == at::kBFloat16 || t->scalar_type() == at::kHalf), what);
+  return t->scalar_type() == at::kHalf ? DSA_FP16 : DSA_BF16;
+}
+
+// [n, heads, D] of 16-bit values, a head's values adjacent.
+struct Heads {
+  void* at;
+  int64_t n, heads, dim;
+  long long row, head;
+  int dtype;
+};
+
+Heads heads_of(const at::Tensor* t, const char* what) {
+  const int dtype = type16(t, what);
+  need(t->dim() == 3 && t->stride(2) == 1, what);
+  // a dimension of one has any stride
+  return Heads{ptr(t), t->size(0), t->size(1), t->size(2), t->size(0) > 1 ? t->stride(0) : t->size(2),
+               t->size(1) > 1 ? t->stride(1) : t->size(2), dtype};
+}
+
+// A cache [pages, 64, heads, D].
+struct Cache {
+  void* at;
+  long long page, slot, head;
+  int64_t pages, heads, dim;
+  int kv;
+};
+
+Cache cache_of(const at::Tensor* t, const char* what) {
+  need(t && t->dim() == 4 && t->size(1) == 64 && t->stride(3) == 1, what);
+  const auto type = t->scalar_type();
+  const int kv = type == at::kBFloat16 ? DSA_KV_BF16 : type == at::kHalf ? DSA_KV_FP16 : type == at::kFloat8_e4m3fn ? DSA_KV_FP8_E4M3 : -1;
+  need(kv >= 0, what);
+  return Cache{ptr(t), t->stride(0), t->stride(1), t->stride(2), t->size(0), t->size(2), t->size(3), kv};
+}
+
+const float* scales_of(const at::Tensor* t, const Cache& c, const char* what) {
+  if (c.kv != DSA_KV_FP8_E4M3) {
+    need(!t, "k_scale, v_scale: for an fp8 cache only");
+    return nullptr;
+  }
+  need(t && t->scalar_type() == at::kFloat && t->dim() == 3 && t->size(0) == c.pages && t->size(1) == c.heads &&
+           t->size(2) == 64 && t->is_contiguous(),
+       what);
+  return static_cast<const float*>(ptr(t));
+}
+
+constexpr const char* kKCache = "k_cache: [pages, 64, Hkv, D] of bfloat16, float16 or float8_e4m3fn, values adjacent";
+constexpr const char* kVCache = "v_cache: like k_cache";
+constexpr const char* kKScale = "k_scale: contiguous float32 [pages, Hkv, 64] for an fp8 cache";
+constexpr const char* kVScale = "v_scale: contiguous float32 [pages, Hkv, 64] for an fp8 cache";
+
+Cache values_of(const at::Tensor* t, const Cache& k) {
+  const Cache v = cache_of(t, kVCache);
+  need(v.kv == k.kv && v.pages == k.pages && v.heads == k.heads && v.dim == k.dim, kVCache);
+  return v;
+}
+
+// lengths, new_tokens, free_pages, block_table, n, slots, positions, seqlens,
+// cu_rows, used, dev_status, stream
+PyObject* request_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 12, [&] {
+    const at::Tensor *lengths = tensor(a[0], "lengths"), *free_pages = tensor(a[2], "free_pages");
+    const int* held = ints(lengths, "lengths", -1);
+    need(lengths, "lengths: int32 [requests] expected");
+    const int64_t req = lengths->size(0);
+    const at::Tensor* fresh = tensor(a[1], "new_tokens");
+    need(fresh && free_pages, "new_tokens and free_pages: int32 tensors expected");
+    const int* fresh_at = ints(fresh, "new_tokens", req);
+    const int* pages = ints(free_pages, "free_pages", -1);
+    const at::Tensor* t = tensor(a[3], "block_table");
+    need(t && t->dim() == 2 && t->size(0) == req, "block_table: int32 [requests, W] expected");
+    const Table table = table_of(t, req);
+    const int rows = small(a[4]);
+    const at::Tensor* slots = tensor(a[5], "slots");
+    need(slots, "slots: int32 [n] expected");
+    return launch(dsa_request_slots, a[11], held, fresh_at, size32(req), pages, size32(free_pages->size(0)),
+                  writable(table.at), table.stride, table.W, 64, rows, writable(ints(slots, "slots", rows)),
+                  writable(ints(tensor(a[6], "positions"), "positions", rows)),
+                  writable(ints(tensor(a[7], "seqlens"), "seqlens", req)),
+                  writable(ints(tensor(a[8], "cu_rows"), "cu_rows", req + 1)),
+                  writable(ints(tensor(a[9], "used"), "used", 1)), status_word(a[10]));
+  });
+}
+
+// k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, dev_status, stream
+PyObject* kv_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 9, [&] {
+    const Heads k = heads_of(tensor(a[0], "k"), "k: bfloat16 or float16 [n, Hkv, D], values adjacent");
+    const Heads v = heads_of(tensor(a[1], "v"), "v: like k");
+    need(v.n == k.n && v.heads == k.heads && v.dim == k.dim && v.dtype == k.dtype, "v: like k");
+    const Cache kc = cache_of(tensor(a[3], "k_cache"), kKCache), vc = values_of(tensor(a[4], "v_cache"), kc);
+    need(kc.heads == k.heads && kc.dim == k.dim, "k_cache: k's heads and values");
+    const at::Tensor* slot_tensor = tensor(a[2], "slot_mapping");
+    need(slot_tensor, "slot_mapping: int32 [n] expected");
+    const int* slots = ints(slot_tensor, "slot_mapping", k.n);
+    const float* ks = scales_of(tensor(a[5], "k_scale"), kc, kKScale);
+    const float* vs = scales_of(tensor(a[6], "v_scale"), vc, kVScale);
+    return launch(dsa_kv_store, a[8], k.at, k.row, k.head, v.at, v.row, v.head, size32(k.n), size32(k.heads), size32(k.dim),
+                  k.dtype, slots, kc.at, kc.page, kc.slot, kc.head, vc.at, vc.page, vc.slot, vc.head,
+                  const_cast<float*>(ks), const_cast<float*>(vs), size32(kc.pages), kc.kv, 64, status_word(a[7]));
+  });
+}
+
+// bounds and their scales, for `pages` pages of `heads` heads of `dim` values
+signed char* bounds_of(const at::Tensor* t, int64_t pages, int64_t heads, int64_t dim) {
+  need(t && t->scalar_type() == at::kChar && t->dim() == 4 && t->size(0) == pages && t->size(1) == heads &&
+           t->size(2) == 2 && t->size(3) == dim && t->is_contiguous(),
+       "bounds: contiguous int8 [pages, Hkv, 2, D]");
+  return static_cast<signed char*>(ptr(t));
+}
+
+// k_cache, block_table, starts, seqlens, max_tokens, bounds, bound_scale,
+// k_scale, dev_status, stream
+PyObject* block_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 10, [&] {
+    const Cache c = cache_of(tensor(a[0], "k_cache"), kKCache);
+    const at::Tensor* lens = tensor(a[3], "seqlens");
+    need(lens, "seqlens: int32 [requests] expected");
+    const int* seqlens = ints(lens, "seqlens", -1);
+    const int64_t req = lens->size(0);
+    const int* starts = ints(tensor(a[2], "starts"), "starts", req);
+    const Table t = table_of(tensor(a[1], "block_table"), req);
+    signed char* bounds = bounds_of(tensor(a[5], "bounds"), c.pages, c.heads, c.dim);
+    const at::Tensor* scale = tensor(a[6], "bound_scale");
+    need(scale, "bound_scale: float32 [pages, Hkv] expected");
+    const float* unit = floats(scale, "bound_scale", c.pages, c.heads);
+    const float* ks = scales_of(tensor(a[7], "k_scale"), c, kKScale);
+    return launch(dsa_block_bounds, a[9], c.at, c.page, c.slot, c.head, ks, size32(c.pages), c.kv, size32(c.heads),
+                  size32(c.dim), 64, t.at, t.stride, t.W, starts, seqlens, size32(req), small(a[4]), bounds,
+                  const_cast<float*>(unit), status_word(a[8]));
+  });
+}
+
+// q, bounds, bound_scale, block_table, seqlens, k, first, last, out,
+// dev_status, stream
+PyObject* block_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 11, [&] {
+    const Heads q = heads_of(tensor(a[0], "q"), "q: bfloat16 or float16 [rows, Hq, D], values adjacent");
+    const at::Tensor* b = tensor(a[1], "bounds");
+    need(b && b->dim() == 4, "bounds: contiguous int8 [pages, Hkv, 2, D]");
+    const int64_t pages = b->size(0), heads = b->size(1);
+    signed char* bounds = bounds_of(b, pages, heads, q.dim);
+    const at::Tensor* scale = tensor(a[2], "bound_scale");
+    need(scale, "bound_scale: float32 [pages, Hkv] expected");
+    const float* unit = floats(scale, "bound_scale", pages, heads);
+    const at::Tensor* lens = tensor(a[4], "seqlens");
+    need(lens, "seqlens: int32 [rows] expected");
+    const int* seqlens = ints(lens, "seqlens", q.n);
+    const Table t = table_of(tensor(a[3], "block_table"), q.n);
+    const int k = small(a[5]);
+    const at::Tensor* out = tensor(a[8], "out");
+    need(out && out->scalar_type() == at::kInt && out->dim() == 3 && out->size(0) == q.n && out->size(1) == heads &&
+             out->size(2) == k && out->is_contiguous(),
+         "out: contiguous int32 [rows, Hkv, k]");
+    return launch(dsa_block_select, a[10], q.at, q.row, q.head, size32(q.n), size32(q.heads), size32(heads), size32(q.dim),
+                  q.dtype, bounds, unit, size32(pages), t.at, t.stride, t.W, 64, seqlens, k, small(a[6]), small(a[7]),
+                  static_cast<int*>(ptr(out)), status_word(a[9]));
+  });
+}
+
+// q, k_cache, v_cache, block_table, seqlens, scale, blocks, k_scale, v_scale,
+// out, lse, workspace, dev_status, stream
+PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 14, [&] {
+    const Heads q = heads_of(tensor(a[0], "q"), "q: bfloat16 or float16 [rows, Hq, D], values adjacent");
+    const Cache kc = cache_of(tensor(a[1], "k_cache"), kKCache), vc = values_of(tensor(a[2], "v_cache"), kc);
+    need(kc.dim == q.dim, "k_cache: q's values per head");
+    const at::Tensor* lens = tensor(a[4], "seqlens");
+    need(lens, "seqlens: int32 [rows] expected");
+    const int* seqlens = ints(lens, "seqlens", q.n);
+    const at::Tensor* b = tensor(a[6], "blocks");
+    int64_t k = 0, b_row = 0, b_head = 0;
+    if (b) {
+      need(b->scalar_type() == at::kInt && b->dim() == 3 && b->size(0) == q.n && b->size(1) == kc.heads &&
+               (b->stride(2) == 1 || b->size(2) == 1),
+           "blocks: int32 [rows, Hkv, k]");
+      // an empty tensor has no address, and no address stands for "no lists"
+      need(b->size(2) > 0 || q.n == 0, "blocks: lists of at least one entry (None: every page)");
+      k = b->size(2), b_row = b->stride(0), b_head = b->stride(1);
+    }
+    const Heads out = heads_of(tensor(a[9], "out"), "out: like q");
+    need(out.n == q.n && out.heads == q.heads && out.dim == q.dim && out.dtype == q.dtype, "out: like q");
+    const float* lse = floats(tensor(a[10], "lse"), "lse", q.n, q.heads);
+    const at::Tensor* ws = tensor(a[11], "workspace");
+    need(ws && ws->scalar_type() == at::kFloat && ws->is_contiguous(), "workspace: contiguous float32");
+    const Table t = table_of(tensor(a[3], "block_table"), q.n);
+    const float* ks = scales_of(tensor(a[7], "k_scale"), kc, kKScale);
+    const float* vs = scales_of(tensor(a[8], "v_scale"), vc, kVScale);
+    return launch(dsa_paged_attention, a[13], q.at, q.row, q.head, size32(q.n), size32(q.heads), size32(kc.heads),
+                  size32(q.dim), q.dtype, real(a[5]), kc.at, kc.page, kc.slot, kc.head, vc.at, vc.page, vc.slot, vc.head,
+                  ks, vs, size32(kc.pages), kc.kv, 64, t.at, t.stride, t.W, seqlens,
+                  static_cast<const int*>(ptr(b)), b_row, b_head, size32(k), out.at, out.row, out.head,
+                  const_cast<float*>(lse), static_cast<float*>(ptr(ws)), ws->numel(), status_word(a[12]));
+  });
+}
+
 PyMethodDef methods[] = {
     {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, nullptr},
     {"latent_store", (PyCFunction)(void (*)(void))latent_store, METH_FASTCALL, nullptr},
     {"latent_load", (PyCFunction)(void (*)(void))latent_load, METH_FASTCALL, nullptr},
     {"latent_attention", (PyCFunction)(void (*)(void))latent_attention, METH_FASTCALL, nullptr},
+    {"request_slots", (PyCFunction)(void (*)(void))request_slots, METH_FASTCALL, nullptr},
+    {"kv_store", (PyCFunction)(void (*)(void))kv_store, METH_FASTCALL, nullptr},
+    {"block_bounds", (PyCFunction)(void (*)(void))block_bounds, METH_FASTCALL, nullptr},
+    {"block_select", (PyCFunction)(void (*)(void))block_select, METH_FASTCALL, nullptr},
+    {"paged_attention", (PyCFunction)(void (*)(void))paged_attention, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dsa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

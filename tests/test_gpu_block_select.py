@@ -1,0 +1,133 @@
+"""The selection of pages: exact scores, so that the lists are those of the definition, entry by entry."""
+import math
+
+import pytest
+import torch
+
+import sparse_attention_paged_gb300 as lib
+from tests import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+class Case:
+    def __init__(self, lens, heads, kv_heads, dim, dtype, seed=0, shared=False, alike=False):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.heads, self.kv_heads, self.dim, self.R = lens, heads, kv_heads, dim, len(lens)
+        rows = [max(lens)] if shared else lens
+        used = [ref.pages_of(max(n, 0)) for n in rows]
+        pages = sum(used) + 1
+        self.W = max(1, max(used))
+        perm, at = torch.randperm(pages, generator=g).to(torch.int32), 0
+        self.table = torch.full((len(rows), self.W), -1, dtype=torch.int32)
+        for r, m in enumerate(used):
+            self.table[r, :m] = perm[at:at + m]
+            at += m
+        shape = (pages, kv_heads, 2, dim)
+        if alike:                                           # few kinds of pages: many equal scores
+            kinds = torch.randint(-127, 128, (3, kv_heads, 2, dim), generator=g)
+            self.bounds = kinds[torch.randint(0, 3, (pages,), generator=g)].to(torch.int8)
+            self.unit = torch.full((pages, kv_heads), 0.25)
+        else:
+            self.bounds = torch.randint(-127, 128, shape, generator=g).to(torch.int8)
+            self.unit = torch.exp2(torch.randint(-3, 3, (pages, kv_heads), generator=g).float())
+        self.q = torch.randn((self.R, heads, dim), generator=g).to(ref.TYPES[dtype])
+        self.seqlens = torch.tensor(lens, dtype=torch.int32)
+
+    def run(self, k, first=1, last=1, q=None):
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.k, self.first, self.last = k, first, last
+        out = torch.full((self.R, self.kv_heads, k), 12345, dtype=torch.int32, device="cuda")
+        back = lib.block_select(self.q.cuda() if q is None else q, self.bounds.cuda(), self.unit.cuda(), self.table.cuda(),
+                                self.seqlens.cuda(), k, first=first, last=last, out=out, dev_status=self.status)
+        assert back is out
+        self.out = out.cpu()
+        return self
+
+    def want(self, r, h):
+        n = ref.pages_of(max(self.lens[r], 0))
+        page = self.table[0 if self.table.shape[0] == 1 else r, :n].long()
+        group = self.heads // self.kv_heads
+        found = ref.select(self.q[r, h * group:(h + 1) * group], self.bounds[page, h], self.unit[page, h], self.k,
+                           self.first, self.last)
+        return found + [-1] * (self.k - len(found))
+
+    def check(self, status=0, rows=None):
+        assert int(self.status) == status
+        for r in range(self.R) if rows is None else rows:
+            for h in range(self.kv_heads):
+                assert self.out[r, h].tolist() == self.want(r, h), (r, h)
+        return self
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 2), (35, 5), (64, 1), (128, 1)])
+@pytest.mark.parametrize("k", [2, 7, 32])
+def test_select(dtype, dim, heads, kv_heads, k):
+    Case([1, 0, 64, 65, 64 * k, 64 * k + 1, 5000, 20000], heads, kv_heads, dim, dtype, seed=k).run(k).check()
+
+
+@pytest.mark.parametrize("first,last", [(0, 0), (0, 3), (4, 0), (5, 3), (8, 0), (0, 8)])
+@pytest.mark.parametrize("alike", [False, True])
+def test_pages_that_are_always_taken(first, last, alike):
+    Case([700, 2000, 513, 9000], 8, 2, 64, "bf16", seed=first, alike=alike).run(8, first, last).check()
+
+
+@pytest.mark.parametrize("k", [1, 3, 64, 100, 333])
+def test_equal_scores_from_the_front(k):
+    Case([30000, 6400, 6401], 4, 2, 128, "bf16", seed=k, alike=True).run(k, 0, min(k, 1)).check()
+
+
+def test_all_scores_equal():
+    c = Case([4000], 4, 1, 64, "bf16", seed=1)
+    c.q[:] = 0
+    c.run(9, 0, 0).check()
+    assert c.out[0, 0].tolist() == list(range(9))
+
+
+@pytest.mark.parametrize("k", [16, 600])
+def test_long_row(k):
+    """The most pages that a row may have, and one list of many."""
+    Case([32768 * 64, 100000], 2, 1, 64, "bf16", seed=k).run(k).check()
+
+
+def test_shared_table():
+    Case(list(range(3000, 3100)), 8, 2, 128, "fp16", seed=2, shared=True).run(6).check(rows=range(0, 100, 7))
+
+
+def test_strided_queries():
+    c = Case([3000, 900], 6, 3, 64, "bf16", seed=3)
+    wide = torch.full((2, 14, 64), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:14:2] = c.q.cuda()
+    c.run(5, q=wide[:, 2:14:2]).check()
+
+
+def test_special_queries():
+    """NaN, infinities, the smallest and the largest numbers."""
+    c = Case([3000] * 6, 4, 2, 64, "bf16", seed=4)
+    c.q[0, 0, 3] = math.nan
+    c.q[1, 1, 5] = math.inf
+    c.q[2, 2, 6] = -math.inf
+    c.q[3] *= 2.0 ** -133                                  # subnormal
+    c.q[4] *= 2.0 ** 120
+    c.q[5, :2] = 0
+    c.run(7).check()
+
+
+def test_scores_past_the_largest_float():
+    c = Case([3000], 4, 2, 64, "bf16", seed=5)
+    c.unit[:] = 2.0 ** 122
+    c.run(7).check()
+
+
+def test_data_errors():
+    """A length past the table, pages outside the pool among the row's: no list, a status; others as they are."""
+    c = Case([3000, 640, 2000, 300], 4, 2, 64, "bf16", seed=6)
+    c.table[1, 3] = 10 ** 7
+    c.table[3, 2] = -1                                     # of a row that has all its pages listed
+    c.seqlens[0] = c.W * 64 + 1
+    c.run(5).check(status=7, rows=[2])
+    assert (c.out[[0, 1]] == -1).all()
+    c.run(8)
+    assert (c.out[[0, 1, 3]] == -1).all()
