@@ -578,8 +578,8 @@ int dsa_block_select(const void* q, long long q_row_stride, long long q_head_str
  * the cache's type.  With an fp8 cache the codes are taken as fp16 (exact); a
  * head's queries as fp16 under a power of two, exact down to 2^-28 of the
  * head's largest and to 2^-39 of it below; weights times the tokens' value
- * scales as fp16, rounded by 2^-11 of themselves and by 2^-38 of the row's
- * largest where they are below 2^-27 of it.  The same call gives the same bits.
+ * scales as fp16, rounded by 2^-11 of themselves and by 2^-31 of the row's
+ * largest where they are below 2^-20 of it.  The same call gives the same bits.
  * Two kernel launches, whose shapes depend on Hq / Hkv and D only: a captured
  * call may be replayed with other lengths, lists and tables.
  * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a

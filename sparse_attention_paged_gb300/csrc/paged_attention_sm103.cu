@@ -9,17 +9,20 @@
 // One pass over the tokens with a running maximum and sum per head.  A page of
 // 64 tokens of one key head, keys and values, is a stage of a ring in shared
 // memory that TMA fills through the pools' own strides; four warps take 16 of
-// its tokens each:
+// its tokens each, with the tokens (and then the values) on the M side of the
+// products and eight heads a column tile on the N side:
 //
-//   S [16 heads x 16 tokens] = Q (A) * K^T (B)        m16n8k16, fp32 sums
-//   O [16 heads x D]        += P (A) * V (B)
+//   S^T [16 tokens x 8 heads] = K (A) * Q^T (B)       m16n8k16, fp32 sums
+//   O^T [D x 8 heads]        += V^T (A) * P^T (B)
 //
-// Q's fragments stay in registers, and so does O; S becomes P in the registers
-// where it is.  The order of the values in a dot product is free: lane t of
-// four takes the 16-byte units 2t and 2t + 1 of a key's 128 bytes as they lie,
-// with the queries in the same order, so that keys are read 16 bytes at a
-// time without a bank conflict.  Each warp has a running maximum of its own;
-// the four meet once a row, in the row's last stage.
+// Q's fragments stay in registers, and so does O^T; P^T is S^T's fragments
+// after one 8 x 8 transpose in registers.  The order of the values in a dot
+// product is free: lane t of four takes the 16-byte units 2t and 2t + 1 of a
+// key's 128 bytes as they lie, with the queries in the same order, so that keys
+// are read 16 bytes at a time without a bank conflict.  The reference of the
+// running softmax is raised only when a score passes it by 2^8, which one vote
+// finds out: sums are fp32, so that it changes no relative precision.  Each warp
+// has its own; the four meet once a row, in the row's last stage.
 //
 // Decode reads 2 D values per token for 4 D * group operations: 16 operations
 // a byte at 8 heads a group, where 285 would balance HBM and tensor cores.
@@ -31,8 +34,8 @@
 // scaled to a largest magnitude below 2^14 by a power of two; scores take the
 // token's key scale; the weights take its value scale before they are rounded
 // to fp16, under a reference of their own that follows the largest weight *
-// scale: that is 2^13 to 2^14, and a token's weight is exact to 2^-11 of
-// itself down to 2^-27 of it, and to 2^-38 of it below.
+// scale: that lies between 2^6 and 2^15, and a token's weight is rounded by
+// 2^-11 of itself down to 2^-20 of it, and by 2^-31 of it below.
 // 16-bit caches: the weights are rounded to the cache's type (2^-8 of
 // themselves for bf16, 2^-11 for fp16, 2^-25 of the largest where it is below
 // fp16's normal numbers), independently from token to token.
@@ -70,8 +73,9 @@ using namespace sm100;
 constexpr uint32_t kWaitLimit = DSA_WAIT_LIMIT_CYCLES < 2000000000ll ? DSA_WAIT_LIMIT_CYCLES : 2000000000ll;
 constexpr unsigned kAll = 0xffffffffu;
 
-// Shapes of one instance: cache type, values per head, tiles of 16 query heads.
-template <int KV, int D, int MT>
+// Shapes of one instance: cache type, values per head, column tiles of 8 query
+// heads per warp, and sets of four warps with heads of their own.
+template <int KV, int D, int NT, int MT>
 struct Shape {
   static constexpr bool kFp8 = KV == DSA_KV_FP8_E4M3;
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
@@ -79,7 +83,7 @@ struct Shape {
   static constexpr int kBoxes = kRowBytes / kBoxBytes;
   static constexpr int kBox = kPage * kBoxBytes;               // bytes of one box in shared memory
   static constexpr int kSide = kPage * kRowBytes;              // keys or values of a page
-  static constexpr int kHeadsMax = 16 * MT;
+  static constexpr int kHeadsMax = 8 * NT * MT;
   static constexpr int kScaleBytes = kFp8 ? kPage * 4 : 0;
   static constexpr int kOffScale = 2 * kSide;
   static constexpr int kOffQ = kOffScale + 2 * kScaleBytes;
@@ -92,7 +96,7 @@ struct Shape {
   static constexpr int kStages = kRoom < 8 ? kRoom : 8;
   static constexpr int kSmem = kStages * kStage + kMisc + 1024;
   // the four token slices of a row meet in a stage's keys and values, some columns at a time
-  static constexpr int kPasses = 4 * kHeadsMax * D * 4 / (2 * kSide) < 1 ? 1 : 4 * kHeadsMax * D * 4 / (2 * kSide);
+  static constexpr int kWant = 4 * kHeadsMax * D * 4 / (2 * kSide), kPasses = kWant < 1 ? 1 : kWant;
   static constexpr int kCols = D / kPasses;
   static_assert(kStages >= 3 && kSmem <= 232448 && kCols >= 8 && kPasses * kCols == D, "shape");
 };
@@ -117,6 +121,10 @@ constexpr int kWhole = 1 << 10;  // the piece is the whole row
 constexpr int kFirst = 1 << 11;  // the piece has the row's first unit
 constexpr int kBad = 1 << 12;    // a page that it needs is not in the pool
 constexpr int kDone = 1 << 13;   // the slice ends here: no unit
+
+// A reference is raised to the largest score when one is this far above it
+// (log2 units), and fp8's weights * value scales are 2^kBelow at theirs.
+constexpr float kAbove = 8.f, kBelow = 6.f, kSmallest = 1.f / 64.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -144,9 +152,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The transpose of 8 x 8 values of 16 bits: lane 4 g + t has row g, columns 2 t and 2 t + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
@@ -160,10 +180,14 @@ __device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t at) {
                : "r"(at));
 }
 
-// Two e4m3 codes as two fp16 values.
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  return (uint32_t)r.x | (uint32_t)r.y << 16;
+// Four e4m3 codes as two pairs of fp16 values.
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t& low, uint32_t& high) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(low), "=r"(high)
+      : "r"(codes));
 }
 
 template <bool FP16>
@@ -261,10 +285,10 @@ __device__ void find_slice(const PagedAttnParams& p, Misc* m) {
 
 // ---- the warp that loads ------------------------------------------------------
 
-template <int KV, int D, int MT>
+template <int KV, int D, int NT, int MT>
 __device__ void produce(const PagedAttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, Misc* m,
                         uint32_t stages) {
-  using S = Shape<KV, D, MT>;
+  using S = Shape<KV, D, NT, MT>;
   const int lane = threadIdx.x & 31;
   Waiter wait{p.status, true};
   int stage = 0, issued = 0;
@@ -380,20 +404,23 @@ __device__ void produce(const PagedAttnParams& p, const CUtensorMap* kmap, const
 
 // ---- the warps that compute -----------------------------------------------------
 
-template <int KV, int D, int MT>
+template <int KV, int D, int NT, int MT>
 struct Consumer {
-  using S = Shape<KV, D, MT>;
+  using S = Shape<KV, D, NT, MT>;
   static constexpr bool kFp8 = S::kFp8;
   static constexpr bool kHalf = KV != DSA_KV_BF16;    // the products' operands are fp16
-  static constexpr int kSteps = D / 16;               // k steps of S, and pairs of column tiles of O
-  static constexpr int kTiles = D / 8;                // column tiles of O
+  static constexpr int kSteps = D / 16;               // k steps of S^T, and row tiles of O^T
+  static constexpr int kWarpHeads = 8 * NT;
 
   const PagedAttnParams& p;
   Misc* m;
-  int warp, lane, g, t, slice, mt, heads;             // heads: of this warp's tile of 16
-  uint32_t qa[kSteps][4];
-  float o[kTiles][4];
-  float top[2], ref[2], sum[2], qf[2];                // rows g and g + 8
+  int warp, lane, g, t, slice, mt, heads;             // heads: of this warp's column tiles
+  uint32_t qb[NT][kSteps][2];
+  float o[kSteps][NT][4];
+  // heads 2 t and 2 t + 1 of each column tile: reference of the scores, that of
+  // the weights * value scales (fp8), this lane's part of the total, and the
+  // factor from a product to log2 units
+  float top[NT][2], ref[NT][2], sum[NT][2], qf[NT][2];
   Waiter wait;
   uint32_t meet_phase, turn;
 
@@ -412,18 +439,23 @@ struct Consumer {
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    top[0] = top[1] = ref[0] = ref[1] = -CUDART_INF_F;
-    sum[0] = sum[1] = 0.f;
+    for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      top[n][0] = top[n][1] = ref[n][0] = ref[n][1] = -CUDART_INF_F;
+      sum[n][0] = sum[n][1] = 0.f;
+    }
   }
 
-  // Queries of rows g and g + 8, in the order in which the keys are read.
+  // Queries of head g of each column tile, in the order in which the keys are read.
   __device__ __forceinline__ void load_queries(uint32_t q) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = mt * 16 + g + 8 * half;
-      const uint32_t at = q + row * (D * 2);
-      const bool there = g + 8 * half < heads;
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t at = q + (mt * kWarpHeads + 8 * n + g) * (D * 2);
+      const bool there = 8 * n + g < heads;
+      qf[n][0] = qf[n][1] = p.scale_log2;
       if (!kFp8) {
         // unit u = 2t + i of each 64 values: two steps
 #pragma unroll
@@ -432,7 +464,7 @@ struct Consumer {
           for (int i = 0; i < 2; ++i) {
             const uint4 v = there ? lds128(at + b * 128 + (2 * t + i) * 16) : make_uint4(0, 0, 0, 0);
             const int s = b * 4 + i * 2;
-            qa[s][half] = v.x, qa[s][half + 2] = v.y, qa[s + 1][half] = v.z, qa[s + 1][half + 2] = v.w;
+            qb[n][s][0] = v.x, qb[n][s][1] = v.y, qb[n][s + 1][0] = v.z, qb[n][s + 1][1] = v.w;
           }
         continue;
       }
@@ -441,13 +473,10 @@ struct Consumer {
       uint32_t w[kUnits * 8];
       float big = 0.f;
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 v = there ? lds128(at + ((kUnits * t + i) * 2 + j) * 16) : make_uint4(0, 0, 0, 0);
-          const int k = i * 8 + j * 4;
-          w[k] = v.x, w[k + 1] = v.y, w[k + 2] = v.z, w[k + 3] = v.w;
-        }
+      for (int i = 0; i < 2 * kUnits; ++i) {
+        const uint4 v = there ? lds128(at + (2 * kUnits * t + i) * 16) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
       auto low = [&](uint32_t u) {
         return p.dtype == DSA_FP16 ? __half2float(__ushort_as_half((unsigned short)u)) : __uint_as_float(u << 16);
       };
@@ -462,75 +491,84 @@ struct Consumer {
       // big < 2^x; queries times 2^(14 - x)
       const int x = max((int)(__float_as_uint(big) >> 23) - 126, -100);
       const float up = __uint_as_float((uint32_t)(127 + 14 - x) << 23);
-      qf[half] = __uint_as_float((uint32_t)(127 - 14 + x) << 23) * p.scale_log2;
+      const float down = __uint_as_float((uint32_t)(127 - 14 + x) << 23) * p.scale_log2;
 #pragma unroll
-      for (int k = 0; k < kUnits * 8; ++k) w[k] = pack2<true>(low(w[k]) * up, high(w[k]) * up);
+      for (int c = 0; c < 2; ++c) qf[n][c] = __shfl_sync(kAll, down, (2 * t + c) * 4);  // heads 2t + c
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) qa[s][half] = w[2 * s], qa[s][half + 2] = w[2 * s + 1];
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) qb[n][s][c] = pack2<true>(low(w[2 * s + c]) * up, high(w[2 * s + c]) * up);
     }
-    if (!kFp8) qf[0] = qf[1] = p.scale_log2;
   }
 
-  // S for the warp's 16 tokens: two column tiles of 8.
-  __device__ __forceinline__ void scores(uint32_t k, float (&s)[2][4]) {
-    float even[2][4], odd[2][4];
+  // S^T of the warp's 16 tokens: rows g and g + 8, heads 2t and 2t + 1.
+  __device__ __forceinline__ void scores(uint32_t k, float (&s)[NT][4]) {
+    float odd[NT][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) even[j][c] = odd[j][c] = 0.f;
+      for (int c = 0; c < 4; ++c) s[n][c] = odd[n][c] = 0.f;
+    const int token = slice * 16 + g;
+    if (!kFp8) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int token = slice * 16 + j * 8 + g;          // g: the column of a B fragment
-      if (!kFp8) {
+      for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-        for (int b = 0; b < D / 64; ++b)
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t at = k + b * S::kBox + token * 128 + (((2 * t + i) ^ (token & 7)) << 4);
+          const uint4 v = lds128(at), w = lds128(at + 8 * 128);
+          const uint32_t a0[4] = {v.x, w.x, v.y, w.y}, a1[4] = {v.z, w.z, v.w, w.w};
+          const int st = b * 4 + i * 2;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 v = lds128(k + b * S::kBox + token * 128 + (((2 * t + i) ^ (token & 7)) << 4));
-            const int st = b * 4 + i * 2;
-            mma16816<kHalf>(even[j], qa[st], v.x, v.y);
-            mma16816<kHalf>(odd[j], qa[st + 1], v.z, v.w);
+          for (int n = 0; n < NT; ++n) {
+            mma16816<kHalf>(s[n], a0, qb[n][st][0], qb[n][st][1]);
+            mma16816<kHalf>(odd[n], a1, qb[n][st + 1][0], qb[n][st + 1][1]);
           }
-      } else {
+        }
+    } else {
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const uint32_t at = D == 128 ? token * 128 + (((2 * t + i) ^ (token & 7)) << 4)
-                                       : token * 64 + ((t ^ ((token >> 1) & 3)) << 4);
-          const uint4 v = lds128(k + at);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < D / 64; ++i) {
+        const uint32_t at = k + (D == 128 ? token * 128 + (((2 * t + i) ^ (token & 7)) << 4)
+                                          : token * 64 + ((t ^ ((token >> 1) & 3)) << 4));
+        const uint4 v = lds128(at), w = lds128(at + 8 * S::kBoxBytes);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w}, y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float(&into)[4] = (c & 1) ? odd[j] : even[j];
-            mma16816<true>(into, qa[i * 4 + c], widen2(w[c] & 0xffffu), widen2(w[c] >> 16));
+        for (int c = 0; c < 4; ++c) {
+          uint32_t a[4];
+          widen4(x[c], a[0], a[2]);
+          widen4(y[c], a[1], a[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float(&into)[4] = (c & 1) ? odd[n] : s[n];
+            mma16816<true>(into, a, qb[n][i * 4 + c][0], qb[n][i * 4 + c][1]);
           }
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[j][c] = even[j][c] + odd[j][c];
+      for (int c = 0; c < 4; ++c) s[n][c] += odd[n][c];
   }
 
-  // O += P * V; `keep`: masks of the tokens 2t, 2t + 1 (low and high half) and
-  // + 8 of a page that ends inside the warp's tokens.
+  // O^T += V^T * P^T; `keep`: masks of the tokens 2t, 2t + 1 (low and high half)
+  // and + 8 of a page that ends inside the warp's tokens.
   template <bool CUT>
-  __device__ __forceinline__ void values(uint32_t v, const uint32_t (&pa)[4], uint32_t keep0, uint32_t keep1) {
+  __device__ __forceinline__ void values(uint32_t v, const uint32_t (&pb)[NT][2], uint32_t keep0, uint32_t keep1) {
     if (!kFp8) {
-      // matrices of 8 tokens x 8 values: tokens 0-7 and 8-15 of two column tiles
-      const int token = slice * 16 + (lane & 15);
+      // matrices of 8 tokens x 8 values: two of the values' units, tokens 0-7 and 8-15
+      const int token = slice * 16 + (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
-      for (int j = 0; j < kTiles; j += 2) {
-        const int unit = j + (lane >> 4);                // of 16 bytes
-        uint32_t b[4];
-        ldmatrix_t(b, v + (unit >> 3) * S::kBox + token * 128 + (((unit & 7) ^ (token & 7)) << 4));
-        if (CUT) b[0] &= keep0, b[1] &= keep1, b[2] &= keep0, b[3] &= keep1;
-        mma16816<kHalf>(o[j], pa, b[0], b[1]);
-        mma16816<kHalf>(o[j + 1], pa, b[2], b[3]);
+      for (int j = 0; j < kSteps; ++j) {
+        const int unit = 2 * j + (lane >> 3 & 1);        // of 16 bytes
+        uint32_t a[4];
+        ldmatrix_t(a, v + (unit >> 3) * S::kBox + token * 128 + (((unit & 7) ^ (token & 7)) << 4));
+        if (CUT) a[0] &= keep0, a[1] &= keep0, a[2] &= keep1, a[3] &= keep1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<kHalf>(o[j][n], a, pb[n][0], pb[n][1]);
       }
       return;
     }
-    // lane column g holds the D / 8 values from D / 8 * g on: one per column tile
+    // row g of all tiles holds the D / 8 values from D / 8 * g on: two per tile, rows g and g + 8
     constexpr int kWords = D / 32;
     uint32_t w[4][kWords];
 #pragma unroll
@@ -549,100 +587,116 @@ struct Consumer {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // codes of two tokens side by side: (2t, 2t + 1) and (2t + 8, 2t + 9), two values each
-        const uint32_t a = __byte_perm(w[0][c], w[1][c], h ? 0x7362 : 0x5140);
-        const uint32_t b = __byte_perm(w[2][c], w[3][c], h ? 0x7362 : 0x5140);
-        uint32_t a0 = widen2(a & 0xffffu), a1 = widen2(a >> 16), b0 = widen2(b & 0xffffu), b1 = widen2(b >> 16);
-        if (CUT) a0 &= keep0, a1 &= keep0, b0 &= keep1, b1 &= keep1;
-        mma16816<true>(o[c * 4 + h * 2], pa, a0, b0);
-        mma16816<true>(o[c * 4 + h * 2 + 1], pa, a1, b1);
+        uint32_t a[4];
+        widen4(__byte_perm(w[0][c], w[1][c], h ? 0x7362 : 0x5140), a[0], a[1]);
+        widen4(__byte_perm(w[2][c], w[3][c], h ? 0x7362 : 0x5140), a[2], a[3]);
+        if (CUT) a[0] &= keep0, a[1] &= keep0, a[2] &= keep1, a[3] &= keep1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<true>(o[c * 2 + h][n], a, pb[n][0], pb[n][1]);
       }
+  }
+
+  // The largest value of a head over the lanes that have its tokens.
+  static __device__ __forceinline__ float over_tokens(float x) {
+    x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+    return fmaxf(x, __shfl_xor_sync(kAll, x, 16));
   }
 
   __device__ __forceinline__ void page(uint32_t stage, int tokens) {
     if (tokens <= slice * 16) return;
-    float s[2][4];
+    float s[NT][4];
     scores(stage, s);
     const int valid = tokens - slice * 16;               // of the warp's 16
-    // this lane's tokens: 8 j + 2 t and the next
-    float e[2][2], f[2][2];                              // fp8: exponent and mantissa of the value scales
+    float e[2], f[2];                                    // fp8: exponent and mantissa of the tokens' value scales
     if (kFp8) {
+      const uint32_t at = stage + S::kOffScale + (slice * 16 + g) * 4;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t at = stage + S::kOffScale + (slice * 16 + 8 * j + 2 * t) * 4;
-        const uint2 ks = lds64(at), vs = lds64(at + S::kScaleBytes);
-        const uint32_t bits[2] = {vs.x, vs.y};
+      for (int h = 0; h < 2; ++h) {
+        const float ks = __uint_as_float(lds32(at + h * 32));
+        const uint32_t bits = lds32(at + S::kScaleBytes + h * 32);
+        const int x = (int)(bits >> 23 & 255u);
+        e[h] = (float)(x - 127);
+        f[h] = x ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u)
+                 : __uint_as_float(bits) * 1.7014118346046923e38f;  // 2^127
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int x = (int)(bits[c] >> 23 & 255u);
-          e[j][c] = (float)(x - 127);
-          f[j][c] = x ? __uint_as_float((bits[c] & 0x807fffffu) | 0x3f800000u)
-                      : __uint_as_float(bits[c]) * 1.7014118346046923e38f;  // 2^127
-        }
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          s[j][c] = s[j][c] * qf[c >> 1] * __uint_as_float((c & 1) ? ks.y : ks.x);
+          for (int c = 0; c < 2; ++c) s[n][2 * h + c] = s[n][2 * h + c] * qf[n][c] * ks;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[j][c] *= p.scale_log2;
+        for (int c = 0; c < 4; ++c) s[n][c] *= qf[n][c & 1];
     }
     if (valid < 16) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (8 * j + 2 * t + (c & 1) >= valid) s[j][c] = -CUDART_INF_F;
+          if (g + 8 * (c >> 1) >= valid) s[n][c] = -CUDART_INF_F;
     }
-    uint32_t pa[4];
-    float shrink[2];
+    bool over = false;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int a = 2 * half, b = a + 1;
-      float big = fmaxf(fmaxf(s[0][a], s[0][b]), fmaxf(s[1][a], s[1][b]));
-      big = fmaxf(big, __shfl_xor_sync(kAll, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
-      const float now = fmaxf(top[half], big), base = now == -CUDART_INF_F ? 0.f : now;
-      const float p0 = ex2(s[0][a] - base), p1 = ex2(s[0][b] - base), p2 = ex2(s[1][a] - base),
-                  p3 = ex2(s[1][b] - base);
-      const float less = ex2(top[half] - base);
-      sum[half] = sum[half] * less + ((p0 + p1) + (p2 + p3));
-      top[half] = now;
-      if (!kFp8) {
-        shrink[half] = less;
-        pa[half] = pack2<kHalf>(p0, p1), pa[half + 2] = pack2<kHalf>(p2, p3);
-      } else {
-        const float y0 = s[0][a] + e[0][0], y1 = s[0][b] + e[0][1], y2 = s[1][a] + e[1][0], y3 = s[1][b] + e[1][1];
-        float high = fmaxf(fmaxf(y0, y1), fmaxf(y2, y3));
-        high = fmaxf(high, __shfl_xor_sync(kAll, high, 1));
-        high = fmaxf(high, __shfl_xor_sync(kAll, high, 2));
-        const float next = fmaxf(ref[half], high), from = (next == -CUDART_INF_F ? 0.f : next) - 13.f;
-        shrink[half] = ex2(ref[half] - (from + 13.f));
-        ref[half] = next;
-        pa[half] = pack2<true>(ex2(y0 - from) * f[0][0], ex2(y1 - from) * f[0][1]);
-        pa[half + 2] = pack2<true>(ex2(y2 - from) * f[1][0], ex2(y3 - from) * f[1][1]);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        over |= s[n][c] > top[n][c & 1] + kAbove;
+        if (kFp8) over |= s[n][c] + e[c >> 1] > ref[n][c & 1] + kAbove;
       }
-    }
-    if (__any_sync(kAll, shrink[0] != 1.f || shrink[1] != 1.f)) {
+    if (__any_sync(kAll, over)) raise(s, e);
+    uint32_t pb[NT][2];
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j)
-        o[j][0] *= shrink[0], o[j][1] *= shrink[0], o[j][2] *= shrink[1], o[j][3] *= shrink[1];
+    for (int n = 0; n < NT; ++n) {
+      float x[4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float base = top[n][c] == -CUDART_INF_F ? 0.f : top[n][c];
+        x[c] = ex2(s[n][c] - base), x[2 + c] = ex2(s[n][2 + c] - base);
+        sum[n][c] += x[c] + x[2 + c];
+        if (kFp8) {
+          const float from = (ref[n][c] == -CUDART_INF_F ? 0.f : ref[n][c]) - kBelow;
+          x[c] = ex2(s[n][c] + e[0] - from) * f[0], x[2 + c] = ex2(s[n][2 + c] + e[1] - from) * f[1];
+        }
+      }
+      pb[n][0] = transpose8(pack2<kHalf>(x[0], x[1]));
+      pb[n][1] = transpose8(pack2<kHalf>(x[2], x[3]));
     }
     if (valid >= 16) {
-      values<false>(stage + S::kSide, pa, 0, 0);
+      values<false>(stage + S::kSide, pb, 0, 0);
     } else {
       // masked tokens may hold anything, and 0 * NaN is NaN
       auto mask = [&](int token) {
         return (token < valid ? 0xffffu : 0u) | (token + 1 < valid ? 0xffff0000u : 0u);
       };
-      values<true>(stage + S::kSide, pa, mask(2 * t), mask(2 * t + 8));
+      values<true>(stage + S::kSide, pb, mask(2 * t), mask(2 * t + 8));
     }
   }
 
-  // Column of O's register c (0 or 1 of a row) of column tile j.
+  // New references where a score is too far above the old one: the largest.
+  __device__ __forceinline__ void raise(const float (&s)[NT][4], const float (&e)[2]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float big = over_tokens(fmaxf(s[n][c], s[n][2 + c]));
+        float less = 1.f;
+        if (big > top[n][c] + kAbove) less = ex2(top[n][c] - big), top[n][c] = big;
+        sum[n][c] *= less;
+        if (kFp8) {
+          const float high = over_tokens(fmaxf(s[n][c] + e[0], s[n][2 + c] + e[1]));
+          less = 1.f;
+          if (high > ref[n][c] + kAbove) less = ex2(ref[n][c] - high), ref[n][c] = high;
+        }
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) o[j][n][c] *= less, o[j][n][2 + c] *= less;
+      }
+  }
+
+  // Value of O^T's row tile j that register c (rows g and g + 8) holds.
   __device__ __forceinline__ int column(int j, int c) const {
-    return kFp8 ? (D / 8) * (2 * t + c) + j : 8 * j + 2 * t + c;
+    return kFp8 ? (D / 8) * g + 2 * j + c : 16 * j + 8 * c + g;
   }
 
   // A row's four slices of tokens meet in the stage; results or partial sums go out.
@@ -650,27 +704,32 @@ struct Consumer {
     float(*stats)[16][3] = m->stat[turn];
     turn ^= 1;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      sum[half] += __shfl_xor_sync(kAll, sum[half], 1);
-      sum[half] += __shfl_xor_sync(kAll, sum[half], 2);
-      if (!kFp8) ref[half] = top[half];
-      if (t == 0) {
-        float* s = stats[warp][g + 8 * half];
-        s[0] = top[half], s[1] = ref[half], s[2] = sum[half];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        sum[n][c] += __shfl_xor_sync(kAll, sum[n][c], 4);
+        sum[n][c] += __shfl_xor_sync(kAll, sum[n][c], 8);
+        sum[n][c] += __shfl_xor_sync(kAll, sum[n][c], 16);
+        if (!kFp8) ref[n][c] = top[n][c];
+        if (g == 0) {
+          float* s = stats[warp][8 * n + 2 * t + c];
+          s[0] = top[n][c], s[1] = ref[n][c], s[2] = sum[n][c];
+        }
       }
-    }
     if (!meet()) return;
     const int group0 = (meta.y % p.tiles) * S::kHeadsMax, key_head = meta.y / p.tiles;
     const int all = min(S::kHeadsMax, p.group - group0);  // of the CTA
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float high = -CUDART_INF_F;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) high = fmaxf(high, stats[mt * 4 + w][g + 8 * half][1]);
-      const float f = ref[half] == -CUDART_INF_F ? 0.f : ex2(ref[half] - high);
+      for (int c = 0; c < 2; ++c) {
+        float high = -CUDART_INF_F;
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) o[j][2 * half] *= f, o[j][2 * half + 1] *= f;
-    }
+        for (int w = 0; w < 4; ++w) high = fmaxf(high, stats[mt * 4 + w][8 * n + 2 * t + c][1]);
+        const float f = ref[n][c] == -CUDART_INF_F ? 0.f : ex2(ref[n][c] - high);
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) o[j][n][c] *= f, o[j][n][2 + c] *= f;
+      }
     const bool whole = meta.z & kWhole;
     const int piece = (meta.z & kFirst) ? 1 : 0;
     const int hv = paged_cta_heads(p.group);
@@ -679,14 +738,19 @@ struct Consumer {
 #pragma unroll 1
     for (int pass = 0; pass < S::kPasses; ++pass) {
       // slices of a column chunk; groups of 8 columns are permuted by row against bank conflicts
-      auto place = [&](int col, int row) { return col ^ ((((row & 7) ^ ((col >> 5) & 3)) << 3) & (S::kCols - 1)); };
+      auto place = [&](int col, int row) {
+        return col ^ ((((row >> 1 & 3) ^ ((col >> 5) & 3)) << 3) & (S::kCols - 1));
+      };
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j)
+      for (int j = 0; j < kSteps; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = column(j, c & 1) - pass * S::kCols, row = mt * 16 + g + 8 * (c >> 1);
-          if (col >= 0 && col < S::kCols) parts[(slice * S::kHeadsMax + row) * S::kCols + place(col, row)] = o[j][c];
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int col = column(j, c >> 1) - pass * S::kCols, row = mt * kWarpHeads + 8 * n + 2 * t + (c & 1);
+            if (col >= 0 && col < S::kCols)
+              parts[(slice * S::kHeadsMax + row) * S::kCols + place(col, row)] = o[j][n][c];
+          }
       if (!meet()) return;
       constexpr int kGroups = S::kCols / 8;
       for (int i = warp * 32 + lane; i < all * kGroups; i += S::kConsumers * 32) {
@@ -699,15 +763,16 @@ struct Consumer {
           const float4 a = from[0], b = from[1];
           x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w, x[4] += b.x, x[5] += b.y, x[6] += b.z, x[7] += b.w;
         }
-        const float(*st)[16][3] = stats + (row >> 4) * 4;
+        const float(*st)[16][3] = stats + (row / kWarpHeads) * 4;
+        const int h = row % kWarpHeads;
         float big = -CUDART_INF_F, high = -CUDART_INF_F, total = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) big = fmaxf(big, st[w][row & 15][0]), high = fmaxf(high, st[w][row & 15][1]);
+        for (int w = 0; w < 4; ++w) big = fmaxf(big, st[w][h][0]), high = fmaxf(high, st[w][h][1]);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float l = st[w][row & 15][2];
-          // a slice without tokens has no maximum; a NaN total stays one
-          total += st[w][row & 15][0] == -CUDART_INF_F ? l : l * ex2(st[w][row & 15][0] - big);
+          const float l = st[w][h][2];
+          // a slice without tokens has no reference; a NaN total stays one
+          total += st[w][h][0] == -CUDART_INF_F ? l : l * ex2(st[w][h][0] - big);
         }
         if (meta.z & kBad) total = CUDART_NAN_F;
         const int c0 = pass * S::kCols + col;
@@ -733,7 +798,7 @@ struct Consumer {
   static __device__ __forceinline__ void write_out(const PagedAttnParams& p, int row, int head, int c0, float (&x)[8],
                                                    float big, float high, float total) {
     // no visible token: zeros, -inf
-    const float f = total == 0.f ? 0.f : (kFp8 ? 1.f / 8192.f : 1.f) / total;
+    const float f = total == 0.f ? 0.f : (kFp8 ? kSmallest : 1.f) / total;
     const float unit = kFp8 ? ex2_small(high - big) : 1.f;  // of the size of the value scales
     uint32_t w[4];
 #pragma unroll
@@ -809,7 +874,7 @@ struct Consumer {
       const int tokens = meta.z & 127;
       if (meta.z & kBegin) {
         reset();
-        heads = min(max(p.group - (meta.y % p.tiles) * S::kHeadsMax - mt * 16, 0), 16);
+        heads = min(max(p.group - (meta.y % p.tiles) * S::kHeadsMax - mt * kWarpHeads, 0), kWarpHeads);
         if (tokens) load_queries(base + S::kOffQ);
       }
       if (heads > 0) page(base, tokens);
@@ -826,11 +891,11 @@ struct Consumer {
   }
 };
 
-template <int KV, int D, int MT>
-__global__ void __launch_bounds__(Shape<KV, D, MT>::kThreads, Shape<KV, D, MT>::kCtas)
+template <int KV, int D, int NT, int MT>
+__global__ void __launch_bounds__(Shape<KV, D, NT, MT>::kThreads, Shape<KV, D, NT, MT>::kCtas)
     paged_attention_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap) {
-  using S = Shape<KV, D, MT>;
+  using S = Shape<KV, D, NT, MT>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   Misc* m = reinterpret_cast<Misc*>(smem + S::kStages * S::kStage);
@@ -849,9 +914,9 @@ __global__ void __launch_bounds__(Shape<KV, D, MT>::kThreads, Shape<KV, D, MT>::
   griddep_launch_dependents();
   find_slice<S::kThreads>(p, m);             // its barriers also publish the mbarriers
   if (warp == S::kConsumers) {
-    produce<KV, D, MT>(p, &kmap, &vmap, m, smem_u32(smem));
+    produce<KV, D, NT, MT>(p, &kmap, &vmap, m, smem_u32(smem));
   } else {
-    Consumer<KV, D, MT> c(p, m, warp, lane);
+    Consumer<KV, D, NT, MT> c(p, m, warp, lane);
     c.run(smem);
   }
 }
@@ -928,7 +993,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     for (int k = 0; k < kGroups; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] += sums[k][c0 + i];
-    Consumer<KV, D, 1>::write_out(p, row, (tile / p.tiles) * p.group + group0 + h, c0, y, big, high, total);
+    Consumer<KV, D, 1, 1>::write_out(p, row, (tile / p.tiles) * p.group + group0 + h, c0, y, big, high, total);
   }
 }
 
@@ -947,21 +1012,21 @@ cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int KV, int D, int MT>
+template <int KV, int D, int NT, int MT>
 cudaError_t launch_t(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
                      cudaStream_t stream) {
-  using S = Shape<KV, D, MT>;
+  using S = Shape<KV, D, NT, MT>;
   static bool ready[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices || !ready[dev]) {
-    e = cudaFuncSetAttribute(paged_attention_kernel<KV, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    e = cudaFuncSetAttribute(paged_attention_kernel<KV, D, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) ready[dev] = true;
   }
   const int ctas = sms * S::kCtas;
-  e = launch(paged_attention_kernel<KV, D, MT>, dim3(ctas), S::kThreads, S::kSmem, stream, p, kmap, vmap);
+  e = launch(paged_attention_kernel<KV, D, NT, MT>, dim3(ctas), S::kThreads, S::kSmem, stream, p, kmap, vmap);
   if (e != cudaSuccess) return e;
   return launch(paged_join_kernel<KV, D>, dim3(ctas, paged_cta_heads(p.group)), kJoinThreads, 0, stream, p, ctas,
                 S::kHeadsMax);
@@ -970,8 +1035,11 @@ cudaError_t launch_t(const PagedAttnParams& p, const CUtensorMap& kmap, const CU
 template <int KV, int D>
 cudaError_t launch_d(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
                      cudaStream_t stream) {
-  return paged_head_tiles(p.group) == 1 ? launch_t<KV, D, 1>(p, kmap, vmap, sms, stream)
-                                        : launch_t<KV, D, 2>(p, kmap, vmap, sms, stream);
+  switch (paged_heads_max(p.group)) {
+    case 8: return launch_t<KV, D, 1, 1>(p, kmap, vmap, sms, stream);
+    case 16: return launch_t<KV, D, 2, 1>(p, kmap, vmap, sms, stream);
+    default: return launch_t<KV, D, 2, 2>(p, kmap, vmap, sms, stream);
+  }
 }
 
 }  // namespace

@@ -106,13 +106,12 @@ struct PagedAttnParams {
   int* status;
 };
 
-// The attention's launch: query heads that a CTA takes (16 per head tile) and
-// CTAs per SM, by the query heads of a key head.
-constexpr int paged_head_tiles(int group) { return group > 16 ? 2 : 1; }
+// The attention's launch, by the query heads of a key head: heads that a CTA
+// takes (one or two column tiles of 8 per warp, one or two sets of warps), and
+// CTAs per SM.
+constexpr int paged_heads_max(int group) { return group > 16 ? 32 : group > 8 ? 16 : 8; }
 constexpr int paged_ctas_per_sm(int group) { return group > 16 ? 1 : 2; }
-constexpr int paged_cta_heads(int group) {
-  return group < 16 * paged_head_tiles(group) ? group : 16 * paged_head_tiles(group);
-}
+constexpr int paged_cta_heads(int group) { return group < paged_heads_max(group) ? group : paged_heads_max(group); }
 
 // Its workspace: two partial results per CTA (sums of the CTA's heads, then
 // their statistics, four floats a head), then a split record of four ints per CTA.
