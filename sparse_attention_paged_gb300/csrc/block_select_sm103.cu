@@ -13,16 +13,27 @@
 // not depend on how the work is split.  Scores past the largest float count as
 // that.  NaN queries count as 0, infinities as the largest float.
 //
-// A block per row and key head.  8 lanes have a page: 2 D bytes of codes, four
-// products an instruction.  The k-th largest score is found by its bits, 8 at
-// a time (histograms in shared memory), then each thread takes its run of
-// pages in order.  Bound by HBM at long rows (2 D + 4 bytes a page and head),
-// by latency at short ones.
+// Rows with tables of their own: a cluster of up to eight blocks per row and
+// key head, each with a run of the row's pages.  8 lanes have a page: 2 D bytes
+// of codes, four products an instruction.  Every block finds the best k of its
+// run, and the first one the best k of those.  Bound by HBM at long rows (2 D + 4
+// bytes a page and head), by latency at short ones.
+//
+// Rows that share a table (a prompt): a block per 16 rows and key head reads the
+// boxes once, on the tensor cores' 8-bit products, and a warp selects for a row.
+// Bound by its instructions.
+//
+// The k-th largest score is found bit by bit from the top of the scores' common
+// prefix on, a count a bit, and the search ends as soon as a count is k: most
+// often after 10 to 15 bits.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <float.h>
+#include <limits.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "paged_common.cuh"
 #include "sm100_ptx.cuh"
@@ -33,17 +44,11 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBlocksPerSm = 2;
+constexpr int kOrdered = 128;        // rows that are started by their lengths, at most
+constexpr int kRun = 256;            // pages that a block has before another one joins it
 constexpr int kGridBits = 20;
-
-struct Shared {
-  int parts[kThreads / 64][2][128];  // partial sums of P and N
-  alignas(16) uint32_t codes[64];    // p (D bytes), then -n
-  float tops[kWarps];
-  int sizes[kWarps];
-  uint32_t hist[256];
-  uint32_t sums[kWarps];
-  int bad, digit, rank;
-};
+constexpr uint32_t kAlways = 0xffffffffu;  // key of a page that is taken whatever its score
 
 // Floats in the order of unsigned numbers.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -51,199 +56,595 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ float value(uint16_t u, int dtype) {
-  float x = dtype == DSA_FP16 ? __half2float(__ushort_as_half(u)) : __uint_as_float((uint32_t)u << 16);
+// A page's key: its score's place in the order.
+__device__ __forceinline__ uint32_t key_of(int dot, float scale, int i, int n, const BlockSelectParams& p) {
+  const float score = fminf(fmaxf((float)dot * scale, -FLT_MAX), FLT_MAX);
+  return i < p.first || i >= n - p.last ? kAlways : ordered(score + 0.f);
+}
+
+__device__ __forceinline__ float value(uint32_t u, int dtype) {
+  float x = dtype == DSA_FP16 ? __half2float(__ushort_as_half((unsigned short)u)) : __uint_as_float(u << 16);
   if (x != x) x = 0.f;
   return fminf(fmaxf(x, -FLT_MAX), FLT_MAX);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelectParams p) {
-  extern __shared__ uint32_t keys[];     // [W] page ids, then scores
-  __shared__ Shared s;
-  const int row = blockIdx.x / p.heads, head = blockIdx.x % p.heads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  sm100::griddep_wait();
-  sm100::griddep_launch_dependents();
-  const int len = __ldg(p.seqlens + row);
-  int* out = p.blocks + ((long long)row * p.heads + head) * p.k;
-  const bool past = (long long)len > (long long)p.W * kPage;
-  const int n = len <= 0 || past ? 0 : (len - 1) / kPage + 1;
-  if (past && threadIdx.x == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
-  if (threadIdx.x == 0) s.bad = 0;
-  __syncthreads();
-  const int* table = p.block_table + (long long)row * p.bt_stride;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int page = __ldg(table + i);
-    keys[i] = (uint32_t)page;
-    if (page < 0 || page >= p.num_pages) s.bad = 1;
-  }
-  if (n <= p.k) {                        // every page
-    __syncthreads();
-    const bool bad = s.bad;
-    if (bad && threadIdx.x == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
-    for (int i = threadIdx.x; i < p.k; i += kThreads) out[i] = i < n && !bad ? i : -1;
-    return;
-  }
+// A query value on the group's grid, 2^x above the group's largest magnitude.
+__device__ __forceinline__ int on_grid(float v, int x) { return (int)rintf(scalbnf(v, kGridBits - x)); }
 
-  // the group's queries
-  const uint16_t* q = p.q + (long long)row * p.q_row + (long long)head * p.group * p.q_head;
-  const int d = threadIdx.x % D, part = threadIdx.x / D;
-  constexpr int kParts = kThreads / D;
-  float top = 0.f;
-  for (int h = part; h < p.group; h += kParts) top = fmaxf(top, fabsf(value(__ldg(q + h * p.q_head + d), p.dtype)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-  if (lane == 0) s.tops[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.tops[w]);
+__device__ __forceinline__ int exponent_above(float top) {
   int x;
-  frexpf(top, &x);                       // top < 2^x
-  int above = 0, below = 0;
-  for (int h = part; h < p.group; h += kParts) {
-    const int i = (int)rintf(scalbnf(value(__ldg(q + h * p.q_head + d), p.dtype), kGridBits - x));
-    above += max(i, 0), below += max(-i, 0);
-  }
-  s.parts[part][0][d] = above, s.parts[part][1][d] = below;
-  __syncthreads();
-  int sum = 0;
-  if (threadIdx.x < 2 * D) {
-#pragma unroll
-    for (int k = 0; k < kParts; ++k) sum += s.parts[k][threadIdx.x / D][d];
-  }
-  int size = sum;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) size = max(size, __shfl_xor_sync(kAll, size, o));
-  if (lane == 0) s.sizes[warp] = size;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) size = max(size, s.sizes[w]);
+  frexpf(top, &x);
+  return x;
+}
+
+// The smallest s with size <= 127 * 2^s.
+__device__ __forceinline__ int code_shift(int size) {
   int shift = max(0, 25 - __clz(size | 1));  // size < 128 * 2^shift
   if (size > 127 << shift) ++shift;
-  if (threadIdx.x < 2 * D) {
-    const int code = (sum + (1 << shift) - 1) >> shift;
-    reinterpret_cast<int8_t*>(s.codes)[threadIdx.x] = (int8_t)(threadIdx.x < D ? code : -code);
-  }
-  __syncthreads();
-  if (s.bad) {
-    if (threadIdx.x == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
-    for (int i = threadIdx.x; i < p.k; i += kThreads) out[i] = -1;
-    return;
-  }
+  return shift;
+}
+__device__ __forceinline__ int code_of(int sum, int shift) { return (sum + (1 << shift) - 1) >> shift; }
 
-  // scores: 8 lanes a page, 16 bytes at a time
-  constexpr int kLoads = 2 * D / 128, kTeams = kThreads / 8, kAhead = 4;
-  const int team = lane / 8, l = lane % 8;
-  int4 code[kLoads];
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j) code[j] = reinterpret_cast<const int4*>(s.codes)[j * 8 + l];
-  for (int first = warp * 4; first < n; first += kTeams * kAhead) {  // by the warp together
-    const int i0 = first + team;
-    int4 box[kAhead][kLoads];
-    float scale[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + a * kTeams;
-      // a page's id is read by its own lanes only, before they put the score there
-      const long long record = (long long)(i < n ? keys[i] : 0u) * p.heads + head;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-        box[a][j] = __ldg(reinterpret_cast<const int4*>(p.bounds + record * (2 * D)) + j * 8 + l);
-      scale[a] = __ldg(p.bound_scale + record);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + a * kTeams;
-      int dot = 0;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        dot = __dp4a(box[a][j].x, code[j].x, dot);
-        dot = __dp4a(box[a][j].y, code[j].y, dot);
-        dot = __dp4a(box[a][j].z, code[j].z, dot);
-        dot = __dp4a(box[a][j].w, code[j].w, dot);
-      }
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
-      if (i < n && l == 0) {
-        const float score = fminf(fmaxf((float)dot * scale[a], -FLT_MAX), FLT_MAX);
-        keys[i] = i < p.first || i >= n - p.last ? 0xffffffffu : ordered(score + 0.f);
-      }
-    }
-  }
-  __syncthreads();
+__device__ __forceinline__ int dot16(int4 a, int4 b, int sum) {
+  sum = __dp4a(a.x, b.x, sum);
+  sum = __dp4a(a.y, b.y, sum);
+  sum = __dp4a(a.z, b.z, sum);
+  return __dp4a(a.w, b.w, sum);
+}
 
-  // the k-th largest key, 8 bits at a time; `rank` of those with its upper bits are taken
-  uint32_t prefix = 0;
-  int rank = p.k;
-#pragma unroll
-  for (int at = 24; at >= 0; at -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kThreads) s.hist[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const uint32_t key = keys[i];
-      if (at == 24 || key >> (at + 8) == prefix) atomicAdd(&s.hist[key >> at & 255u], 1u);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // lane: 8 digits, the largest ones first
-      uint32_t c[8], mine = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mine += c[j] = s.hist[255 - (lane * 8 + j)];
-      uint32_t before = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(kAll, before, o);
-        if (lane >= o) before += v;
-      }
-      before -= mine;
-      if (before < (uint32_t)rank && (uint32_t)rank <= before + mine) {
-        int j = 0;
-        while (before + c[j] < (uint32_t)rank) before += c[j++];
-        s.digit = 255 - (lane * 8 + j), s.rank = rank - (int)before;
-      }
-    }
-    __syncthreads();
-    prefix = prefix << 8 | (uint32_t)s.digit;
-    rank = s.rank;
-  }
+// Pages of a row; 0 where its length is past the table.
+__device__ __forceinline__ int row_pages(const BlockSelectParams& p, int row, bool* past) {
+  const int len = __ldg(p.seqlens + row);
+  *past = (long long)len > (long long)p.W * kPage;
+  return len <= 0 || *past ? 0 : (len - 1) / kPage + 1;
+}
 
-  // a thread takes its run of pages: larger keys, and the first `rank` equal ones
-  const int run = (n + kThreads - 1) / kThreads;
-  const int i0 = min((int)threadIdx.x * run, n), i1 = min(i0 + run, n);
-  uint32_t found = 0;                      // larger ones in the low half, equal ones in the high half
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t key = keys[i];
-    found += key > prefix ? 1u : key == prefix ? 0x10000u : 0u;
-  }
-  uint32_t before = found;
+// ---- rows with tables of their own ---------------------------------------------
+
+constexpr int kBinBits = 10, kBins = 1 << kBinBits;
+constexpr int kBinned = 256;         // keys of a bin that are ranked by all pairs
+
+struct Shared {
+  union {
+    struct {
+      int length[kOrdered], row;
+    } order;
+    int parts[kThreads / 64][2][128];  // partial sums of P and N
+    struct {
+      uint32_t bins[kBins];
+      uint32_t key[kBinned];
+      int index[kBinned];
+    } sort;
+  };
+  alignas(16) uint32_t codes[64];    // p (D bytes), then -n
+  float tops[kWarps];
+  int sizes[kWarps > 8 ? kWarps : 8];  // of queries; then the runs' best ones, summed up
+  uint32_t low[kWarps], high[kWarps], always[kWarps], sums[kWarps];
+  uint32_t bin, rest, inside, listed;  // the k-th largest's bin: keys of it that are taken, keys in it
+  int bad, count;                    // of this block's run: a page outside the pool, pages for the choice
+};
+
+// Sums before this thread's over the block, the threads in order; a barrier inside.
+__device__ __forceinline__ uint32_t sum_before(uint32_t mine, Shared& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t v = __shfl_up_sync(kAll, before, o);
     if (lane >= o) before += v;
   }
   if (lane == 31) s.sums[warp] = before;
-  before -= found;
+  before -= mine;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w)
     if (w < warp) before += s.sums[w];
-  int larger = (int)(before & 0xffffu), equal = (int)(before >> 16);
+  return before;
+}
+
+// Takes the k largest of n >= k keys in shared memory, equal ones from the front:
+// emit(place among them, index), in the order of the indices.  Bins of equal
+// width between the smallest and the largest score; the keys of the bin with the
+// k-th largest are ranked by all pairs (those that are not taken fall to 0), or,
+// where they are too many (equal scores), it is found bit by bit.
+template <typename F>
+__device__ void block_select(uint32_t* keys, int n, int k, Shared& s, F emit) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t low = kAlways, high = 0;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) s.sort.bins[i] = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t key = keys[i];
+    low = min(low, key);
+    if (key != kAlways) high = max(high, key);
+  }
+  low = __reduce_min_sync(kAll, low), high = __reduce_max_sync(kAll, high);
+  if (lane == 0) s.low[warp] = low, s.high[warp] = high;
+  if (threadIdx.x == 0) s.bin = kBins, s.rest = s.inside = s.listed = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) low = min(low, s.low[w]), high = max(high, s.high[w]);
+  const int shift = high > low ? max(0, 32 - kBinBits - __clz(high - low)) : 0;
+  auto bin_of = [&](uint32_t key) { return (key - low) >> shift; };
+  uint32_t always = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t key = keys[i];
+    if (key == kAlways) ++always;
+    else atomicAdd(&s.sort.bins[bin_of(key)], 1u);
+  }
+  always = __reduce_add_sync(kAll, always);
+  if (lane == 0) s.always[warp] = always;
+  __syncthreads();
+  // the bin with the k-th largest, counted from the top: a few bins a thread
+  constexpr int kEach = kBins / kThreads;
+  uint32_t c[kEach], mine = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) mine += c[j] = s.sort.bins[kBins - 1 - (threadIdx.x * kEach + j)];
+  uint32_t above = sum_before(mine, s);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) above += s.always[w];
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    if (above < (uint32_t)k && (uint32_t)k <= above + c[j])
+      s.bin = kBins - 1 - (threadIdx.x * kEach + j), s.rest = k - above, s.inside = c[j];
+    above += c[j];
+  }
+  __syncthreads();
+  const uint32_t bin = s.bin, rest = s.rest, inside = s.inside;
+  // taken: keys above `least`, and the first `equal` ones that equal it
+  uint32_t least = bin < kBins ? low + (bin << shift) : kAlways, equal = n;
+  if (inside > rest && inside <= kBinned) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const uint32_t key = keys[i];
+      if (key != kAlways && bin_of(key) == bin) {
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        s.sort.key[at] = key, s.sort.index[at] = i;
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < inside; i += kThreads) {
+      const uint32_t key = s.sort.key[i];
+      const int index = s.sort.index[i];
+      uint32_t better = 0;
+      for (uint32_t j = 0; j < inside; ++j)
+        better += s.sort.key[j] > key || (s.sort.key[j] == key && s.sort.index[j] < index);
+      if (better >= rest) keys[index] = 0u;  // below every score
+    }
+    __syncthreads();
+  } else if (inside > rest) {
+    auto count = [&](uint32_t from) {
+      int sum = 0;
+      for (int i = threadIdx.x; i < (n + kThreads - 1) / kThreads * kThreads; i += kThreads)
+        sum += __syncthreads_count(i < n && keys[i] >= from);
+      return sum;
+    };
+    for (int bit = shift - 1; bit >= 0; --bit)
+      if (count(least + (1u << bit)) >= k) least += 1u << bit;
+    equal = k - count(least + 1);
+  }
+  const int run = (n + kThreads - 1) / kThreads;
+  const int i0 = min((int)threadIdx.x * run, n), i1 = min(i0 + run, n);
+  uint32_t found = 0;                      // larger ones in the low half, equal ones in the high half
+  for (int i = i0; i < i1; ++i) found += keys[i] > least ? 1u : keys[i] == least ? 0x10000u : 0u;
+  const uint32_t before = sum_before(found, s);
+  uint32_t larger = before & 0xffffu, same = before >> 16;
   for (int i = i0; i < i1; ++i) {
     const uint32_t key = keys[i];
-    if (key > prefix) {
-      out[larger + min(equal, rank)] = i;
+    if (key > least) {
+      emit((int)(larger + min(same, equal)), i);
       ++larger;
-    } else if (key == prefix) {
-      if (equal < rank) out[larger + equal] = i;
-      ++equal;
+    } else if (key == least) {
+      if (same < equal) emit((int)(larger + same), i);
+      ++same;
     }
   }
 }
 
+// Another block's shared memory.
+__device__ __forceinline__ uint32_t far_address(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(sm100::smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t far_load(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Pages of each block's run, at least kRun: a row of few pages is one block's.
+__device__ __forceinline__ int run_of(int n, int blocks) { return max((n + blocks - 1) / blocks, min(n, kRun)); }
+
 template <int D>
-cudaError_t launch_t(const BlockSelectParams& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) block_select_kernel(const BlockSelectParams p, int blocks, int run_max, bool by_length) {
+  extern __shared__ uint32_t keys[];     // [run_max] page ids, then keys; for more blocks than one the best of
+                                         // each run: [most] keys and [most] places, then those of all
+  __shared__ Shared s;
+  const int rank = blockIdx.x % blocks, head = blockIdx.x / blocks % p.heads;
+  int row = blockIdx.x / blocks / p.heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int most = min(run_max, p.k);
+  uint32_t *best = keys + run_max, *place = best + most;
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  if (by_length) {
+    // the longest rows first: blocks start in the order of their numbers
+    const int i = threadIdx.x;
+    if (i < p.rows) s.order.length[i] = __ldg(p.seqlens + i);
+    __syncthreads();
+    if (i < p.rows) {
+      const int mine = s.order.length[i];
+      int before = 0;
+      for (int j = 0; j < p.rows; ++j) before += s.order.length[j] > mine || (s.order.length[j] == mine && j < i);
+      if (before == row) s.order.row = i;
+    }
+    __syncthreads();
+    row = s.order.row;
+    __syncthreads();
+  }
+  bool past;
+  const int n = row_pages(p, row, &past);
+  int* out = p.blocks + ((long long)row * p.heads + head) * p.k;
+  if (past && rank == 0 && threadIdx.x == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
+  if (threadIdx.x == 0) s.bad = 0, s.count = 0;
+  __syncthreads();
+  const int run = run_of(n, blocks), begin = min(rank * run, n), mine = min(run, n - begin);
+  const bool all = n <= p.k;             // every page is taken: no scores
+  if (rank > 0 && mine == 0) return;     // (the cluster's barrier goes by the threads that are there)
+  const int active = max(1, (n + run - 1) / run);
+  const int* table = p.block_table + (long long)row * p.bt_stride + begin;
+  for (int i = threadIdx.x; i < mine; i += kThreads) {
+    int page = __ldg(table + i);
+    if (page < 0 || page >= p.num_pages) s.bad = 1, page = 0;
+    keys[i] = (uint32_t)page;
+  }
+  if (mine > 0 && !all) {
+    // the group's queries
+    const uint16_t* q = p.q + (long long)row * p.q_row + (long long)head * p.group * p.q_head;
+    const int d = threadIdx.x % D, part = threadIdx.x / D;
+    constexpr int kParts = kThreads / D;
+    float top = 0.f;
+    for (int h = part; h < p.group; h += kParts) top = fmaxf(top, fabsf(value(__ldg(q + h * p.q_head + d), p.dtype)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    if (lane == 0) s.tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.tops[w]);
+    const int x = exponent_above(top);
+    int above = 0, below = 0;
+    for (int h = part; h < p.group; h += kParts) {
+      const int i = on_grid(value(__ldg(q + h * p.q_head + d), p.dtype), x);
+      above += max(i, 0), below += max(-i, 0);
+    }
+    s.parts[part][0][d] = above, s.parts[part][1][d] = below;
+    __syncthreads();
+    int sum = 0;
+    if (threadIdx.x < 2 * D) {
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) sum += s.parts[k][threadIdx.x / D][d];
+    }
+    const int size = __reduce_max_sync(kAll, sum);
+    if (lane == 0) s.sizes[warp] = size;
+    __syncthreads();
+    int largest = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) largest = max(largest, s.sizes[w]);
+    if (threadIdx.x < 2 * D) {
+      const int code = code_of(sum, code_shift(largest));
+      reinterpret_cast<int8_t*>(s.codes)[threadIdx.x] = (int8_t)(threadIdx.x < D ? code : -code);
+    }
+    __syncthreads();
+
+    // scores: 8 lanes a page, 16 bytes at a time
+    constexpr int kLoads = 2 * D / 128, kTeams = kThreads / 8, kAhead = 4;
+    const int team = lane / 8, l = lane % 8;
+    int4 code[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) code[j] = reinterpret_cast<const int4*>(s.codes)[j * 8 + l];
+    for (int first = warp * 4; first < mine; first += kTeams * kAhead) {  // by the warp together
+      const int i0 = first + team;
+      int4 box[kAhead][kLoads];
+      float scale[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int i = i0 + a * kTeams;
+        // a page's id is read by its own lanes only, before they put the key there
+        const long long record = (long long)(i < mine ? keys[i] : 0u) * p.heads + head;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+          box[a][j] = __ldg(reinterpret_cast<const int4*>(p.bounds + record * (2 * D)) + j * 8 + l);
+        scale[a] = __ldg(p.bound_scale + record);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int i = i0 + a * kTeams;
+        int dot = 0;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) dot = dot16(box[a][j], code[j], dot);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+        if (i < mine && l == 0) keys[i] = key_of(dot, scale[a], begin + i, n, p);
+      }
+    }
+    __syncthreads();
+    if (run < n) {
+      // the best of the run
+      if (mine <= p.k) {
+        for (int i = threadIdx.x; i < mine; i += kThreads) best[i] = keys[i], place[i] = begin + i;
+      } else {
+        block_select(keys, mine, p.k, s, [&](int at, int i) { best[at] = keys[i], place[at] = begin + i; });
+      }
+      if (threadIdx.x == 0) s.count = min(mine, p.k);
+    }
+  }
+  if (active > 1) {
+    cluster_sync();
+    if (rank == 0) {
+      // where each run's best go among all, and whether a page was bad
+      uint32_t *all_keys = place + most, *all_places = all_keys + blocks * most;
+      if (warp == 0) {
+        const bool other = lane < active;
+        const int count = other ? (int)far_load(far_address(&s.count, lane)) : 0;
+        const bool bad = __any_sync(kAll, other && far_load(far_address(&s.bad, lane)));
+        int before = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(kAll, before, o);
+          if (lane >= o) before += v;
+        }
+        if (other) s.sizes[lane] = before;
+        __syncwarp();
+        if (lane == 0) s.bad = bad;
+      }
+      __syncthreads();
+      const int total = s.sizes[active - 1];
+      for (int i = threadIdx.x; i < total; i += kThreads) {
+        int r = 0;
+        while (i >= s.sizes[r]) ++r;
+        const int at = r ? i - s.sizes[r - 1] : i;
+        all_keys[i] = far_load(far_address(best + at, r)), all_places[i] = far_load(far_address(place + at, r));
+      }
+      __syncthreads();
+      if (!s.bad && !all && run < n) {
+        // no more than k candidates only where the row has no more pages
+        block_select(all_keys, total, p.k, s, [&](int at, int i) { out[at] = (int)all_places[i]; });
+      }
+    }
+    cluster_sync();                      // nobody leaves while its memory is read
+    if (rank > 0) return;
+  } else {
+    __syncthreads();
+  }
+  if (s.bad) {
+    if (threadIdx.x == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
+    for (int i = threadIdx.x; i < p.k; i += kThreads) out[i] = -1;
+  } else if (all) {
+    for (int i = threadIdx.x; i < p.k; i += kThreads) out[i] = i < n ? i : -1;
+  } else if (run >= n) {
+    block_select(keys, n, p.k, s, [&](int at, int i) { out[at] = i; });
+  }
+}
+
+// ---- rows that share a table ------------------------------------------------------
+
+constexpr int kTileThreads = 256, kTileWarps = kTileThreads / 32;
+constexpr int kRows = 16;                // of a block
+constexpr int kTileMaxPages = 2048;      // keys of 16 rows in shared memory: 130 KB
+constexpr int kTileRows = 64;            // fewer rows are spread over more blocks by the other kernel
+
+// Keys of a row in shared memory: eight rows' pairs of keys are in 32 banks.
+constexpr int tile_stride(int W) { return (W + 31) / 32 * 32 + 8; }
+
+// D += A * B, 16 rows x 32 values of 8 bits, 8 columns.
+__device__ __forceinline__ void mma16832(int (&c)[4], int a0, int a1, int a2, int a3, int b0, int b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// One warp: the best k of n > k keys in shared memory, in order.  KEEP: so many
+// keys a lane are kept in registers, and n is at most 32 times that.
+template <int KEEP>
+__device__ __forceinline__ void warp_select(const uint32_t* keys, int n, int k, int lane, int* out) {
+  uint32_t low = 0xffffffffu, high = 0, mine[KEEP ? KEEP : 1];
+  if (KEEP) {
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+      const int i = j * 32 + lane;
+      mine[j] = i < n ? keys[i] : 0u;      // below every key of a score
+      if (i < n) low = min(low, mine[j]), high = max(high, mine[j]);
+    }
+  } else {
+    for (int i = lane; i < n; i += 32) low = min(low, keys[i]), high = max(high, keys[i]);
+  }
+  low = __reduce_min_sync(kAll, low), high = __reduce_max_sync(kAll, high);
+  auto count = [&](uint32_t least) {       // least > 0
+    int c = 0;
+    if (KEEP) {
+#pragma unroll
+      for (int j = 0; j < KEEP; ++j) c += mine[j] >= least;
+    } else {
+#pragma unroll 4
+      for (int i = lane; i < n; i += 32) c += keys[i] >= least;
+    }
+    return __reduce_add_sync(kAll, c);
+  };
+  uint32_t least = high;
+  if (low != high) {
+    int bit = 31 - __clz(low ^ high);
+    least = (high >> bit >> 1) << bit << 1;
+    for (; bit >= 0; --bit) {
+      const int c = count(least | 1u << bit);
+      if (c >= k) least |= 1u << bit;
+      if (c == k) break;
+    }
+  }
+  const int take = k - (least == 0xffffffffu ? 0 : count(least + 1));  // of the equal ones
+  int larger = 0, equal = 0;
+  const uint32_t below = (1u << lane) - 1;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const uint32_t key = i0 + lane < n ? keys[i0 + lane] : 0u;
+    const bool in = i0 + lane < n;
+    const uint32_t more = __ballot_sync(kAll, in && key > least), same = __ballot_sync(kAll, in && key == least);
+    const int l = larger + __popc(more & below), e = equal + __popc(same & below);
+    if (in && (key > least || (key == least && e < take))) out[l + min(e, take)] = i0 + lane;
+    larger += __popc(more), equal += __popc(same);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(const BlockSelectParams p) {
+  extern __shared__ uint32_t keys[];     // [kRows][stride]
+  const int stride = tile_stride(p.W);
+  __shared__ alignas(16) uint32_t codes[kRows][D / 2];  // p (D bytes), then -n
+  __shared__ int pages[kRows];
+  __shared__ int bad_at;                 // the first page of the table that is not in the pool
+  const int row0 = blockIdx.x / p.heads * kRows, head = blockIdx.x % p.heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  if (threadIdx.x == 0) bad_at = INT_MAX;
+  if (threadIdx.x < kRows) {
+    bool past = false;
+    pages[threadIdx.x] = row0 + threadIdx.x < p.rows ? row_pages(p, row0 + threadIdx.x, &past) : 0;
+    if (past) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
+  }
+  __syncthreads();
+  int n_max = 0;
+  uint32_t scored = 0;                   // rows that need scores
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    n_max = max(n_max, pages[r]);
+    if (pages[r] > p.k) scored |= 1u << r;
+  }
+  for (int i = threadIdx.x; i < n_max; i += kTileThreads) {
+    const int page = __ldg(p.block_table + i);
+    if (page < 0 || page >= p.num_pages) atomicMin(&bad_at, i);
+  }
+  // a warp's rows' codes: D / 32 values a lane
+  constexpr int kEach = D / 32;
+  for (int r = warp; r < kRows; r += kTileWarps) {
+    if (!(scored >> r & 1)) continue;
+    const uint16_t* q =
+        p.q + (long long)(row0 + r) * p.q_row + (long long)head * p.group * p.q_head + lane * kEach;
+    auto load = [&](int h, float (&v)[kEach]) {
+      uint32_t u[kEach / 2];
+      if (kEach == 4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(q + h * p.q_head));
+        u[0] = w.x, u[kEach / 2 - 1] = w.y;
+      } else {
+        u[0] = __ldg(reinterpret_cast<const uint32_t*>(q + h * p.q_head));
+      }
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) v[j] = value(j & 1 ? u[j / 2] >> 16 : u[j / 2] & 0xffffu, p.dtype);
+    };
+    float top = 0.f, v[kEach];
+#pragma unroll 4
+    for (int h = 0; h < p.group; ++h) {
+      load(h, v);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) top = fmaxf(top, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    const int x = exponent_above(top);
+    int above[kEach] = {}, below[kEach] = {}, size = 0;
+#pragma unroll 4
+    for (int h = 0; h < p.group; ++h) {
+      load(h, v);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int i = on_grid(v[j], x);
+        above[j] += max(i, 0), below[j] += max(-i, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) size = max(size, max(above[j], below[j]));
+    const int shift = code_shift(__reduce_max_sync(kAll, size));
+    int8_t* to = reinterpret_cast<int8_t*>(codes[r]) + lane * kEach;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) to[j] = (int8_t)code_of(above[j], shift), to[D + j] = (int8_t)-code_of(below[j], shift);
+  }
+  __syncthreads();
+  if (scored) {
+    // Products of 16 rows and 8 pages: a dot product may take its values in any
+    // order, so that lane t of four reads units t, t + 4, ... of 16 bytes of
+    // page and row g as they lie.
+    constexpr int kUnits = 2 * D / 64;     // of a lane
+    const int g = lane >> 2, t = lane & 3;
+    int4 low[kUnits], high[kUnits];        // rows g and g + 8
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      low[u] = reinterpret_cast<const int4*>(codes[g])[t + 4 * u];
+      high[u] = reinterpret_cast<const int4*>(codes[g + 8])[t + 4 * u];
+    }
+    const int n_low = pages[g], n_high = pages[g + 8];
+#pragma unroll 2
+    for (int first = warp * 8; first < n_max; first += kTileWarps * 8) {
+      auto page_at = [&](int i) {
+        const int page = i < n_max ? __ldg(p.block_table + i) : 0;
+        return page < 0 || page >= p.num_pages ? 0LL : (long long)page * p.heads + head;
+      };
+      const int4* from = reinterpret_cast<const int4*>(p.bounds + page_at(first + g) * (2 * D)) + t;
+      int4 box[kUnits];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) box[u] = __ldg(from + 4 * u);
+      int c[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        mma16832(c, low[u].x, high[u].x, low[u].y, high[u].y, box[u].x, box[u].y);
+        mma16832(c, low[u].z, high[u].z, low[u].w, high[u].w, box[u].z, box[u].w);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = first + 2 * t + j;
+        const float scale = __ldg(p.bound_scale + page_at(i));
+        if (i < n_low) keys[g * stride + i] = key_of(c[j], scale, i, n_low, p);
+        if (i < n_high) keys[(g + 8) * stride + i] = key_of(c[2 + j], scale, i, n_high, p);
+      }
+    }
+  }
+  __syncthreads();
+  for (int r = warp; r < kRows; r += kTileWarps) {
+    if (row0 + r >= p.rows) continue;
+    int* out = p.blocks + ((long long)(row0 + r) * p.heads + head) * p.k;
+    const int n = pages[r];
+    if (bad_at < n) {
+      if (lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
+      for (int i = lane; i < p.k; i += 32) out[i] = -1;
+    } else if (n <= p.k) {
+      for (int i = lane; i < p.k; i += 32) out[i] = i < n ? i : -1;
+    } else {
+      if (n <= 512) warp_select<16>(keys + r * stride, n, p.k, lane, out);
+      else warp_select<0>(keys + r * stride, n, p.k, lane, out);
+    }
+  }
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, long long grid, int threads, size_t smem, int cluster, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D>
+cudaError_t launch_t(const BlockSelectParams& p, int sms, cudaStream_t stream) {
   static bool ready[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -251,25 +652,32 @@ cudaError_t launch_t(const BlockSelectParams& p, cudaStream_t stream) {
   if (dev >= kMaxDevices || !ready[dev]) {
     e = cudaFuncSetAttribute(block_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectMaxPages * 4);
     if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(block_select_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kRows * tile_stride(kTileMaxPages) * 4);
+    if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) ready[dev] = true;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)p.rows * p.heads));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)p.W * 4;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_select_kernel<D>, p);
+  if (p.bt_stride == 0 && p.rows >= kTileRows && p.W <= kTileMaxPages)
+    return launch(block_select_tile_kernel<D>, ((long long)p.rows + kRows - 1) / kRows * p.heads,
+                  kTileThreads, (size_t)kRows * tile_stride(p.W) * 4, 1,
+                  stream, p);
+  // More blocks than one for a row while all of them are on the GPU together: the
+  // blocks of a cluster start and end together, and with more of them than fit
+  // the cluster's idle ones keep others out.  A list of many entries leaves no
+  // room for all blocks' best ones beside each other.
+  const long long items = (long long)p.rows * p.heads, slots = (long long)sms * kBlocksPerSm;
+  int blocks = 1;
+  while (blocks < 8 && 2 * blocks * items <= slots && blocks * kRun < p.W && p.k <= kSelectMaxList) blocks *= 2;
+  const int run = std::max((p.W + blocks - 1) / blocks, std::min(p.W, kRun)), most = std::min(run, p.k);
+  const size_t smem = 4 * (size_t)(blocks > 1 ? run + 2 * most + 2 * blocks * most : run);
+  return launch(block_select_kernel<D>, items * blocks, kThreads, smem, blocks, stream, p, blocks, run,
+                items > slots && p.rows <= kOrdered);
 }
 
 }  // namespace
 
-cudaError_t launch_block_select(const BlockSelectParams& p, cudaStream_t stream) {
-  return p.dim == 128 ? launch_t<128>(p, stream) : launch_t<64>(p, stream);
+cudaError_t launch_block_select(const BlockSelectParams& p, int sms, cudaStream_t stream) {
+  return p.dim == 128 ? launch_t<128>(p, sms, stream) : launch_t<64>(p, sms, stream);
 }
 
 }  // namespace dsa

@@ -12,7 +12,7 @@ namespace dsa {
 cudaError_t launch_request_slots(const RequestSlotsParams& p, cudaStream_t stream);
 cudaError_t launch_kv_store(const KvStoreParams& p, int kv_dtype, cudaStream_t stream);
 cudaError_t launch_block_bounds(const BlockBoundsParams& p, int kv_dtype, cudaStream_t stream);
-cudaError_t launch_block_select(const BlockSelectParams& p, cudaStream_t stream);
+cudaError_t launch_block_select(const BlockSelectParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedAttnParams& p, int dim, int kv_dtype, const CUtensorMap& kmap,
                                    const CUtensorMap& vmap, int sms, cudaStream_t stream);
 }  // namespace dsa
@@ -167,7 +167,7 @@ int dsa_block_select(const void* q, long long q_row_stride, long long q_head_str
   if (k <= 0 || first < 0 || last < 0 || (long long)first + last > k || num_pages <= 0) return DSA_ERR_INVALID_ARG;
   DSA_CHECK(check_table(block_table, bt_stride, W));
   // scores in shared memory; sums of a group's queries in 32 bits
-  if (W > dsa::kSelectMaxPages || Hq / Hkv > 1024 || (long long)rows * Hkv >= k2G ||
+  if (W > dsa::kSelectMaxPages || Hq / Hkv > 1024 || (long long)rows * Hkv * 8 >= k2G ||
       (long long)num_pages * dsa::kPage >= k2G)
     return DSA_ERR_UNSUPPORTED;
   if (rows > 0 && (!q || !bounds || !bound_scale || !block_table || !seqlens || !blocks)) return DSA_ERR_INVALID_ARG;
@@ -178,7 +178,9 @@ int dsa_block_select(const void* q, long long q_row_stride, long long q_head_str
   const dsa::BlockSelectParams p{static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, rows, Hkv, Hq / Hkv, D,
                                  dtype, reinterpret_cast<const int8_t*>(bounds), bound_scale, num_pages, block_table,
                                  bt_stride, W, seqlens, k, first, last, blocks, dev_status};
-  return launched(dsa::launch_block_select(p, static_cast<cudaStream_t>(stream)));
+  const int sms = sm_count();
+  if (sms <= 0) return DSA_ERR_CUDA;
+  return launched(dsa::launch_block_select(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 long long dsa_paged_attention_workspace(int Hq, int Hkv, int D) {

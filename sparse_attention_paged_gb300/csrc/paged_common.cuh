@@ -63,8 +63,9 @@ struct BlockBoundsParams {
   int* status;
 };
 
-// The selection keeps a row's scores in shared memory.
-constexpr int kSelectMaxPages = 32768;
+// The selection keeps a row's scores in shared memory, and up to a list's
+// length also the best of several blocks.
+constexpr int kSelectMaxPages = 32768, kSelectMaxList = 1024;
 
 struct BlockSelectParams {
   const uint16_t* q;           // bf16 or fp16 bits, [rows, Hq, dim] through the strides

@@ -131,3 +131,39 @@ def test_data_errors():
     assert (c.out[[0, 1]] == -1).all()
     c.run(8)
     assert (c.out[[0, 1, 3]] == -1).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 7, 7), (128, 16, 2), (128, 12, 1)])
+@pytest.mark.parametrize("low,rows,k", [(1, 200, 3), (1000, 64, 8), (100000, 77, 33), (131000, 70, 700)])
+def test_rows_of_a_prompt(dtype, dim, heads, kv_heads, low, rows, k):
+    """Many rows that share a table: pages from none to all that the shared kernel has room for."""
+    lens = list(range(low - 1, low - 1 + rows))
+    lens[rows // 2] = 0
+    c = Case(lens, heads, kv_heads, dim, dtype, seed=k, shared=True, alike=k == 8)
+    c.run(k).check(rows=sorted({0, 1, rows // 2, rows - 1, *range(0, rows, 13)}))
+
+
+def test_rows_of_a_prompt_data_errors():
+    """A page outside the pool touches the rows that reach it, a length past the table its own."""
+    c = Case(list(range(300, 400)), 4, 2, 64, "bf16", seed=7, shared=True)
+    c.table[0, 5] = 10 ** 7                                # position 320
+    c.seqlens[3] = c.W * 64 + 1
+    c.run(4)
+    assert int(c.status) == 7
+    assert (c.out[3] == -1).all() and (c.out[21:] == -1).all()
+    c.check(status=7, rows=[0, 1, 2, 4, 20])
+
+
+@pytest.mark.parametrize("k", [1, 40, 1024, 1025, 3000])
+@pytest.mark.parametrize("alike", [False, True])
+def test_lists_of_any_length(k, alike):
+    """Rows of one block beside rows of several, lists longer than a block's run and than the joint choice takes."""
+    Case([200000, 64 * 256, 64 * 257, 40000, 100, 0], 2, 1, 64, "bf16", seed=k, alike=alike).run(k, 0, 1).check()
+
+
+def test_bad_page_of_another_block():
+    c = Case([100000, 90000], 2, 1, 64, "bf16", seed=8)
+    c.table[0, 1400] = -1
+    c.run(9).check(status=6, rows=[1])
+    assert (c.out[0] == -1).all()
