@@ -20,7 +20,7 @@
 // bytes a page and head), by latency at short ones.
 //
 // Rows that share a table (a prompt): a block per 16 rows and key head reads the
-// boxes once, on the tensor cores' 8-bit products, and a warp selects for a row.
+// boxes once, multiplies them on the tensor cores, and a warp selects for a row.
 // Bound by its instructions.
 //
 // The k-th largest score is found bit by bit from the top of the scores' common
@@ -57,8 +57,8 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 
 // A page's key: its score's place in the order.
-__device__ __forceinline__ uint32_t key_of(int dot, float scale, int i, int n, const BlockSelectParams& p) {
-  const float score = fminf(fmaxf((float)dot * scale, -FLT_MAX), FLT_MAX);
+__device__ __forceinline__ uint32_t key_of(float dot, float scale, int i, int n, const BlockSelectParams& p) {
+  const float score = fminf(fmaxf(dot * scale, -FLT_MAX), FLT_MAX);
   return i < p.first || i >= n - p.last ? kAlways : ordered(score + 0.f);
 }
 
@@ -68,14 +68,19 @@ __device__ __forceinline__ float value(uint32_t u, int dtype) {
   return fminf(fmaxf(x, -FLT_MAX), FLT_MAX);
 }
 
-// A query value on the group's grid, 2^x above the group's largest magnitude.
-__device__ __forceinline__ int on_grid(float v, int x) { return (int)rintf(scalbnf(v, kGridBits - x)); }
-
-__device__ __forceinline__ int exponent_above(float top) {
-  int x;
-  frexpf(top, &x);
-  return x;
-}
+// A query value on its group's grid: 2^20 times itself over the power of two
+// above the group's largest magnitude.  Two factors, as one can be past 2^127;
+// a product that is not exact is below 1/2.
+struct Grid {
+  float a, b;
+  __device__ __forceinline__ explicit Grid(float top) {
+    int x;
+    frexpf(top, &x);                     // top < 2^x, -148 <= x <= 128
+    const int e = kGridBits - x;
+    a = __uint_as_float((uint32_t)(min(e, 127) + 127) << 23), b = __uint_as_float((uint32_t)(max(e - 127, 0) + 127) << 23);
+  }
+  __device__ __forceinline__ int operator()(float v) const { return __float2int_rn(v * a * b); }
+};
 
 // The smallest s with size <= 127 * 2^s.
 __device__ __forceinline__ int code_shift(int size) {
@@ -313,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) block_select_kernel(co
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.tops[w]);
-    const int x = exponent_above(top);
+    const Grid grid(top);
     int above = 0, below = 0;
     for (int h = part; h < p.group; h += kParts) {
-      const int i = on_grid(value(__ldg(q + h * p.q_head + d), p.dtype), x);
+      const int i = grid(value(__ldg(q + h * p.q_head + d), p.dtype));
       above += max(i, 0), below += max(-i, 0);
     }
     s.parts[part][0][d] = above, s.parts[part][1][d] = below;
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) block_select_kernel(co
         for (int j = 0; j < kLoads; ++j) dot = dot16(box[a][j], code[j], dot);
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
-        if (i < mine && l == 0) keys[i] = key_of(dot, scale[a], begin + i, n, p);
+        if (i < mine && l == 0) keys[i] = key_of((float)dot, scale[a], begin + i, n, p);
       }
     }
     __syncthreads();
@@ -431,77 +436,150 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) block_select_kernel(co
 
 // ---- rows that share a table ------------------------------------------------------
 
-constexpr int kTileThreads = 256, kTileWarps = kTileThreads / 32;
+constexpr int kTileThreads = 512, kTileWarps = kTileThreads / 32;
 constexpr int kRows = 16;                // of a block
 constexpr int kTileMaxPages = 2048;      // keys of 16 rows in shared memory: 130 KB
-constexpr int kTileRows = 64;            // fewer rows are spread over more blocks by the other kernel
 
 // Keys of a row in shared memory: eight rows' pairs of keys are in 32 banks.
 constexpr int tile_stride(int W) { return (W + 31) / 32 * 32 + 8; }
+constexpr int tile_smem(int W) { return (kRows * tile_stride(W) + W) * 4; }
 
-// D += A * B, 16 rows x 32 values of 8 bits, 8 columns.
-__device__ __forceinline__ void mma16832(int (&c)[4], int a0, int a1, int a2, int a3, int b0, int b1) {
+// D += A * B, 16 rows x 16 values (fp16), 8 columns, fp32.
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One warp: the best k of n > k keys in shared memory, in order.  KEEP: so many
-// keys a lane are kept in registers, and n is at most 32 times that.
-template <int KEEP>
-__device__ __forceinline__ void warp_select(const uint32_t* keys, int n, int k, int lane, int* out) {
-  uint32_t low = 0xffffffffu, high = 0, mine[KEEP ? KEEP : 1];
-  if (KEEP) {
-#pragma unroll
-    for (int j = 0; j < KEEP; ++j) {
-      const int i = j * 32 + lane;
-      mine[j] = i < n ? keys[i] : 0u;      // below every key of a score
-      if (i < n) low = min(low, mine[j]), high = max(high, mine[j]);
-    }
-  } else {
-    for (int i = lane; i < n; i += 32) low = min(low, keys[i]), high = max(high, keys[i]);
+// Four 8-bit whole numbers as fp16: the byte plus 128 under the exponent of 1024.
+__device__ __forceinline__ void halves(uint32_t x, uint32_t& low, uint32_t& high) {
+  x ^= 0x80808080u;
+  const uint32_t u[2] = {__byte_perm(x, 0x64646464u, 0x4140), __byte_perm(x, 0x64646464u, 0x4342)};
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+  const __half2 l = __hsub2(*reinterpret_cast<const __half2*>(&u[0]), off);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u[1]), off);
+  low = *reinterpret_cast<const uint32_t*>(&l), high = *reinterpret_cast<const uint32_t*>(&h);
+}
+
+constexpr int kWarpBins = 256;           // as block_select()'s, a warp's own
+
+// One warp: the best k of n > k keys in shared memory, equal ones from the front,
+// in order.  As block_select() does it: the keys of the k-th largest's bin that are
+// not taken fall to 0.
+__device__ __forceinline__ void warp_select(uint32_t* keys, int n, int k, int lane, uint32_t* bins, int* out) {
+  uint32_t low = kAlways, high = 0;
+#pragma unroll 4
+  for (int i = lane; i < n; i += 32) {
+    const uint32_t key = keys[i];
+    low = min(low, key);
+    if (key != kAlways) high = max(high, key);
   }
   low = __reduce_min_sync(kAll, low), high = __reduce_max_sync(kAll, high);
-  auto count = [&](uint32_t least) {       // least > 0
-    int c = 0;
-    if (KEEP) {
+  constexpr int kEach = kWarpBins / 32;
 #pragma unroll
-      for (int j = 0; j < KEEP; ++j) c += mine[j] >= least;
-    } else {
+  for (int j = 0; j < kEach; ++j) bins[j * 32 + lane] = 0;
+  __syncwarp();
+  const int shift = high > low ? max(0, 32 - 8 - __clz(high - low)) : 0;
+  static_assert(kWarpBins == 1 << 8, "the bits of a bin");
+  auto bin_of = [&](uint32_t key) { return (key - low) >> shift; };
+  int above = 0;
 #pragma unroll 4
-      for (int i = lane; i < n; i += 32) c += keys[i] >= least;
-    }
-    return __reduce_add_sync(kAll, c);
-  };
-  uint32_t least = high;
-  if (low != high) {
-    int bit = 31 - __clz(low ^ high);
-    least = (high >> bit >> 1) << bit << 1;
-    for (; bit >= 0; --bit) {
-      const int c = count(least | 1u << bit);
-      if (c >= k) least |= 1u << bit;
-      if (c == k) break;
+  for (int i = lane; i < n; i += 32) {
+    const uint32_t key = keys[i];
+    if (key == kAlways) ++above;
+    else atomicAdd(&bins[bin_of(key)], 1u);
+  }
+  above = __reduce_add_sync(kAll, above);
+  __syncwarp();
+  // lane: bins from the top
+  int c[kEach], mine = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) mine += c[j] = (int)bins[kWarpBins - 1 - (lane * kEach + j)];
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, before, o);
+    if (lane >= o) before += v;
+  }
+  above += before - mine;
+  int bin = -1, rest = 0, inside = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    if (above < k && k <= above + c[j]) bin = kWarpBins - 1 - (lane * kEach + j), rest = k - above, inside = c[j];
+    above += c[j];
+  }
+  const uint32_t owner = __ballot_sync(kAll, bin >= 0);
+  uint32_t least = kAlways;                // no bin: pages that are always taken are all
+  int equal = n;
+  if (owner) {
+    const int from = __ffs(owner) - 1;
+    bin = __shfl_sync(kAll, bin, from), rest = __shfl_sync(kAll, rest, from), inside = __shfl_sync(kAll, inside, from);
+    least = low + ((uint32_t)bin << shift);
+    if (inside > rest && inside <= 32) {
+      // its keys and places beside each other, then each against all
+      int count = 0;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const uint32_t key = i0 + lane < n ? keys[i0 + lane] : kAlways;
+        const bool in = key != kAlways && bin_of(key) == (uint32_t)bin;
+        const uint32_t who = __ballot_sync(kAll, in);
+        if (in) {
+          const int at = count + __popc(who & ((1u << lane) - 1));
+          bins[at] = key, bins[32 + at] = i0 + lane;
+        }
+        count += __popc(who);
+      }
+      __syncwarp();
+      const uint32_t key = bins[lane];
+      int better = 0;
+      for (int j = 0; j < inside; ++j) {
+        const uint32_t other = __shfl_sync(kAll, key, j);
+        better += other > key || (other == key && j < lane);  // places are in order
+      }
+      if (lane < inside && better >= rest) keys[bins[32 + lane]] = 0u;
+      __syncwarp();
+    } else if (inside > rest) {
+      auto count = [&](uint32_t from) {
+        int sum = 0;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) sum += keys[i] >= from;
+        return __reduce_add_sync(kAll, sum);
+      };
+      for (int bit = shift - 1; bit >= 0; --bit)
+        if (count(least + (1u << bit)) >= k) least += 1u << bit;
+      equal = k - count(least + 1);
     }
   }
-  const int take = k - (least == 0xffffffffu ? 0 : count(least + 1));  // of the equal ones
-  int larger = 0, equal = 0;
-  const uint32_t below = (1u << lane) - 1;
+  int larger = 0, same = 0;
+  const uint32_t left = (1u << lane) - 1;
+  if (equal == n) {                        // all from `least` on
+#pragma unroll 4
+    for (int i = lane; i - lane < n; i += 32) {
+      const bool take = i < n && keys[i] >= least;
+      const uint32_t who = __ballot_sync(kAll, take);
+      if (take) out[larger + __popc(who & left)] = i;
+      larger += __popc(who);
+    }
+    return;
+  }
   for (int i0 = 0; i0 < n; i0 += 32) {
-    const uint32_t key = i0 + lane < n ? keys[i0 + lane] : 0u;
     const bool in = i0 + lane < n;
-    const uint32_t more = __ballot_sync(kAll, in && key > least), same = __ballot_sync(kAll, in && key == least);
-    const int l = larger + __popc(more & below), e = equal + __popc(same & below);
-    if (in && (key > least || (key == least && e < take))) out[l + min(e, take)] = i0 + lane;
-    larger += __popc(more), equal += __popc(same);
+    const uint32_t key = in ? keys[i0 + lane] : 0u;
+    const uint32_t more = __ballot_sync(kAll, in && key > least), alike = __ballot_sync(kAll, in && key == least);
+    const int l = larger + __popc(more & left), e = same + __popc(alike & left);
+    if (in && (key > least || (key == least && e < equal))) out[l + min(e, equal)] = i0 + lane;
+    larger += __popc(more), same += __popc(alike);
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(const BlockSelectParams p) {
-  extern __shared__ uint32_t keys[];     // [kRows][stride]
+  extern __shared__ uint32_t keys[];     // [kRows][stride], then the table's page ids
   const int stride = tile_stride(p.W);
-  __shared__ alignas(16) uint32_t codes[kRows][D / 2];  // p (D bytes), then -n
+  int* ids = reinterpret_cast<int*>(keys + kRows * stride);
+  __shared__ alignas(16) uint16_t codes[kRows][2 * D + 8];  // p, then -n, as fp16; rows in other banks
+  __shared__ uint32_t bins[kTileWarps][kWarpBins];
   __shared__ int pages[kRows];
   __shared__ int bad_at;                 // the first page of the table that is not in the pool
   const int row0 = blockIdx.x / p.heads * kRows, head = blockIdx.x % p.heads;
@@ -523,8 +601,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(cons
     if (pages[r] > p.k) scored |= 1u << r;
   }
   for (int i = threadIdx.x; i < n_max; i += kTileThreads) {
-    const int page = __ldg(p.block_table + i);
-    if (page < 0 || page >= p.num_pages) atomicMin(&bad_at, i);
+    int page = __ldg(p.block_table + i);
+    if (page < 0 || page >= p.num_pages) atomicMin(&bad_at, i), page = 0;
+    ids[i] = page;
   }
   // a warp's rows' codes: D / 32 values a lane
   constexpr int kEach = D / 32;
@@ -552,61 +631,71 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(cons
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    const int x = exponent_above(top);
+    const Grid grid(top);
     int above[kEach] = {}, below[kEach] = {}, size = 0;
 #pragma unroll 4
     for (int h = 0; h < p.group; ++h) {
       load(h, v);
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
-        const int i = on_grid(v[j], x);
+        const int i = grid(v[j]);
         above[j] += max(i, 0), below[j] += max(-i, 0);
       }
     }
 #pragma unroll
     for (int j = 0; j < kEach; ++j) size = max(size, max(above[j], below[j]));
     const int shift = code_shift(__reduce_max_sync(kAll, size));
-    int8_t* to = reinterpret_cast<int8_t*>(codes[r]) + lane * kEach;
+    uint16_t* to = codes[r] + lane * kEach;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) to[j] = (int8_t)code_of(above[j], shift), to[D + j] = (int8_t)-code_of(below[j], shift);
+    for (int j = 0; j < kEach; ++j) {
+      to[j] = __half_as_ushort(__int2half_rn(code_of(above[j], shift)));
+      to[D + j] = __half_as_ushort(__int2half_rn(-code_of(below[j], shift)));
+    }
   }
   __syncthreads();
   if (scored) {
-    // Products of 16 rows and 8 pages: a dot product may take its values in any
-    // order, so that lane t of four reads units t, t + 4, ... of 16 bytes of
-    // page and row g as they lie.
+    // Products of 16 rows and 16 pages, whole numbers below 2^24 in fp32: exact.  A
+    // dot product may take its values in any order, so that lane t of four reads
+    // units t, t + 4, ... of 16 codes of a page as they lie, and rows likewise.
     constexpr int kUnits = 2 * D / 64;     // of a lane
     const int g = lane >> 2, t = lane & 3;
-    int4 low[kUnits], high[kUnits];        // rows g and g + 8
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      low[u] = reinterpret_cast<const int4*>(codes[g])[t + 4 * u];
-      high[u] = reinterpret_cast<const int4*>(codes[g + 8])[t + 4 * u];
-    }
     const int n_low = pages[g], n_high = pages[g + 8];
-#pragma unroll 2
-    for (int first = warp * 8; first < n_max; first += kTileWarps * 8) {
-      auto page_at = [&](int i) {
-        const int page = i < n_max ? __ldg(p.block_table + i) : 0;
-        return page < 0 || page >= p.num_pages ? 0LL : (long long)page * p.heads + head;
-      };
-      const int4* from = reinterpret_cast<const int4*>(p.bounds + page_at(first + g) * (2 * D)) + t;
-      int4 box[kUnits];
+    auto record = [&](int i) { return (long long)(i < n_max ? ids[i] : 0) * p.heads + head; };
+    for (int first = warp * 16; first < n_max; first += kTileWarps * 16) {
+      int4 box[2][kUnits];
+      float scale[2][2];
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) box[u] = __ldg(from + 4 * u);
-      int c[4] = {0, 0, 0, 0};
+      for (int w = 0; w < 2; ++w) {
+        const int4* from = reinterpret_cast<const int4*>(p.bounds + record(first + 8 * w + g) * (2 * D)) + t;
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        mma16832(c, low[u].x, high[u].x, low[u].y, high[u].y, box[u].x, box[u].y);
-        mma16832(c, low[u].z, high[u].z, low[u].w, high[u].w, box[u].z, box[u].w);
+        for (int u = 0; u < kUnits; ++u) box[w][u] = __ldg(from + 4 * u);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) scale[w][j] = __ldg(p.bound_scale + record(first + 8 * w + 2 * t + j));
       }
+      float c[2][4] = {};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = first + 2 * t + j;
-        const float scale = __ldg(p.bound_scale + page_at(i));
-        if (i < n_low) keys[g * stride + i] = key_of(c[j], scale, i, n_low, p);
-        if (i < n_high) keys[(g + 8) * stride + i] = key_of(c[2 + j], scale, i, n_high, p);
-      }
+      for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {      // halves of a unit: 8 codes
+          const uint4 a = *reinterpret_cast<const uint4*>(codes[g] + (t + 4 * u) * 16 + v * 8);
+          const uint4 b = *reinterpret_cast<const uint4*>(codes[g + 8] + (t + 4 * u) * 16 + v * 8);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint32_t x, y;
+            halves(v ? box[w][u].z : box[w][u].x, x, y);
+            mma16816(c[w], a.x, b.x, a.y, b.y, x, y);
+            halves(v ? box[w][u].w : box[w][u].y, x, y);
+            mma16816(c[w], a.z, b.z, a.w, b.w, x, y);
+          }
+        }
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int i = first + 8 * w + 2 * t + j;
+          if (i < n_low) keys[g * stride + i] = key_of(c[w][j], scale[w][j], i, n_low, p);
+          if (i < n_high) keys[(g + 8) * stride + i] = key_of(c[w][2 + j], scale[w][j], i, n_high, p);
+        }
     }
   }
   __syncthreads();
@@ -620,8 +709,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(cons
     } else if (n <= p.k) {
       for (int i = lane; i < p.k; i += 32) out[i] = i < n ? i : -1;
     } else {
-      if (n <= 512) warp_select<16>(keys + r * stride, n, p.k, lane, out);
-      else warp_select<0>(keys + r * stride, n, p.k, lane, out);
+      warp_select(keys + r * stride, n, p.k, lane, bins[warp], out);
     }
   }
 }
@@ -653,19 +741,21 @@ cudaError_t launch_t(const BlockSelectParams& p, int sms, cudaStream_t stream) {
     e = cudaFuncSetAttribute(block_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectMaxPages * 4);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(block_select_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kRows * tile_stride(kTileMaxPages) * 4);
+                             tile_smem(kTileMaxPages));
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) ready[dev] = true;
   }
-  if (p.bt_stride == 0 && p.rows >= kTileRows && p.W <= kTileMaxPages)
-    return launch(block_select_tile_kernel<D>, ((long long)p.rows + kRows - 1) / kRows * p.heads,
-                  kTileThreads, (size_t)kRows * tile_stride(p.W) * 4, 1,
-                  stream, p);
+  const long long items = (long long)p.rows * p.heads, slots = (long long)sms * kBlocksPerSm;
+  // Rows of a shared table by 16 once they fill the GPU: 352 pages, 8 heads, 32
+  // rows 11.0 us and 17.4 by 16, 64 rows 21.2 and 17.5, 256 rows 62.9 and 17.7; 2,048
+  // pages, 32 rows 25.4 and 52.6, 64 rows 47.6 and 52.8, 256 rows 147 and 53.
+  if (p.bt_stride == 0 && items > slots && p.W <= kTileMaxPages)
+    return launch(block_select_tile_kernel<D>, ((long long)p.rows + kRows - 1) / kRows * p.heads, kTileThreads,
+                  tile_smem(p.W), 1, stream, p);
   // More blocks than one for a row while all of them are on the GPU together: the
   // blocks of a cluster start and end together, and with more of them than fit
   // the cluster's idle ones keep others out.  A list of many entries leaves no
   // room for all blocks' best ones beside each other.
-  const long long items = (long long)p.rows * p.heads, slots = (long long)sms * kBlocksPerSm;
   int blocks = 1;
   while (blocks < 8 && 2 * blocks * items <= slots && blocks * kRun < p.W && p.k <= kSelectMaxList) blocks *= 2;
   const int run = std::max((p.W + blocks - 1) / blocks, std::min(p.W, kRun)), most = std::min(run, p.k);

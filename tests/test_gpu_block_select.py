@@ -135,18 +135,18 @@ def test_data_errors():
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("dim,heads,kv_heads", [(64, 7, 7), (128, 16, 2), (128, 12, 1)])
-@pytest.mark.parametrize("low,rows,k", [(1, 200, 3), (1000, 64, 8), (100000, 77, 33), (131000, 70, 700)])
+@pytest.mark.parametrize("low,rows,k", [(1, 400, 3), (1000, 333, 8), (100000, 310, 33), (131000, 306, 700)])
 def test_rows_of_a_prompt(dtype, dim, heads, kv_heads, low, rows, k):
     """Many rows that share a table: pages from none to all that the shared kernel has room for."""
     lens = list(range(low - 1, low - 1 + rows))
     lens[rows // 2] = 0
     c = Case(lens, heads, kv_heads, dim, dtype, seed=k, shared=True, alike=k == 8)
-    c.run(k).check(rows=sorted({0, 1, rows // 2, rows - 1, *range(0, rows, 13)}))
+    c.run(k).check(rows=sorted({0, 1, rows // 2, rows - 1, *range(0, rows, 37)}))
 
 
 def test_rows_of_a_prompt_data_errors():
     """A page outside the pool touches the rows that reach it, a length past the table its own."""
-    c = Case(list(range(300, 400)), 4, 2, 64, "bf16", seed=7, shared=True)
+    c = Case(list(range(300, 500)), 4, 2, 64, "bf16", seed=7, shared=True)
     c.table[0, 5] = 10 ** 7                                # position 320
     c.seqlens[3] = c.W * 64 + 1
     c.run(4)
