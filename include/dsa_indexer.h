@@ -580,8 +580,9 @@ int dsa_block_select(const void* q, long long q_row_stride, long long q_head_str
  * head's largest and to 2^-39 of it below; weights times the tokens' value
  * scales as fp16, rounded by 2^-11 of themselves and by 2^-31 of the row's
  * largest where they are below 2^-20 of it.  The same call gives the same bits.
- * Two kernel launches, whose shapes depend on Hq / Hkv and D only: a captured
- * call may be replayed with other lengths, lists and tables.
+ * One kernel launch for few rows of narrow tables or short lists, else two;
+ * their shapes depend on the arguments, not on lengths, lists or tables: a
+ * captured call may be replayed with others of those.
  * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
  * visible token without a page in the pool NaN for the heads that see it and
  * DSA_ERR_BAD_PAGE; a wait that runs out DSA_ERR_TIMEOUT and NaN rows.

@@ -43,7 +43,8 @@
 // Work: units of one page of one key head (a group of more than 32 query heads
 // is several), rows in order, cut into equal slices, one per CTA.  A row that a
 // slice cuts leaves partial sums in the workspace, joined by a second kernel in
-// the order of the slices: the same bits every time.
+// the order of the slices: the same bits every time.  Few short rows are not cut
+// by slices but shared by the CTAs of a cluster, in one launch.
 //
 // Warps: the last one walks the slice (lengths, list, table; 32 pages at a
 // time) and issues TMA, the others compute.
@@ -74,8 +75,9 @@ constexpr uint32_t kWaitLimit = DSA_WAIT_LIMIT_CYCLES < 2000000000ll ? DSA_WAIT_
 constexpr unsigned kAll = 0xffffffffu;
 
 // Shapes of one instance: cache type, values per head, column tiles of 8 query
-// heads per warp, and sets of four warps with heads of their own.
-template <int KV, int D, int NT, int MT>
+// heads per warp, sets of four warps with heads of their own, and whether a
+// cluster's CTAs share a row.
+template <int KV, int D, int NT, int MT, bool CL>
 struct Shape {
   static constexpr bool kFp8 = KV == DSA_KV_FP8_E4M3;
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
@@ -93,12 +95,15 @@ struct Shape {
   static constexpr int kThreads = (kConsumers + 1) * 32;
   static constexpr int kMisc = 4096;
   static constexpr int kRoom = (233472 / kCtas - 1024 - 1024 - kMisc) / kStage;
-  static constexpr int kStages = kRoom < 8 ? kRoom : 8;
-  static constexpr int kSmem = kStages * kStage + kMisc + 1024;
+  static constexpr int kStages = (kRoom < 8 ? kRoom : 8) - CL;  // a cluster's CTAs exchange results in the last one
+  static constexpr int kOffSums = kStages * kStage;            // [heads][D] sums, then [heads][4] statistics
+  static constexpr int kOffMisc = (kStages + CL) * kStage;
+  static constexpr int kSmem = kOffMisc + kMisc + 1024;
   // the four token slices of a row meet in a stage's keys and values, some columns at a time
   static constexpr int kWant = 4 * kHeadsMax * D * 4 / (2 * kSide), kPasses = kWant < 1 ? 1 : kWant;
   static constexpr int kCols = D / kPasses;
-  static_assert(kStages >= 3 && kSmem <= 232448 && kCols >= 8 && kPasses * kCols == D, "shape");
+  static_assert(kStages >= 2 && kSmem <= 232448 && kCols >= 8 && kPasses * kCols == D, "shape");
+  static_assert(kHeadsMax * (D + 4) * 4 <= kStage, "results of a cluster's CTA");
 };
 
 struct Misc {
@@ -108,6 +113,7 @@ struct Misc {
   int scan[16];
   int begin, end, share, total;  // the slice, units per CTA, units in all
   int row, tile, unit;           // the slice's first unit
+  int rank;                      // in a cluster
   // per consumer warp and head: maximum, reference of the sums, total.  Two of
   // them in turn: a warp may reach the end of the next row while another still
   // reads those of this one.
@@ -163,6 +169,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, float4 v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   uint32_t v;
@@ -283,12 +292,39 @@ __device__ void find_slice(const PagedAttnParams& p, Misc* m) {
   __syncthreads();
 }
 
+// The same for a CTA of a cluster, which shares the units of one row and head tile.
+__device__ void cluster_slice(const PagedAttnParams& p, Misc* m, int ctas) {
+  if (threadIdx.x == 0) {
+    const int rank = blockIdx.x % ctas, item = blockIdx.x / ctas, per_row = p.heads * p.tiles;
+    const int n = row_units(p, __ldg(p.seqlens + item / per_row)), share = max(1, (n + ctas - 1) / ctas);
+    m->row = item / per_row, m->tile = item % per_row, m->rank = rank, m->total = n, m->share = share;
+    m->unit = m->begin = min(rank * share, n), m->end = min(m->begin + share, n);
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// 16 bytes of another CTA's shared memory; `at` is the address in this one's.
+__device__ __forceinline__ float4 far_load(uint32_t at, int rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
 // ---- the warp that loads ------------------------------------------------------
 
-template <int KV, int D, int NT, int MT>
+template <int KV, int D, int NT, int MT, bool CL>
 __device__ void produce(const PagedAttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, Misc* m,
                         uint32_t stages) {
-  using S = Shape<KV, D, NT, MT>;
+  using S = Shape<KV, D, NT, MT, CL>;
   const int lane = threadIdx.x & 31;
   Waiter wait{p.status, true};
   int stage = 0, issued = 0;
@@ -404,9 +440,9 @@ __device__ void produce(const PagedAttnParams& p, const CUtensorMap* kmap, const
 
 // ---- the warps that compute -----------------------------------------------------
 
-template <int KV, int D, int NT, int MT>
+template <int KV, int D, int NT, int MT, bool CL>
 struct Consumer {
-  using S = Shape<KV, D, NT, MT>;
+  using S = Shape<KV, D, NT, MT, CL>;
   static constexpr bool kFp8 = S::kFp8;
   static constexpr bool kHalf = KV != DSA_KV_BF16;    // the products' operands are fp16
   static constexpr int kSteps = D / 16;               // k steps of S^T, and row tiles of O^T
@@ -422,11 +458,15 @@ struct Consumer {
   // factor from a product to log2 units
   float top[NT][2], ref[NT][2], sum[NT][2], qf[NT][2];
   Waiter wait;
-  uint32_t meet_phase, turn;
+  uint32_t meet_phase, turn, smem;
 
-  __device__ Consumer(const PagedAttnParams& params, Misc* misc, int w, int l)
+  __device__ Consumer(const PagedAttnParams& params, Misc* misc, int w, int l, uint32_t shared)
       : p(params), m(misc), warp(w), lane(l), g(l >> 2), t(l & 3), slice(w & 3), mt(w >> 2), heads(0),
-        wait{params.status, true}, meet_phase(0), turn(0) {}
+        wait{params.status, true}, meet_phase(0), turn(0), smem(shared) {}
+
+  // Where a cluster's CTA leaves its sums (head h of its tile) and statistics.
+  __device__ __forceinline__ uint32_t sums_at(int h) const { return smem + S::kOffSums + h * D * 4; }
+  __device__ __forceinline__ uint32_t stat_at(int h) const { return smem + S::kOffSums + (S::kHeadsMax * D + h * 4) * 4; }
 
   // All consumer warps.
   __device__ __forceinline__ bool meet() {
@@ -776,6 +816,12 @@ struct Consumer {
         }
         if (meta.z & kBad) total = CUDART_NAN_F;
         const int c0 = pass * S::kCols + col;
+        if (CL && !whole) {
+          sts128(sums_at(row) + c0 * 4, make_float4(x[0], x[1], x[2], x[3]));
+          sts128(sums_at(row) + c0 * 4 + 16, make_float4(x[4], x[5], x[6], x[7]));
+          if (c0 == 0) sts128(stat_at(row), make_float4(big, high, total, 0.f));
+          continue;
+        }
         if (!whole) {
           float4* to = reinterpret_cast<float4*>(part + (long long)row * D + c0);
           to[0] = make_float4(x[0], x[1], x[2], x[3]), to[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -788,7 +834,7 @@ struct Consumer {
       if (pass + 1 < S::kPasses && !meet()) return;
     }
     if ((meta.z & kBad) && warp == 0 && lane == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
-    if (!whole && piece == 1 && warp == 0 && lane == 0) {
+    if (!CL && !whole && piece == 1 && warp == 0 && lane == 0) {
       int4* record = reinterpret_cast<int4*>(p.ws + (long long)gridDim.x * 2 * hv * (D + 4)) + blockIdx.x;
       *record = make_int4(meta.x, meta.y, meta.w, 0);
     }
@@ -826,6 +872,15 @@ struct Consumer {
 
   // Rows without units: zeros, or NaN where the length is past the table.
   __device__ void empty_rows() {
+    if (CL) {
+      // the cluster's row and heads, by its first CTA
+      if (m->total > 0 || m->rank > 0) return;
+      const bool bad = __ldg(p.seqlens + m->row) > 0;
+      if (bad && warp == 0 && lane == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
+      const int group0 = (m->tile % p.tiles) * S::kHeadsMax, h0 = (m->tile / p.tiles) * p.group + group0;
+      fill(m->row, h0, h0 + min(S::kHeadsMax, p.group - group0), bad, warp * 32 + lane, S::kConsumers * 32);
+      return;
+    }
     for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
       const int len = __ldg(p.seqlens + row);
       if (row_units(p, len) > 0) continue;
@@ -837,9 +892,13 @@ struct Consumer {
 
   // After a wait that ran out: NaN for every row of the slice, and for its partial results.
   __device__ void poison() {
+    if (CL) {
+      for (int h = lane; h < S::kHeadsMax; h += 32) sts128(stat_at(h), make_float4(0.f, 0.f, CUDART_NAN_F, 0.f));
+      if (m->share < m->total) return;     // (one CTA's row: below)
+    }
     const int hv = paged_cta_heads(p.group);
     float* part = p.ws + (long long)blockIdx.x * 2 * hv * (D + 4);
-    for (int i = lane; i < 2 * hv; i += 32)
+    for (int i = lane; !CL && i < 2 * hv; i += 32)
       *reinterpret_cast<float4*>(part + (long long)(i / hv) * hv * (D + 4) + (long long)hv * D + (i % hv) * 4) =
           make_float4(0.f, 0.f, CUDART_NAN_F, 0.f);
     int left = m->end - m->begin, row = m->row, tile = m->tile, unit = m->unit;
@@ -857,8 +916,8 @@ struct Consumer {
     }
   }
 
-  __device__ void run(uint8_t* smem) {
-    if (warp == 0 && lane == 0) {
+  __device__ void run(uint8_t* stages) {
+    if (!CL && warp == 0 && lane == 0) {
       const int hv = paged_cta_heads(p.group);
       reinterpret_cast<int4*>(p.ws + (long long)gridDim.x * 2 * hv * (D + 4))[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
@@ -869,7 +928,7 @@ struct Consumer {
     while (wait(&m->full[stage], phase)) {
       const int4 meta = m->meta[stage];
       if (meta.z & kDone) return;
-      uint8_t* at = smem + stage * S::kStage;
+      uint8_t* at = stages + stage * S::kStage;
       const uint32_t base = smem_u32(at);
       const int tokens = meta.z & 127;
       if (meta.z & kBegin) {
@@ -889,16 +948,47 @@ struct Consumer {
     }
     poison();
   }
+
+  // After the cluster's barrier: the row's results from all its CTAs' sums, some
+  // heads and columns by each CTA.
+  __device__ void join_cluster(int ctas) {
+    const int active = (m->total + m->share - 1) / m->share;
+    if (active < 2) return;
+    const int group0 = (m->tile % p.tiles) * S::kHeadsMax, h0 = (m->tile / p.tiles) * p.group + group0;
+    const int all = min(S::kHeadsMax, p.group - group0) * (D / 8);
+    for (int i = m->rank * S::kConsumers * 32 + warp * 32 + lane; i < all; i += ctas * S::kConsumers * 32) {
+      const int h = i / (D / 8), c0 = i % (D / 8) * 8;
+      float4 st[8], a[8], b[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < active)
+          st[r] = far_load(stat_at(h), r), a[r] = far_load(sums_at(h) + c0 * 4, r), b[r] = far_load(sums_at(h) + c0 * 4 + 16, r);
+      float big = -CUDART_INF_F, high = -CUDART_INF_F, total = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < active) big = fmaxf(big, st[r].x), high = fmaxf(high, st[r].y);
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < active) {
+          total += st[r].x == -CUDART_INF_F ? st[r].z : st[r].z * ex2(st[r].x - big);
+          const float w = st[r].y == -CUDART_INF_F ? 0.f : ex2(st[r].y - high);
+          x[0] += w * a[r].x, x[1] += w * a[r].y, x[2] += w * a[r].z, x[3] += w * a[r].w;
+          x[4] += w * b[r].x, x[5] += w * b[r].y, x[6] += w * b[r].z, x[7] += w * b[r].w;
+        }
+      write_out(p, m->row, h0 + h, c0, x, big, high, total);
+    }
+  }
 };
 
-template <int KV, int D, int NT, int MT>
-__global__ void __launch_bounds__(Shape<KV, D, NT, MT>::kThreads, Shape<KV, D, NT, MT>::kCtas)
+template <int KV, int D, int NT, int MT, bool CL>
+__global__ void __launch_bounds__(Shape<KV, D, NT, MT, CL>::kThreads, Shape<KV, D, NT, MT, CL>::kCtas)
     paged_attention_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap kmap,
-                           const __grid_constant__ CUtensorMap vmap) {
-  using S = Shape<KV, D, NT, MT>;
+                           const __grid_constant__ CUtensorMap vmap, int cluster) {
+  using S = Shape<KV, D, NT, MT, CL>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  Misc* m = reinterpret_cast<Misc*>(smem + S::kStages * S::kStage);
+  Misc* m = reinterpret_cast<Misc*>(smem + S::kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -912,12 +1002,24 @@ __global__ void __launch_bounds__(Shape<KV, D, NT, MT>::kThreads, Shape<KV, D, N
   }
   griddep_wait();
   griddep_launch_dependents();
-  find_slice<S::kThreads>(p, m);             // its barriers also publish the mbarriers
+  // (the barriers in these also publish the mbarriers)
+  if (CL) cluster_slice(p, m, cluster);
+  else find_slice<S::kThreads>(p, m);
   if (warp == S::kConsumers) {
-    produce<KV, D, NT, MT>(p, &kmap, &vmap, m, smem_u32(smem));
+    produce<KV, D, NT, MT, CL>(p, &kmap, &vmap, m, smem_u32(smem));
   } else {
-    Consumer<KV, D, NT, MT> c(p, m, warp, lane);
+    Consumer<KV, D, NT, MT, CL> c(p, m, warp, lane, smem_u32(smem));
     c.run(smem);
+  }
+  if (CL) {
+    __syncwarp();
+    cluster_sync();
+    if (warp < S::kConsumers) {
+      Consumer<KV, D, NT, MT, CL> c(p, m, warp, lane, smem_u32(smem));
+      c.join_cluster(cluster);
+    }
+    __syncwarp();
+    cluster_sync();                          // nobody leaves while its memory is read
   }
 }
 
@@ -993,42 +1095,69 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     for (int k = 0; k < kGroups; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] += sums[k][c0 + i];
-    Consumer<KV, D, 1, 1>::write_out(p, row, (tile / p.tiles) * p.group + group0 + h, c0, y, big, high, total);
+    Consumer<KV, D, 1, 1, false>::write_out(p, row, (tile / p.tiles) * p.group + group0 + h, c0, y, big, high, total);
   }
 }
 
 template <typename K, typename... A>
-cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// The kernel's shared memory, allowed once per device.
+template <int KV, int D, int NT, int MT, bool CL>
+cudaError_t set_up() {
+  static bool ready[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < kMaxDevices && ready[dev])) return e;
+  e = cudaFuncSetAttribute(paged_attention_kernel<KV, D, NT, MT, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Shape<KV, D, NT, MT, CL>::kSmem);
+  if (e == cudaSuccess && dev < kMaxDevices) ready[dev] = true;
+  return e;
+}
+
+// Few short rows: a cluster of CTAs for each row and head tile, which join their
+// results in their own memory; one launch where the balanced split takes two.  Up
+// to so many pages a CTA, by the table's width (rows may be of any lengths) or by
+// the lists (rows mostly are alike).  Measured, 32 heads on 8, 128 values, bf16,
+// a cluster and the split: one row of 1,024 tokens 6.3 us and 8.5, of 4,096 9.2
+// and 9.8, of 8,192 13.0 and 10.8; 16 rows of 1,024 10.7 and 13.0; fp8, lists of 32
+// pages, one row 8.8 and 10.6, 16 rows 17.7 and 20.5.
+constexpr int kClusterPages = 8, kClusterEntries = 16;
 
 template <int KV, int D, int NT, int MT>
 cudaError_t launch_t(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
                      cudaStream_t stream) {
-  using S = Shape<KV, D, NT, MT>;
-  static bool ready[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= kMaxDevices || !ready[dev]) {
-    e = cudaFuncSetAttribute(paged_attention_kernel<KV, D, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices) ready[dev] = true;
-  }
+  using S = Shape<KV, D, NT, MT, false>;
   const int ctas = sms * S::kCtas;
-  e = launch(paged_attention_kernel<KV, D, NT, MT>, dim3(ctas), S::kThreads, S::kSmem, stream, p, kmap, vmap);
+  const long long items = (long long)p.rows * p.heads * p.tiles, most = p.blocks ? p.k : p.W;
+  int cluster = 1;
+  while (cluster < 8 && 2 * cluster * items <= ctas && cluster < most) cluster *= 2;
+  if (cluster > 1 && most <= (long long)cluster * (p.blocks ? kClusterEntries : kClusterPages)) {
+    using C = Shape<KV, D, NT, MT, true>;
+    const cudaError_t e = set_up<KV, D, NT, MT, true>();
+    if (e != cudaSuccess) return e;
+    return launch(paged_attention_kernel<KV, D, NT, MT, true>, dim3((unsigned)items * cluster), C::kThreads, C::kSmem,
+                  cluster, stream, p, kmap, vmap, cluster);
+  }
+  cudaError_t e = set_up<KV, D, NT, MT, false>();
   if (e != cudaSuccess) return e;
-  return launch(paged_join_kernel<KV, D>, dim3(ctas, paged_cta_heads(p.group)), kJoinThreads, 0, stream, p, ctas,
+  e = launch(paged_attention_kernel<KV, D, NT, MT, false>, dim3(ctas), S::kThreads, S::kSmem, 1, stream, p, kmap, vmap, 1);
+  if (e != cudaSuccess) return e;
+  return launch(paged_join_kernel<KV, D>, dim3(ctas, paged_cta_heads(p.group)), kJoinThreads, 0, 1, stream, p, ctas,
                 S::kHeadsMax);
 }
 

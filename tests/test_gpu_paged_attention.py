@@ -12,6 +12,7 @@ from tests import paged_ref as ref
 pytestmark = pytest.mark.gpu
 
 PAGE = ref.PAGE
+WIDE = 300                                               # a table of so many pages is not a cluster's
 KINDS = [("bf16", "bf16"), ("fp16", "fp16"), ("fp8", "bf16"), ("fp8", "fp16")]   # cache, queries
 
 
@@ -92,23 +93,36 @@ class Case:
 @pytest.mark.parametrize("kv,dtype", KINDS)
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("heads,kv_heads", [(8, 1), (35, 5)])
-def test_one_page_and_less(kv, dtype, dim, heads, kv_heads):
-    Case([1, 2, 15, 16, 17, 33, 63, 64, 0], heads, kv_heads, dim, kv, dtype, seed=1).run().check()
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_one_page_and_less(kv, dtype, dim, heads, kv_heads, W):
+    Case([1, 2, 15, 16, 17, 33, 63, 64, 0], heads, kv_heads, dim, kv, dtype, seed=1, W=W).run().check()
 
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("layout", ["head", "token", "both", "wide"])
-def test_layouts(kv, dtype, dim, layout):
-    Case([65, 0, 200, 129, 640], 12, 3, dim, kv, dtype, layout, seed=2).run().check()
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_layouts(kv, dtype, dim, layout, W):
+    Case([65, 0, 200, 129, 640], 12, 3, dim, kv, dtype, layout, seed=2, W=W).run().check()
 
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("group", [1, 2, 7, 8, 9, 16, 17, 24, 32, 33, 40, 64, 100])
-def test_groups(kv, dtype, dim, group):
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_groups(kv, dtype, dim, group, W):
     """Query heads of a key head: less than a tile, whole ones, more than a CTA takes."""
-    Case([100, 700], 2 * group, 2, dim, kv, dtype, "token", seed=group).run().check()
+    Case([100, 700], 2 * group, 2, dim, kv, dtype, "token", seed=group, W=W).run().check()
+
+
+@pytest.mark.parametrize("kv,dtype", KINDS)
+@pytest.mark.parametrize("rows,lens", [(1, [500]), (1, [512]), (1, [2]), (2, [4000, 130]), (9, [64, 0, 640, 1, 1024]), (20, [500, 0, 9]),
+                                       (38, [70, 256])])
+def test_rows_of_a_cluster(kv, dtype, rows, lens):
+    """Clusters of all sizes, with CTAs that have no page, and rows of one CTA or none."""
+    lens = (lens * rows)[:rows]
+    Case(lens, 20, 4, 128, kv, dtype, seed=rows).run().check()
+    Case(lens, 8, 4, 64, kv, dtype, seed=rows).run().check()
 
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
@@ -128,7 +142,7 @@ def test_many_rows(kv, dtype, rows, heads):
 
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
-@pytest.mark.parametrize("k", [1, 5, 32, 33, 70])
+@pytest.mark.parametrize("k", [1, 5, 32, 33, 70, 128, 129, 200])
 def test_lists(kv, dtype, k):
     """Lists in any order, with holes, entries past the row, a page twice, none at all; a list a head."""
     lens, H = [1000, 64, 0, 4000, 1, 2300], 3
@@ -182,9 +196,10 @@ def test_strided_queries_and_results(kv, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("power", [-40, -120])
-def test_fp8_scales_apart(dtype, power):
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_fp8_scales_apart(dtype, power, W):
     """Value scales from 2^power to 1 within a row: tokens of large values beside small and zero ones."""
-    c = Case([500], 8, 1, 128, "fp8", dtype, seed=7, spread=0.0)
+    c = Case([500], 8, 1, 128, "fp8", dtype, seed=7, spread=0.0, W=W)
     page, slot = c.tokens(0, 0)
     t = torch.arange(500)
     c.pools.v_scale[page, 0, slot] = torch.where(t % 3 == 0, 2.0 ** power, 1.0)
@@ -199,11 +214,12 @@ def test_fp8_scales_apart(dtype, power):
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
 @pytest.mark.parametrize("factor", [2.0 ** -60, 30.0, 2000.0])
-def test_scores_of_any_size(kv, dtype, factor):
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_scores_of_any_size(kv, dtype, factor, W):
     """From a uniform softmax to one token that takes all."""
     if dtype == "fp16" and factor < 1:
         factor = 2.0 ** -14
-    c = Case([777, 64], 8, 2, 64, kv, dtype, seed=8, spread=0.0)
+    c = Case([777, 64], 8, 2, 64, kv, dtype, seed=8, spread=0.0, W=W)
     c.q = (c.q.double() * factor).to(c.dtype)
     c.run().check()
 
@@ -232,9 +248,10 @@ def test_nan_of_a_visible_token(kv, dtype):
 
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
-def test_data_errors(kv, dtype):
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_data_errors(kv, dtype, W):
     """A length past the table, pages outside the pool: NaN, a status, and the other rows as they are."""
-    c = Case([300, 200, 64, 1000], 8, 2, 128, kv, dtype, seed=11)
+    c = Case([300, 200, 64, 1000], 8, 2, 128, kv, dtype, seed=11, W=W)
     c.table[1, 2] = 10 ** 6
     c.seqlens[2] = c.W * PAGE + 1
     c.run()
@@ -263,8 +280,9 @@ def test_bad_page_that_no_list_names():
 
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
-def test_same_bits_every_time(kv, dtype):
-    c = Case([5000, 64, 700, 12000], 16, 2, 128, kv, dtype, seed=14)
+@pytest.mark.parametrize("lens", [[5000, 64, 700, 12000], [900, 64, 3, 1000]])
+def test_same_bits_every_time(kv, dtype, lens):
+    c = Case(lens, 16, 2, 128, kv, dtype, seed=14)
     first = c.run().out.clone(), c.lse.clone()
     for _ in range(5):
         c.run()

@@ -90,13 +90,13 @@ def test_calls_side_by_side(kv, dtype):
 
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
-@pytest.mark.parametrize("listed", [False, True])
-def test_replay_with_other_lengths_tables_and_lists(kv, dtype, listed):
+@pytest.mark.parametrize("listed,W", [(False, 40), (False, 100), (True, 40)])
+def test_replay_with_other_lengths_tables_and_lists(kv, dtype, listed, W):
     """Two graphs that share a workspace, replayed in turn after their inputs change in place."""
     def blocks_of(seed):
         g = torch.Generator().manual_seed(seed)
         return torch.randint(-2, 20, (3, 2, 6), generator=g).to(torch.int32) if listed else None
-    sets = [[Case(lens, 8, 2, 64, kv, dtype, seed=i, W=40, blocks=blocks_of(i)) for i, lens in enumerate(l)]
+    sets = [[Case(lens, 8, 2, 64, kv, dtype, seed=i, W=W, blocks=blocks_of(i)) for i, lens in enumerate(l)]
             for l in ([[1, 2500, 64], [900, 0, 1]], [[300, 300, 2000], [0, 0, 65]])]
     ws = torch.empty(lib.dsa_paged_attention_workspace(8, 2, 64), device="cuda")
     graphs = []
@@ -154,10 +154,10 @@ def variant(tmp_path_factory):
 
 
 @pytest.mark.parametrize("kv,dtype", KINDS)
-@pytest.mark.parametrize("lens", [[40], [1000], [300, 0, 20000, 64]])
-def test_wait_that_runs_out(variant, kv, dtype, lens):
+@pytest.mark.parametrize("lens,W", [([40], None), ([1000], None), ([1000], 300), ([300, 0, 700, 64], None), ([300, 0, 20000, 64], None)])
+def test_wait_that_runs_out(variant, kv, dtype, lens, W):
     """NaN for every row that has tokens, zeros for the others, a status, and a context that goes on."""
-    c = Case(lens, 12, 2, 128, kv, dtype, seed=31)
+    c = Case(lens, 12, 2, 128, kv, dtype, seed=31, W=W)
     k, v, ks, vs = c.pools.cuda()
     q, table, seqlens = c.q.cuda(), c.table.cuda(), c.seqlens.cuda()
     out = torch.full(c.q.shape, 3.0, dtype=c.dtype, device="cuda")
