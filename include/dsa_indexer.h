@@ -586,7 +586,7 @@ int dsa_block_select(const void* q, long long q_row_stride, long long q_head_str
  * Data errors: seqlens[r] > W * 64 gives a NaN row and DSA_ERR_BAD_SEQLEN; a
  * visible token without a page in the pool NaN for the heads that see it and
  * DSA_ERR_BAD_PAGE; a wait that runs out DSA_ERR_TIMEOUT and NaN rows.
- * rows * Hkv * ceil(Hq / Hkv / 32) * (blocks ? k : W) must be below 2^31.
+ * rows * Hkv * ceil(Hq / Hkv / 32) * ((blocks ? k : W) + 8) must be below 2^31.
  */
 int dsa_paged_attention(const void* q, long long q_row_stride, long long q_head_stride, int rows,
                         int Hq, int Hkv, int D, int dtype, float scale, const void* k_cache,

@@ -211,7 +211,7 @@ int dsa_paged_attention(const void* q, long long q_row_stride, long long q_head_
   if (blocks && (k <= 0 || blocks_row_stride < 0 || blocks_head_stride < 0)) return DSA_ERR_INVALID_ARG;
   if (rows > 0 && (!q || !block_table || !seqlens || !out || !workspace)) return DSA_ERR_INVALID_ARG;
   const int group = Hq / Hkv, per_cta = dsa::paged_heads_max(group), tiles = (group + per_cta - 1) / per_cta;
-  if ((double)rows * Hkv * tiles * (blocks ? k : W) >= (double)k2G) return DSA_ERR_UNSUPPORTED;
+  if ((double)rows * Hkv * tiles * ((blocks ? k : W) + 8.0) >= (double)k2G) return DSA_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || q_row_stride % 8 || q_head_stride % 8 || !aligned(out, 16) || out_row_stride % 8 ||
       out_head_stride % 8 || !aligned(workspace, 16) || !aligned(seqlens, 4) || !aligned(blocks, 4) ||
       !aligned(lse, 4))

@@ -247,6 +247,18 @@ def test_nan_of_a_visible_token(kv, dtype):
     c.check(rows=[1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("values", [False, True])
+def test_nan_scales_of_a_visible_token(dtype, values):
+    c = Case([130, 70], 4, 2, 128, "fp8", dtype, seed=17)
+    page, slot = c.tokens(0, 0)
+    (c.pools.v_scale if values else c.pools.k_scale)[page[100], 1, slot[100]] = math.nan
+    c.run()
+    torch.cuda.synchronize()
+    assert c.out[0, 2:].isnan().all() and c.out[0, :2].isfinite().all()
+    c.check(rows=[1])
+
+
 @pytest.mark.parametrize("kv,dtype", KINDS)
 @pytest.mark.parametrize("W", [None, WIDE])
 def test_data_errors(kv, dtype, W):

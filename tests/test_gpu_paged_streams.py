@@ -1,6 +1,9 @@
 """The calls on the paged cache on streams other than torch's current one, side by side, captured and
 replayed, and with a wait that runs out."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -14,6 +17,7 @@ pytestmark = pytest.mark.gpu
 
 KINDS = [("bf16", "bf16"), ("fp16", "fp16"), ("fp8", "bf16")]
 BUSY = 20_000_000                                       # cycles, some 10 ms
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def args_of(c):
@@ -141,6 +145,39 @@ def test_replay_with_other_lengths_tables_and_lists(kv, dtype, listed, W):
             c = cases[turn]
             c.out, c.lse, c.status = s["out"], s["lse"], s["status"]
             c.check()
+
+
+def test_first_calls_of_a_process_are_captured(tmp_path):
+    """No call needs one before its capture."""
+    code = tmp_path / "first.py"
+    code.write_text("""
+import torch
+import sparse_attention_paged_gb300 as lib
+int32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+q = torch.ones((2, 8, 64), device="cuda").to(torch.bfloat16)
+k = torch.ones((4, 2, 64, 64), device="cuda").to(torch.bfloat16).transpose(1, 2)
+v = torch.ones((4, 2, 64, 64), device="cuda").to(torch.bfloat16).transpose(1, 2)
+wide = torch.zeros((2, 300), dtype=torch.int32, device="cuda")
+table, lengths, new, free = int32([[0, 1], [2, 3]]), int32([70, 100]), int32([1, 1]), int32([])
+bounds, unit = torch.zeros((4, 2, 2, 64), dtype=torch.int8, device="cuda"), torch.zeros((4, 2), device="cuda")
+ws = torch.empty(lib.dsa_paged_attention_workspace(8, 2, 64), device="cuda")
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    slots, _, lens, _, _ = lib.request_slots(lengths, new, free, table, 2)
+    lib.kv_store(q[:, :2] * 3, q[:, 2:4] * 3, slots, k, v)
+    lib.block_bounds(k, table, lengths, lens, 1, bounds, unit)
+    blocks = lib.block_select(q, bounds, unit, table, lens, 1, first=0, last=1)
+    out = lib.paged_attention(q, k, v, table, lens, 0.1, blocks=blocks, workspace=ws)
+    all_ = lib.paged_attention(q, k, v, wide, lens, 0.1, workspace=ws)
+graph.replay()
+torch.cuda.synchronize()
+assert slots.tolist() == [64 + 6, 192 + 36] and blocks.tolist() == [[[1], [1]], [[1], [1]]], (slots, blocks)
+assert (bounds[1, :, 0] == 96).all() and (out >= 1).all() and (all_ == 1).all()
+""")
+    r = subprocess.run([sys.executable, str(code)], cwd=ROOT, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": ROOT})
+    assert r.returncode == 0, r.stderr
 
 
 @pytest.fixture(scope="module")
