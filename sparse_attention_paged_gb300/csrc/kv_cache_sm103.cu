@@ -14,7 +14,10 @@
 // so that every key of the page lies in the box.  NaN keys are passed over, and
 // infinities count as the largest finite number.  All of it is exact.
 //
-// Both are bound by HBM at a prefill and by latency at a decode step.
+// Measured, bf16, 22,528 tokens, 8 heads of 128: the store 24 us (185 MB, the copy
+// rate), the boxes of its 352 pages 13.8 out of HBM (46 MB; a block's lengths, table, keys
+// and sums follow one another) and some 10 behind the store; a decode step of 64
+// requests 8.3 us for both, which is latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
