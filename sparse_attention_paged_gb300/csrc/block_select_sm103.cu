@@ -18,9 +18,9 @@
 // of codes, four products an instruction.  Every block finds the best k of its
 // run, and the first one the best k of those.  The k-th largest by bins of equal
 // width, the keys of its bin ranked by all pairs.  Bound by latency, and by HBM at
-// long rows, whose records of 2 D bytes lie anywhere (4.4 TB/s).  Measured: 64 rows
-// of 64 to 2,048 pages, 8 heads of 128, 22.6 us (27.6 out of HBM: 78.6 MB); one row
-// of 64 pages 6.2, of 2,048 10.9.
+// long rows, whose later pages are few blocks' work.  Measured: 64 rows
+// of 64 to 2,048 pages, 8 heads of 128, 22.7 us (27.0 out of HBM: 78.6 MB); one row
+// of 64 pages 5.3, of 2,048 11.2.
 //
 // Rows that share a table (a prompt): a block per 16 rows and key head reads the
 // boxes once, multiplies them on the tensor cores, and a warp selects for a row.
@@ -45,7 +45,9 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBlocksPerSm = 2;
 constexpr int kOrdered = 128;        // rows that are started by their lengths, at most
+constexpr int kWarpPages = 256;      // a row of so many is one warp's to choose from: of 64 pages 5.3 us, 6.4 by the block
 constexpr int kRun = 256;            // pages that a block has before another one joins it
+constexpr int kRunFull = 1024;
 constexpr int kGridBits = 20;
 constexpr uint32_t kAlways = 0xffffffffu;  // key of a page that is taken whatever its score
 
@@ -103,6 +105,120 @@ __device__ __forceinline__ int row_pages(const BlockSelectParams& p, int row, bo
   return len <= 0 || *past ? 0 : (len - 1) / kPage + 1;
 }
 
+// ---- the choice by one warp ------------------------------------------------------
+
+constexpr int kWarpBins = 256;
+
+// One warp: the best k of n > k keys in shared memory, equal ones from the front,
+// in order.  Bins of equal width between the smallest and the largest score; the
+// keys of the bin with the k-th largest are ranked by all pairs (those that are
+// not taken fall to 0), or, where they are too many (equal scores), it is found
+// bit by bit.
+__device__ __forceinline__ void warp_select(uint32_t* keys, int n, int k, int lane, uint32_t* bins, int* out) {
+  uint32_t low = kAlways, high = 0;
+#pragma unroll 4
+  for (int i = lane; i < n; i += 32) {
+    const uint32_t key = keys[i];
+    low = min(low, key);
+    if (key != kAlways) high = max(high, key);
+  }
+  low = __reduce_min_sync(kAll, low), high = __reduce_max_sync(kAll, high);
+  constexpr int kEach = kWarpBins / 32;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) bins[j * 32 + lane] = 0;
+  __syncwarp();
+  const int shift = high > low ? max(0, 32 - 8 - __clz(high - low)) : 0;
+  static_assert(kWarpBins == 1 << 8, "the bits of a bin");
+  auto bin_of = [&](uint32_t key) { return (key - low) >> shift; };
+  int above = 0;
+#pragma unroll 4
+  for (int i = lane; i < n; i += 32) {
+    const uint32_t key = keys[i];
+    if (key == kAlways) ++above;
+    else atomicAdd(&bins[bin_of(key)], 1u);
+  }
+  above = __reduce_add_sync(kAll, above);
+  __syncwarp();
+  // lane: bins from the top
+  int c[kEach], mine = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) mine += c[j] = (int)bins[kWarpBins - 1 - (lane * kEach + j)];
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, before, o);
+    if (lane >= o) before += v;
+  }
+  above += before - mine;
+  int bin = -1, rest = 0, inside = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    if (above < k && k <= above + c[j]) bin = kWarpBins - 1 - (lane * kEach + j), rest = k - above, inside = c[j];
+    above += c[j];
+  }
+  const uint32_t owner = __ballot_sync(kAll, bin >= 0);
+  uint32_t least = kAlways;                // no bin: pages that are always taken are all
+  int equal = n;
+  if (owner) {
+    const int from = __ffs(owner) - 1;
+    bin = __shfl_sync(kAll, bin, from), rest = __shfl_sync(kAll, rest, from), inside = __shfl_sync(kAll, inside, from);
+    least = low + ((uint32_t)bin << shift);
+    if (inside > rest && inside <= 32) {
+      // its keys and places beside each other, then each against all
+      int count = 0;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const uint32_t key = i0 + lane < n ? keys[i0 + lane] : kAlways;
+        const bool in = key != kAlways && bin_of(key) == (uint32_t)bin;
+        const uint32_t who = __ballot_sync(kAll, in);
+        if (in) {
+          const int at = count + __popc(who & ((1u << lane) - 1));
+          bins[at] = key, bins[32 + at] = i0 + lane;
+        }
+        count += __popc(who);
+      }
+      __syncwarp();
+      const uint32_t key = bins[lane];
+      int better = 0;
+      for (int j = 0; j < inside; ++j) {
+        const uint32_t other = __shfl_sync(kAll, key, j);
+        better += other > key || (other == key && j < lane);  // places are in order
+      }
+      if (lane < inside && better >= rest) keys[bins[32 + lane]] = 0u;
+      __syncwarp();
+    } else if (inside > rest) {
+      auto count = [&](uint32_t from) {
+        int sum = 0;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) sum += keys[i] >= from;
+        return __reduce_add_sync(kAll, sum);
+      };
+      for (int bit = shift - 1; bit >= 0; --bit)
+        if (count(least + (1u << bit)) >= k) least += 1u << bit;
+      equal = k - count(least + 1);
+    }
+  }
+  int larger = 0, same = 0;
+  const uint32_t left = (1u << lane) - 1;
+  if (equal == n) {                        // all from `least` on
+#pragma unroll 4
+    for (int i = lane; i - lane < n; i += 32) {
+      const bool take = i < n && keys[i] >= least;
+      const uint32_t who = __ballot_sync(kAll, take);
+      if (take) out[larger + __popc(who & left)] = i;
+      larger += __popc(who);
+    }
+    return;
+  }
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const bool in = i0 + lane < n;
+    const uint32_t key = in ? keys[i0 + lane] : 0u;
+    const uint32_t more = __ballot_sync(kAll, in && key > least), alike = __ballot_sync(kAll, in && key == least);
+    const int l = larger + __popc(more & left), e = same + __popc(alike & left);
+    if (in && (key > least || (key == least && e < equal))) out[l + min(e, equal)] = i0 + lane;
+    larger += __popc(more), same += __popc(alike);
+  }
+}
+
 // ---- rows with tables of their own ---------------------------------------------
 
 constexpr int kBinBits = 10, kBins = 1 << kBinBits;
@@ -147,10 +263,7 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t mine, Shared& s) {
 }
 
 // Takes the k largest of n >= k keys in shared memory, equal ones from the front:
-// emit(place among them, index), in the order of the indices.  Bins of equal
-// width between the smallest and the largest score; the keys of the bin with the
-// k-th largest are ranked by all pairs (those that are not taken fall to 0), or,
-// where they are too many (equal scores), it is found bit by bit.
+// emit(place among them, index), in the order of the indices.  As the warp does it.
 template <typename F>
 __device__ void block_select(uint32_t* keys, int n, int k, Shared& s, F emit) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -429,6 +542,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     for (int i = threadIdx.x; i < p.k; i += kThreads) out[i] = -1;
   } else if (all) {
     for (int i = threadIdx.x; i < p.k; i += kThreads) out[i] = i < n ? i : -1;
+  } else if (run >= n && n <= kWarpPages) {
+    if (warp == 0) warp_select(keys, n, p.k, lane, s.sort.bins, out);
   } else if (run >= n) {
     block_select(keys, n, p.k, s, [&](int at, int i) { out[at] = i; });
   }
@@ -461,116 +576,6 @@ __device__ __forceinline__ void halves(uint32_t x, uint32_t& low, uint32_t& high
   const __half2 l = __hsub2(*reinterpret_cast<const __half2*>(&u[0]), off);
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u[1]), off);
   low = *reinterpret_cast<const uint32_t*>(&l), high = *reinterpret_cast<const uint32_t*>(&h);
-}
-
-constexpr int kWarpBins = 256;           // as block_select()'s, a warp's own
-
-// One warp: the best k of n > k keys in shared memory, equal ones from the front,
-// in order.  As block_select() does it: the keys of the k-th largest's bin that are
-// not taken fall to 0.
-__device__ __forceinline__ void warp_select(uint32_t* keys, int n, int k, int lane, uint32_t* bins, int* out) {
-  uint32_t low = kAlways, high = 0;
-#pragma unroll 4
-  for (int i = lane; i < n; i += 32) {
-    const uint32_t key = keys[i];
-    low = min(low, key);
-    if (key != kAlways) high = max(high, key);
-  }
-  low = __reduce_min_sync(kAll, low), high = __reduce_max_sync(kAll, high);
-  constexpr int kEach = kWarpBins / 32;
-#pragma unroll
-  for (int j = 0; j < kEach; ++j) bins[j * 32 + lane] = 0;
-  __syncwarp();
-  const int shift = high > low ? max(0, 32 - 8 - __clz(high - low)) : 0;
-  static_assert(kWarpBins == 1 << 8, "the bits of a bin");
-  auto bin_of = [&](uint32_t key) { return (key - low) >> shift; };
-  int above = 0;
-#pragma unroll 4
-  for (int i = lane; i < n; i += 32) {
-    const uint32_t key = keys[i];
-    if (key == kAlways) ++above;
-    else atomicAdd(&bins[bin_of(key)], 1u);
-  }
-  above = __reduce_add_sync(kAll, above);
-  __syncwarp();
-  // lane: bins from the top
-  int c[kEach], mine = 0;
-#pragma unroll
-  for (int j = 0; j < kEach; ++j) mine += c[j] = (int)bins[kWarpBins - 1 - (lane * kEach + j)];
-  int before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kAll, before, o);
-    if (lane >= o) before += v;
-  }
-  above += before - mine;
-  int bin = -1, rest = 0, inside = 0;
-#pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    if (above < k && k <= above + c[j]) bin = kWarpBins - 1 - (lane * kEach + j), rest = k - above, inside = c[j];
-    above += c[j];
-  }
-  const uint32_t owner = __ballot_sync(kAll, bin >= 0);
-  uint32_t least = kAlways;                // no bin: pages that are always taken are all
-  int equal = n;
-  if (owner) {
-    const int from = __ffs(owner) - 1;
-    bin = __shfl_sync(kAll, bin, from), rest = __shfl_sync(kAll, rest, from), inside = __shfl_sync(kAll, inside, from);
-    least = low + ((uint32_t)bin << shift);
-    if (inside > rest && inside <= 32) {
-      // its keys and places beside each other, then each against all
-      int count = 0;
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const uint32_t key = i0 + lane < n ? keys[i0 + lane] : kAlways;
-        const bool in = key != kAlways && bin_of(key) == (uint32_t)bin;
-        const uint32_t who = __ballot_sync(kAll, in);
-        if (in) {
-          const int at = count + __popc(who & ((1u << lane) - 1));
-          bins[at] = key, bins[32 + at] = i0 + lane;
-        }
-        count += __popc(who);
-      }
-      __syncwarp();
-      const uint32_t key = bins[lane];
-      int better = 0;
-      for (int j = 0; j < inside; ++j) {
-        const uint32_t other = __shfl_sync(kAll, key, j);
-        better += other > key || (other == key && j < lane);  // places are in order
-      }
-      if (lane < inside && better >= rest) keys[bins[32 + lane]] = 0u;
-      __syncwarp();
-    } else if (inside > rest) {
-      auto count = [&](uint32_t from) {
-        int sum = 0;
-#pragma unroll 4
-        for (int i = lane; i < n; i += 32) sum += keys[i] >= from;
-        return __reduce_add_sync(kAll, sum);
-      };
-      for (int bit = shift - 1; bit >= 0; --bit)
-        if (count(least + (1u << bit)) >= k) least += 1u << bit;
-      equal = k - count(least + 1);
-    }
-  }
-  int larger = 0, same = 0;
-  const uint32_t left = (1u << lane) - 1;
-  if (equal == n) {                        // all from `least` on
-#pragma unroll 4
-    for (int i = lane; i - lane < n; i += 32) {
-      const bool take = i < n && keys[i] >= least;
-      const uint32_t who = __ballot_sync(kAll, take);
-      if (take) out[larger + __popc(who & left)] = i;
-      larger += __popc(who);
-    }
-    return;
-  }
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const bool in = i0 + lane < n;
-    const uint32_t key = in ? keys[i0 + lane] : 0u;
-    const uint32_t more = __ballot_sync(kAll, in && key > least), alike = __ballot_sync(kAll, in && key == least);
-    const int l = larger + __popc(more & left), e = same + __popc(alike & left);
-    if (in && (key > least || (key == least && e < equal))) out[l + min(e, equal)] = i0 + lane;
-    larger += __popc(more), same += __popc(alike);
-  }
 }
 
 template <int D>
@@ -752,12 +757,17 @@ cudaError_t launch_t(const BlockSelectParams& p, int sms, cudaStream_t stream) {
   if (p.bt_stride == 0 && items > slots && p.W <= kTileMaxPages)
     return launch(block_select_tile_kernel<D>, ((long long)p.rows + kRows - 1) / kRows * p.heads, kTileThreads,
                   tile_smem(p.W), 1, stream, p);
-  // More blocks than one for a row while all of them are on the GPU together: the
+  // More blocks than one for a row while all of them are on the GPU together (the
   // blocks of a cluster start and end together, and with more of them than fit
-  // the cluster's idle ones keep others out.  A list of many entries leaves no
-  // room for all blocks' best ones beside each other.
+  // the cluster's idle ones keep others out): past 512 pages, from 256 a block on, and
+  // where they fill half of the GPU from 1,024 on.  8 heads, one row of 512 pages 10.8
+  // us and 10.2 by one block, of 2,048 11.2 and 19.3, of 8,192 16.7 and 51.4; 16 rows of
+  // 1,024 pages 16.3 and 14.0, of 4,096 29.7 and 34.6.  A list of many entries leaves no room
+  // for all blocks' best ones beside each other.
   int blocks = 1;
-  while (blocks < 8 && 2 * blocks * items <= slots && blocks * kRun < p.W && p.k <= kSelectMaxList) blocks *= 2;
+  while (blocks < 8 && 2 * blocks * items <= slots && p.k <= kSelectMaxList && p.W > 2 * kRun &&
+         blocks * (4 * blocks * items > slots ? kRunFull : kRun) < p.W)
+    blocks *= 2;
   const int run = std::max((p.W + blocks - 1) / blocks, std::min(p.W, kRun)), most = std::min(run, p.k);
   const size_t smem = 4 * (size_t)(blocks > 1 ? run + 2 * most + 2 * blocks * most : run);
   return launch(block_select_kernel<D>, items * blocks, kThreads, smem, blocks, stream, p, blocks, run,
