@@ -22,9 +22,9 @@
 // of 64 to 2,048 pages, 8 heads of 128, 22.7 us (27.0 out of HBM: 78.6 MB); one row
 // of 64 pages 5.3, of 2,048 11.2.
 //
-// Rows that share a table (a prompt): a block per 16 rows and key head reads the
+// Rows that share a table (a prompt): a block per 16 or 32 rows and key head reads the
 // boxes once, multiplies them on the tensor cores, and a warp selects for a row.
-// Bound by its instructions: 1,024 rows of 352 pages, 8 heads 35 us.
+// Bound by its instructions: 1,024 rows of 352 pages, 8 heads of 128 33 us (38 out of HBM).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -552,12 +552,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // ---- rows that share a table ------------------------------------------------------
 
 constexpr int kTileThreads = 512, kTileWarps = kTileThreads / 32;
-constexpr int kRows = 16;                // of a block
+constexpr int kTileMorePages = 512;     // keys of 32 rows: two such blocks are on an SM
 constexpr int kTileMaxPages = 2048;      // keys of 16 rows in shared memory: 130 KB
 
 // Keys of a row in shared memory: eight rows' pairs of keys are in 32 banks.
 constexpr int tile_stride(int W) { return (W + 31) / 32 * 32 + 8; }
-constexpr int tile_smem(int W) { return (kRows * tile_stride(W) + W) * 4; }
+constexpr int tile_smem(int rows, int W) { return (rows * tile_stride(W) + W) * 4; }
 
 // D += A * B, 16 rows x 16 values (fp16), 8 columns, fp32.
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -578,7 +578,8 @@ __device__ __forceinline__ void halves(uint32_t x, uint32_t& low, uint32_t& high
   low = *reinterpret_cast<const uint32_t*>(&l), high = *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D>
+// kRows, 16 or 32, rows a block.
+template <int D, int kRows>
 __global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(const BlockSelectParams p) {
   extern __shared__ uint32_t keys[];     // [kRows][stride], then the table's page ids
   const int stride = tile_stride(p.W);
@@ -627,26 +628,33 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(cons
 #pragma unroll
       for (int j = 0; j < kEach; ++j) v[j] = value(j & 1 ? u[j / 2] >> 16 : u[j / 2] & 0xffffu, p.dtype);
     };
-    float top = 0.f, v[kEach];
-#pragma unroll 4
-    for (int h = 0; h < p.group; ++h) {
-      load(h, v);
+    // The first eight heads' values stay in registers for the second pass: 1,024 rows of
+    // 352 pages, 8 groups of 4 heads, 27.1 us for 28.4.
+    constexpr int kKept = 8;
+    float top = 0.f, v[kEach], kept[kKept][kEach];
+    auto largest = [&](const float (&x)[kEach]) {
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) top = fmaxf(top, fabsf(v[j]));
-    }
+      for (int j = 0; j < kEach; ++j) top = fmaxf(top, fabsf(x[j]));
+    };
+#pragma unroll
+    for (int h = 0; h < kKept; ++h)
+      if (h < p.group) load(h, kept[h]), largest(kept[h]);
+    for (int h = kKept; h < p.group; ++h) load(h, v), largest(v);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
     const Grid grid(top);
     int above[kEach] = {}, below[kEach] = {}, size = 0;
-#pragma unroll 4
-    for (int h = 0; h < p.group; ++h) {
-      load(h, v);
+    auto add = [&](const float (&x)[kEach]) {
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
-        const int i = grid(v[j]);
+        const int i = grid(x[j]);
         above[j] += max(i, 0), below[j] += max(-i, 0);
       }
-    }
+    };
+#pragma unroll
+    for (int h = 0; h < kKept; ++h)
+      if (h < p.group) add(kept[h]);
+    for (int h = kKept; h < p.group; ++h) load(h, v), add(v);
 #pragma unroll
     for (int j = 0; j < kEach; ++j) size = max(size, max(above[j], below[j]));
     const int shift = code_shift(__reduce_max_sync(kAll, size));
@@ -659,12 +667,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(cons
   }
   __syncthreads();
   if (scored) {
-    // Products of 16 rows and 16 pages, whole numbers below 2^24 in fp32: exact.  A
+    // Products of the rows and 16 pages, whole numbers below 2^24 in fp32: exact.  A
     // dot product may take its values in any order, so that lane t of four reads
     // units t, t + 4, ... of 16 codes of a page as they lie, and rows likewise.
-    constexpr int kUnits = 2 * D / 64;     // of a lane
+    constexpr int kUnits = 2 * D / 64, kTiles = kRows / 16;  // units of a lane, tiles of 16 rows
     const int g = lane >> 2, t = lane & 3;
-    const int n_low = pages[g], n_high = pages[g + 8];
     auto record = [&](int i) { return (long long)(i < n_max ? ids[i] : 0) * p.heads + head; };
     for (int first = warp * 16; first < n_max; first += kTileWarps * 16) {
       int4 box[2][kUnits];
@@ -677,29 +684,40 @@ __global__ void __launch_bounds__(kTileThreads, 2) block_select_tile_kernel(cons
 #pragma unroll
         for (int j = 0; j < 2; ++j) scale[w][j] = __ldg(p.bound_scale + record(first + 8 * w + 2 * t + j));
       }
-      float c[2][4] = {};
+      float c[kTiles][2][4] = {};
 #pragma unroll
       for (int u = 0; u < kUnits; ++u)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {      // halves of a unit: 8 codes
-          const uint4 a = *reinterpret_cast<const uint4*>(codes[g] + (t + 4 * u) * 16 + v * 8);
-          const uint4 b = *reinterpret_cast<const uint4*>(codes[g + 8] + (t + 4 * u) * 16 + v * 8);
+          uint32_t x[2][4];
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            uint32_t x, y;
-            halves(v ? box[w][u].z : box[w][u].x, x, y);
-            mma16816(c[w], a.x, b.x, a.y, b.y, x, y);
-            halves(v ? box[w][u].w : box[w][u].y, x, y);
-            mma16816(c[w], a.z, b.z, a.w, b.w, x, y);
+            halves(v ? box[w][u].z : box[w][u].x, x[w][0], x[w][1]);
+            halves(v ? box[w][u].w : box[w][u].y, x[w][2], x[w][3]);
+          }
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m) {
+            const uint4 a = *reinterpret_cast<const uint4*>(codes[16 * m + g] + (t + 4 * u) * 16 + v * 8);
+            const uint4 b = *reinterpret_cast<const uint4*>(codes[16 * m + g + 8] + (t + 4 * u) * 16 + v * 8);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              mma16816(c[m][w], a.x, b.x, a.y, b.y, x[w][0], x[w][1]);
+              mma16816(c[m][w], a.z, b.z, a.w, b.w, x[w][2], x[w][3]);
+            }
           }
         }
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int i = first + 8 * w + 2 * t + j;
-          if (i < n_low) keys[g * stride + i] = key_of(c[w][j], scale[w][j], i, n_low, p);
-          if (i < n_high) keys[(g + 8) * stride + i] = key_of(c[w][2 + j], scale[w][j], i, n_high, p);
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * m + g + 8 * h, n = pages[r];
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int i = first + 8 * w + 2 * t + j;
+              if (i < n) keys[r * stride + i] = key_of(c[m][w][2 * h + j], scale[w][j], i, n, p);
+            }
         }
     }
   }
@@ -745,8 +763,11 @@ cudaError_t launch_t(const BlockSelectParams& p, int sms, cudaStream_t stream) {
   if (dev >= kMaxDevices || !ready[dev]) {
     e = cudaFuncSetAttribute(block_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectMaxPages * 4);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(block_select_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             tile_smem(kTileMaxPages));
+    e = cudaFuncSetAttribute(block_select_tile_kernel<D, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             tile_smem(16, kTileMaxPages));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(block_select_tile_kernel<D, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             tile_smem(32, kTileMorePages));
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) ready[dev] = true;
   }
@@ -754,9 +775,18 @@ cudaError_t launch_t(const BlockSelectParams& p, int sms, cudaStream_t stream) {
   // Rows of a shared table by 16 once they fill the GPU: 352 pages, 8 heads, 32
   // rows 11.0 us and 17.4 by 16, 64 rows 21.2 and 17.5, 256 rows 62.9 and 17.7; 2,048
   // pages, 32 rows 25.4 and 52.6, 64 rows 47.6 and 52.8, 256 rows 147 and 53.
-  if (p.bt_stride == 0 && items > slots && p.W <= kTileMaxPages)
-    return launch(block_select_tile_kernel<D>, ((long long)p.rows + kRows - 1) / kRows * p.heads, kTileThreads,
-                  tile_smem(p.W), 1, stream, p);
+  // 32 rows a block read and unpack a box once for two products and take 1.73 times as
+  // long as 16: where the SM with most blocks has less to do that way, and not with one on
+  // an SM (608 rows 19.2 us and 15.7 by 16).  8 heads, rows that end at
+  // 352 pages: 700 rows 27.0 us and 24.4 by 16, 1,024 rows 27.1 and 30.0, 2,048 rows
+  // 51.5 and 51.9, 4,096 rows 87.8 and 97.3; at 128 pages 1,024 rows 18.0 and 19.7.
+  if (p.bt_stride == 0 && items > slots && p.W <= kTileMaxPages) {
+    const long long few = ((long long)p.rows + 15) / 16 * p.heads, more = ((long long)p.rows + 31) / 32 * p.heads;
+    const long long deep = (more + sms - 1) / sms;
+    if (p.W <= kTileMorePages && deep > 1 && 7 * deep < 4 * ((few + sms - 1) / sms))
+      return launch(block_select_tile_kernel<D, 32>, more, kTileThreads, tile_smem(32, p.W), 1, stream, p);
+    return launch(block_select_tile_kernel<D, 16>, few, kTileThreads, tile_smem(16, p.W), 1, stream, p);
+  }
   // More blocks than one for a row while all of them are on the GPU together (the
   // blocks of a cluster start and end together, and with more of them than fit
   // the cluster's idle ones keep others out): past 512 pages, from 256 a block on, and

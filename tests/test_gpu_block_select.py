@@ -167,3 +167,23 @@ def test_bad_page_of_another_block():
     c.table[0, 1400] = -1
     c.run(9).check(status=6, rows=[1])
     assert (c.out[0] == -1).all()
+
+
+@pytest.mark.parametrize("rows,kv_heads,most", [(70, 2, 1300), (40, 1, 700), (18, 1, 900), (16, 1, 2100), (3, 2, 1100)])
+@pytest.mark.parametrize("alike", [False, True])
+def test_rows_of_clusters(rows, kv_heads, most, alike):
+    """Two, four and eight blocks a row, some of them without a page."""
+    lens = [1 + (most * 64 - 1) * (rows - r) // rows * (r % 7 != 3) for r in range(rows)]
+    c = Case(lens, 4 * kv_heads, kv_heads, 64, "bf16", seed=rows, alike=alike)
+    c.run(20, 2, 3).check(rows=range(0, rows, max(1, rows // 7)))
+
+
+@pytest.mark.parametrize("dtype,dim,group,kv_heads,rows,most,k", [
+    ("bf16", 128, 4, 8, 1030, 22528, 16), ("fp16", 64, 12, 8, 1101, 9001, 5), ("bf16", 128, 1, 2, 4225, 32768, 100),
+    ("fp16", 128, 9, 16, 489, 640, 3)])
+@pytest.mark.parametrize("alike", [False, True])
+def test_many_rows_of_a_shared_table(dtype, dim, group, kv_heads, rows, most, k, alike):
+    """32 rows a block, the last block's partly there; rows of no length and of one token between long ones."""
+    lens = [0 if r % 11 == 3 else 1 if r % 17 == 5 else max(1, most - rows + 1 + r) for r in range(rows)]
+    c = Case(lens, group * kv_heads, kv_heads, dim, dtype, seed=k, shared=True, alike=alike)
+    c.run(k).check(rows=sorted({*range(0, rows, rows // 9), 3, 5, 31, 32, rows - 2, rows - 1}))
