@@ -14,8 +14,8 @@
 // so that every key of the page lies in the box.  NaN keys are passed over, and
 // infinities count as the largest finite number.  All of it is exact.
 //
-// Measured, bf16, 22,528 tokens, 8 heads of 128: the store 24 us (185 MB, the copy
-// rate), the boxes of its 352 pages 13.8 out of HBM (46 MB; a block's lengths, table, keys
+// Measured, bf16, 22,528 tokens, 8 heads of 128: the store 24 to 28 us (185 MB, the copy
+// rate), into fp8 21; the boxes of its 352 pages 13.8 out of HBM (46 MB; a block's lengths, table, keys
 // and sums follow one another) and some 10 behind the store; a decode step of 64
 // requests 8.3 us for both, which is latency.
 #include <cuda.h>
@@ -49,11 +49,42 @@ __device__ __forceinline__ float2 wide(uint32_t u) {
 // ---- store --------------------------------------------------------------------
 
 constexpr int kStoreThreads = 256;
+// Units of eight values of a key and a value that a thread has: two share a row's scale
+// and addresses (fp8, 8 heads: 131,072 tokens of 128 values 115 us, 138 with one; 65,536 of 64
+// values 30.6, 36.5 with one, 34.4 with four).  A copy has one: HBM bounds it.
+constexpr int store_units(bool fp8) { return fp8 ? 2 : 1; }
 
-// A thread has eight values of one token and head, of its key and its value.
-template <bool FP8, bool FP16, int D>
+// The largest finite magnitude of a row's 16-bit values, of its key in the low and of
+// its value in the high half: magnitudes' bits are in their order.
+template <bool FP16, int LANES, int UNITS>
+__device__ __forceinline__ uint32_t largest(const uint4 (&raw)[2][UNITS]) {
+  constexpr uint32_t kInf = FP16 ? 0x7c007c00u : 0x7f807f80u;
+  auto reduce = [&](auto magnitude) {
+    uint32_t top[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t x = 0;
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i)
+        x = __vmaxu2(x, __vmaxu2(__vmaxu2(magnitude(raw[s][i].x), magnitude(raw[s][i].y)),
+                                 __vmaxu2(magnitude(raw[s][i].z), magnitude(raw[s][i].w))));
+      top[s] = max(x & 0xffffu, x >> 16);
+    }
+    uint32_t both = top[0] | top[1] << 16;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(kAll, both, o));
+    return both;
+  };
+  uint32_t top = reduce([](uint32_t u) { return u & 0x7fff7fffu; });
+  if (__any_sync(kAll, __vcmpgeu2(top, kInf)))
+    top = reduce([](uint32_t u) { return u & 0x7fff7fffu & __vcmpltu2(u & 0x7fff7fffu, kInf); });
+  return top;
+}
+
+// A thread has UNITS times eight values of one token and head, of its key and its value.
+template <bool FP8, bool FP16, int D, int UNITS>
 __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const KvStoreParams p) {
-  constexpr int lanes = D / 8;                       // of a head
+  constexpr int lanes = D / 8 / UNITS;               // of a head
   const uint32_t row = blockIdx.x * (kStoreThreads / lanes) + threadIdx.x / lanes;
   const int c = threadIdx.x % lanes;
   const uint32_t token = row / (uint32_t)p.heads;
@@ -62,54 +93,50 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const KvStorePa
   sm100::griddep_launch_dependents();
   const bool there = token < (uint32_t)p.n;
   const int at = there ? __ldg(p.slots + token) : -1;
-  uint4 raw[2];
+  uint4 raw[2][UNITS];
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
-    raw[s] = there ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x[s]) +
-                                                          (long long)token * p.token[s] + head * p.head[s]) + c)
-                   : make_uint4(0u, 0u, 0u, 0u);
+  for (int s = 0; s < 2; ++s) {
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x[s]) +
+                                                       (long long)token * p.token[s] + head * p.head[s]) + c;
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) raw[s][i] = there ? __ldg(from + i * lanes) : make_uint4(0u, 0u, 0u, 0u);
+  }
   const int page = at / kPage, slot = at % kPage;
   const bool good = at >= 0 && page < p.num_pages;
   if (at >= 0 && !good) raise_status(p.status, DSA_ERR_BAD_PAGE);
+  const uint32_t top = FP8 ? largest<FP16, lanes, UNITS>(raw) : 0u;
+  if (!good) return;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const long long to = (long long)page * p.at[s].page + (long long)slot * p.at[s].slot + head * p.at[s].head + c * 8;
+    const long long to = (long long)page * p.at[s].page + (long long)slot * p.at[s].slot + head * p.at[s].head;
     if (!FP8) {
-      if (good) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.pool[s]) + to) = raw[s];
+      uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.pool[s]) + to) + c;
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i) out[i * lanes] = raw[s][i];
       continue;
     }
-    const uint32_t u[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
-    float x[8], big = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 v = wide<FP16>(u[j]);
-      x[2 * j] = v.x, x[2 * j + 1] = v.y;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = fabsf(x[j]);
-      big = v <= FLT_MAX ? fmaxf(big, v) : big;
-    }
-#pragma unroll
-    for (int o = lanes / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kAll, big, o));
     // big = 1.m * 2^(E - 127): at most 448 * 2^e = 1.75 * 2^(e + 8)
+    const float big = s ? wide<FP16>(top).y : wide<FP16>(top).x;
     const uint32_t bits = __float_as_uint(big);
     const int e = max((int)(bits >> 23) - 135 + ((bits & 0x7fffffu) > 0x600000u), -126);
     const float inverse = power(-e);
-    uint32_t codes[2];
+    uint2* out = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.pool[s]) + to) + c;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float* y = x + 4 * j;
-      const uint32_t a =
-          __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inverse, y[1] * inverse), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t b =
-          __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inverse, y[3] * inverse), __NV_SATFINITE, __NV_E4M3);
-      codes[j] = a | b << 16;
+    for (int i = 0; i < UNITS; ++i) {
+      const uint32_t u[4] = {raw[s][i].x, raw[s][i].y, raw[s][i].z, raw[s][i].w};
+      uint32_t codes[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 x = wide<FP16>(u[2 * j]), y = wide<FP16>(u[2 * j + 1]);
+        const uint32_t a =
+            __nv_cvt_float2_to_fp8x2(make_float2(x.x * inverse, x.y * inverse), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t b =
+            __nv_cvt_float2_to_fp8x2(make_float2(y.x * inverse, y.y * inverse), __NV_SATFINITE, __NV_E4M3);
+        codes[j] = a | b << 16;
+      }
+      out[i * lanes] = make_uint2(codes[0], codes[1]);
     }
-    if (good) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.pool[s]) + to) = make_uint2(codes[0], codes[1]);
-      if (c == 0) p.scale[s][((long long)page * p.heads + head) * kPage + slot] = power(e);
-    }
+    if (c == 0) p.scale[s][((long long)page * p.heads + head) * kPage + slot] = power(e);
   }
 }
 
@@ -260,11 +287,16 @@ cudaError_t launch_bounds_t(const BlockBoundsParams& p, cudaStream_t stream) {
                       : launch(block_bounds_kernel<KV, 64>, blocks, kBoxThreads, p, stream);
 }
 
+template <bool FP8, bool FP16, int D, int UNITS>
+cudaError_t launch_store_u(const KvStoreParams& p, cudaStream_t stream) {
+  const long long rows = (long long)p.n * p.heads, per = (long long)UNITS * kStoreThreads / (D / 8);
+  return launch(kv_store_kernel<FP8, FP16, D, UNITS>, (rows + per - 1) / per, kStoreThreads, p, stream);
+}
+
 template <bool FP8, bool FP16>
 cudaError_t launch_store_t(const KvStoreParams& p, cudaStream_t stream) {
-  const long long rows = (long long)p.n * p.heads, per = kStoreThreads / (p.dim / 8), blocks = (rows + per - 1) / per;
-  return p.dim == 128 ? launch(kv_store_kernel<FP8, FP16, 128>, blocks, kStoreThreads, p, stream)
-                      : launch(kv_store_kernel<FP8, FP16, 64>, blocks, kStoreThreads, p, stream);
+  constexpr int units = store_units(FP8);
+  return p.dim == 128 ? launch_store_u<FP8, FP16, 128, units>(p, stream) : launch_store_u<FP8, FP16, 64, units>(p, stream);
 }
 
 }  // namespace
