@@ -518,6 +518,8 @@ int dsa_kv_store(const void* k, long long k_token_stride, long long k_head_strid
  * 0), infinities count as the largest float.  max_tokens: how many positions a
  * request has from starts[r] on; it shapes the launch, and more are taken all
  * the same, but for 0, which launches nothing.
+ * Requests that share a page, with lengths that end at different places in it,
+ * race for its box: leave all but the longest out (seqlens[r] 0).
  * Data errors: seqlens[r] > W * 64 leaves the request out (DSA_ERR_BAD_SEQLEN),
  * a page outside the pool itself (DSA_ERR_BAD_PAGE).
  */
@@ -567,6 +569,7 @@ int dsa_block_select(const void* q, long long q_row_stride, long long q_head_str
  * page that is named twice counts twice.  A row without a visible token gives
  * zeros and lse = -inf.
  *   q, out    [rows, Hq, D] through their strides, 16-byte aligned, of dtype.
+ *             out may be q itself, with the same strides.
  *   lse       fp32 [rows, Hq] contiguous, nullable.
  *   block_table, bt_stride, seqlens  as for the indexer calls (bt_stride = 0:
  *             all rows share row 0).

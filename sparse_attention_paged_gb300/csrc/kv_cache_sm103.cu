@@ -14,10 +14,10 @@
 // so that every key of the page lies in the box.  NaN keys are passed over, and
 // infinities count as the largest finite number.  All of it is exact.
 //
-// Measured, bf16, 22,528 tokens, 8 heads of 128: the store 24 to 28 us (185 MB, the copy
-// rate), into fp8 21; the boxes of its 352 pages 13.8 out of HBM (46 MB; a block's lengths, table, keys
-// and sums follow one another) and some 10 behind the store; a decode step of 64
-// requests 8.3 us for both, which is latency.
+// Measured, 22,528 tokens, 8 heads of 128: the bf16 store 24 to 28 us (185 MB, the copy
+// rate), into fp8 21; the boxes of its 352 pages 8 us behind the store (46 MB, from L2), 65,536
+// tokens' 24 (HBM at 80 % of the copy rate), fp8 131,072 tokens' 50 (instructions: a code is
+// widened and scaled in fp32); a decode step of 64 requests 8.3 us for both, which is latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -26,6 +26,9 @@
 #include <float.h>
 #include <math_constants.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "paged_common.cuh"
 #include "sm100_ptx.cuh"
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const KvStorePa
 
 // ---- boxes --------------------------------------------------------------------
 
-constexpr int kBoxThreads = 128;
+constexpr int kBoxThreads = 128, kBoxBlocks = 8;  // threads of a block, blocks of an SM
 
 template <bool FP16>
 __device__ __forceinline__ uint32_t pick2(uint32_t a, uint32_t b, bool larger) {
@@ -157,34 +160,49 @@ __device__ __forceinline__ uint32_t pick2(uint32_t a, uint32_t b, bool larger) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// A block has one page of one head: a thread 16 bytes of every few tokens.  Ten
-// blocks an SM where the registers do (fp8 has 16 values a load, and takes more):
-// 352 pages, 8 heads 13.8 us, 14.4 with eight.
+// The lanes of a warp whose indexes agree below UNITS have the same N elements each: the
+// largest (smallest) of all, N / 2 of them after each step, and so on.
+template <int UNITS, int N, typename T, typename F>
+__device__ __forceinline__ void share_out(T (&x)[N], int lane, F pick) {
+  int n = N;
+#pragma unroll
+  for (int m = UNITS; m < 32; m <<= 1) {
+    n >>= 1;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j)
+      if (j < n) {
+        const T keep = lane & m ? x[j + n] : x[j], give = lane & m ? x[j] : x[j + n];
+        x[j] = pick(keep, __shfl_xor_sync(kAll, give, m));
+      }
+  }
+}
+
+// A page of one head is a block's at a time: a thread 16 bytes of every few tokens, the
+// warp shares out their extremes, and the warps meet in shared memory (all lanes'
+// extremes there, in banks that eight lanes have in common, took 62 us for 51 at 131,072 fp8
+// tokens, 8 heads of 128).  The grid covers max_tokens for every request, and where they are of
+// many lengths most of it is no page: a block looks 32 places up at a time (23 prompts of
+// 300 to 9,000 tokens 7 us, 28 with a block for each place).
 template <int KV, int D>
-__global__ void __launch_bounds__(kBoxThreads, KV == DSA_KV_FP8_E4M3 ? 8 : 10) block_bounds_kernel(const BlockBoundsParams p) {
+__global__ void __launch_bounds__(kBoxThreads, kBoxBlocks) block_bounds_kernel(const BlockBoundsParams p) {
   constexpr bool kFp8 = KV == DSA_KV_FP8_E4M3, kHalf = KV == DSA_KV_FP16;
   constexpr int kBytes = kFp8 ? 1 : 2, kUnits = D * kBytes / 16;
+  constexpr int kUnitBits = kUnits == 4 ? 2 : kUnits == 8 ? 3 : 4;
   constexpr int kGroups = kBoxThreads / kUnits, kLoads = kPage / kGroups;
-  __shared__ float high[kGroups][D], low[kGroups][D];
+  // a 16-byte unit's extremes (values, or pairs of 16 bits), and those that a lane ends with
+  constexpr int kHave = kFp8 ? 16 : 4, kLeft = kHave * kUnits / 32, kPair = kFp8 ? 1 : 2;
+  using Extreme = std::conditional_t<kFp8, float, uint32_t>;
+  __shared__ alignas(16) Extreme high[kBoxThreads / 32][D / kPair], low[kBoxThreads / 32][D / kPair];
   __shared__ float tops[kBoxThreads / 32];
-  const int head = blockIdx.x % p.heads;
-  const int turn = blockIdx.x / p.heads % p.pages, req = blockIdx.x / p.heads / p.pages;
+  __shared__ int4 found[32];
+  __shared__ int2 counts;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int unit = threadIdx.x % kUnits, group = threadIdx.x / kUnits;
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  const int len = __ldg(p.seqlens + req), start = p.starts ? max(__ldg(p.starts + req), 0) : 0;
-  if (len <= start) return;
-  if ((long long)len > (long long)p.W * kPage) {
-    if (threadIdx.x == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
-    return;
-  }
-  for (int block = start / kPage + turn; block <= (len - 1) / kPage; block += p.pages) {
-    const int page = __ldg(p.block_table + (long long)req * p.bt_stride + block);
-    if (page < 0 || page >= p.num_pages) {
-      if (threadIdx.x == 0) raise_status(p.status, DSA_ERR_BAD_PAGE);
-      continue;
-    }
-    const int tokens = min(kPage, len - block * kPage);
+  auto box = [&](int at) {
+    const int4 item = found[at];
+    const int page = item.x, head = item.y, tokens = item.z;
     const uint8_t* base = static_cast<const uint8_t*>(p.pool) +
                           ((long long)page * p.at.page + head * p.at.head) * kBytes + unit * 16;
     const long long record = (long long)page * p.heads + head;
@@ -198,9 +216,11 @@ __global__ void __launch_bounds__(kBoxThreads, KV == DSA_KV_FP8_E4M3 ? 8 : 10) b
         scale[i] = kFp8 ? __ldg(p.scale + record * kPage + token) : 1.f;
       }
     }
-    if (!kFp8) {
+    Extreme h[kHave], l[kHave];
+    if constexpr (!kFp8) {
       constexpr uint32_t kInf = kHalf ? 0x7c007c00u : 0x7f807f80u, kLess = kInf | 0x80008000u;
-      uint32_t h[4] = {kLess, kLess, kLess, kLess}, l[4] = {kInf, kInf, kInf, kInf};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = kLess, l[j] = kInf;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
         if (i * kGroups + group < tokens) {
@@ -208,13 +228,9 @@ __global__ void __launch_bounds__(kBoxThreads, KV == DSA_KV_FP8_E4M3 ? 8 : 10) b
 #pragma unroll
           for (int j = 0; j < 4; ++j) h[j] = pick2<kHalf>(h[j], u[j], true), l[j] = pick2<kHalf>(l[j], u[j], false);
         }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        *reinterpret_cast<float2*>(&high[group][unit * 8 + 2 * j]) = wide<kHalf>(h[j]);
-        *reinterpret_cast<float2*>(&low[group][unit * 8 + 2 * j]) = wide<kHalf>(l[j]);
-      }
+      share_out<kUnits>(h, lane, [](uint32_t x, uint32_t y) { return pick2<kHalf>(x, y, true); });
+      share_out<kUnits>(l, lane, [](uint32_t x, uint32_t y) { return pick2<kHalf>(x, y, false); });
     } else {
-      float h[16], l[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) h[j] = -CUDART_INF_F, l[j] = CUDART_INF_F;
 #pragma unroll
@@ -231,25 +247,38 @@ __global__ void __launch_bounds__(kBoxThreads, KV == DSA_KV_FP8_E4M3 ? 8 : 10) b
             h[2 * j + 1] = fmaxf(h[2 * j + 1], y), l[2 * j + 1] = fminf(l[2 * j + 1], y);
           }
         }
+      share_out<kUnits>(h, lane, [](float x, float y) { return fmaxf(x, y); });
+      share_out<kUnits>(l, lane, [](float x, float y) { return fminf(x, y); });
+    }
+    // places: parts of the units (by the lane's upper bits, the first one largest), units, kLeft
+    const int part = __brev((unsigned)lane / kUnits) >> (27 + kUnitBits);
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        *reinterpret_cast<float4*>(&high[group][unit * 16 + j]) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
-        *reinterpret_cast<float4*>(&low[group][unit * 16 + j]) = make_float4(l[j], l[j + 1], l[j + 2], l[j + 3]);
-      }
+    for (int j = 0; j < kLeft; ++j) {
+      high[warp][(part * kUnits + lane % kUnits) * kLeft + j] = h[j];
+      low[warp][(part * kUnits + lane % kUnits) * kLeft + j] = l[j];
     }
     __syncthreads();
-    float h = -CUDART_INF_F, l = CUDART_INF_F;
-    const int d = threadIdx.x;
-    if (d < D) {
+    // a thread has a channel: d, at place `at` of the extremes
+    float h1 = -CUDART_INF_F, l1 = CUDART_INF_F;
+    const int t = threadIdx.x, place = t / kPair, of = place / kLeft;
+    const int d = (of % kUnits * kHave + of / kUnits * kLeft + place % kLeft) * kPair + t % kPair;
+    if (t < D) {
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) h = fmaxf(h, high[g][d]), l = fminf(l, low[g][d]);
+      for (int w = 0; w < kBoxThreads / 32; ++w) {
+        if constexpr (kFp8) {
+          h1 = fmaxf(h1, high[w][place]), l1 = fminf(l1, low[w][place]);
+        } else {
+          const float2 a = wide<kHalf>(high[w][place]), b = wide<kHalf>(low[w][place]);
+          h1 = fmaxf(h1, t & 1 ? a.y : a.x), l1 = fminf(l1, t & 1 ? b.y : b.x);
+        }
+      }
     }
-    if (l > h) l = h = 0.f;                        // no number among the keys, or no channel
-    h = fminf(fmaxf(h, -FLT_MAX), FLT_MAX), l = fminf(fmaxf(l, -FLT_MAX), FLT_MAX);
-    float top = fmaxf(fabsf(h), fabsf(l));
+    if (l1 > h1) l1 = h1 = 0.f;                    // no number among the keys, or no channel
+    h1 = fminf(fmaxf(h1, -FLT_MAX), FLT_MAX), l1 = fminf(fmaxf(l1, -FLT_MAX), FLT_MAX);
+    float top = fmaxf(fabsf(h1), fabsf(l1));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    if (lane == 0) tops[warp] = top;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kBoxThreads / 32; ++w) top = fmaxf(top, tops[w]);
@@ -257,12 +286,53 @@ __global__ void __launch_bounds__(kBoxThreads, KV == DSA_KV_FP8_E4M3 ? 8 : 10) b
     const uint32_t bits = __float_as_uint(top);
     const int e = max((int)(bits >> 23) - 133 + ((bits & 0x7fffffu) > 0x7e0000u), -126);
     const float inverse = power(-e);
-    if (d < D) {
-      p.bounds[(record * 2 + 0) * D + d] = (int8_t)(int)ceilf(h * inverse);
-      p.bounds[(record * 2 + 1) * D + d] = (int8_t)(int)floorf(l * inverse);
-      if (d == 0) p.bound_scale[record] = power(e);
+    if (t < D) {
+      p.bounds[(record * 2 + 0) * D + d] = (int8_t)(int)ceilf(h1 * inverse);
+      p.bounds[(record * 2 + 1) * D + d] = (int8_t)(int)floorf(l1 * inverse);
+      if (t == 0) p.bound_scale[record] = power(e);
     }
-    __syncthreads();                               // the sums before the next page's
+  };
+  // 32 items at a time, a lane of the first warp each; those with a page into a list.
+  // The last ones first: a store just before has left their keys in L2 (16 requests of
+  // 4,096 tokens, both calls 103.8 us for 106.1).
+  const uint32_t items = (uint32_t)p.n_req * p.pages * p.heads;
+  for (uint32_t i0 = blockIdx.x; i0 < items; i0 += 32 * gridDim.x) {
+    // (turns past the first where requests have more than max_tokens)
+    for (int turn = 0;; ++turn) {
+      if (threadIdx.x < 32) {
+        const uint32_t from_end = i0 + lane * gridDim.x, item = items - 1 - from_end;
+        int head = 0, page = -1, tokens = 0;
+        bool more = false;
+        if (from_end < items) {
+          const uint32_t place = item / p.heads, req = place / p.pages;
+          head = (int)(item - place * p.heads);
+          const int start = p.starts ? max(__ldg(p.starts + req), 0) : 0, len = __ldg(p.seqlens + req);
+          if (len > start) {
+            const long long block = start / kPage + (long long)(place - req * p.pages) + (long long)turn * p.pages;
+            const int end = (len - 1) / kPage;
+            if ((long long)len > (long long)p.W * kPage) {
+              raise_status(p.status, DSA_ERR_BAD_SEQLEN);
+            } else if (block <= end) {
+              page = __ldg(p.block_table + (long long)req * p.bt_stride + block);
+              tokens = min(kPage, len - (int)block * kPage);
+              more = block + p.pages <= end;
+              if (page < 0 || page >= p.num_pages) {
+                raise_status(p.status, DSA_ERR_BAD_PAGE);
+                page = -1;
+              }
+            }
+          }
+        }
+        const uint32_t there = __ballot_sync(kAll, page >= 0), again = __ballot_sync(kAll, more);
+        if (page >= 0) found[__popc(there & ((1u << lane) - 1u))] = make_int4(page, head, tokens, 0);
+        if (lane == 0) counts = make_int2(__popc(there), again != 0);
+      }
+      __syncthreads();
+      const int2 n = counts;
+      for (int i = 0; i < n.x; ++i) box(i);
+      __syncthreads();                             // the list before the next one's
+      if (!n.y) break;
+    }
   }
 }
 
@@ -281,8 +351,8 @@ cudaError_t launch(K kernel, long long blocks, int threads, const P& p, cudaStre
 }
 
 template <int KV>
-cudaError_t launch_bounds_t(const BlockBoundsParams& p, cudaStream_t stream) {
-  const long long blocks = (long long)p.n_req * p.pages * p.heads;
+cudaError_t launch_bounds_t(const BlockBoundsParams& p, int sms, cudaStream_t stream) {
+  const long long blocks = std::min((long long)p.n_req * p.pages * p.heads, (long long)sms * kBoxBlocks);
   return p.dim == 128 ? launch(block_bounds_kernel<KV, 128>, blocks, kBoxThreads, p, stream)
                       : launch(block_bounds_kernel<KV, 64>, blocks, kBoxThreads, p, stream);
 }
@@ -306,10 +376,10 @@ cudaError_t launch_kv_store(const KvStoreParams& p, int kv_dtype, cudaStream_t s
   return p.dtype == DSA_FP16 ? launch_store_t<true, true>(p, stream) : launch_store_t<true, false>(p, stream);
 }
 
-cudaError_t launch_block_bounds(const BlockBoundsParams& p, int kv_dtype, cudaStream_t stream) {
-  if (kv_dtype == DSA_KV_BF16) return launch_bounds_t<DSA_KV_BF16>(p, stream);
-  if (kv_dtype == DSA_KV_FP16) return launch_bounds_t<DSA_KV_FP16>(p, stream);
-  return launch_bounds_t<DSA_KV_FP8_E4M3>(p, stream);
+cudaError_t launch_block_bounds(const BlockBoundsParams& p, int kv_dtype, int sms, cudaStream_t stream) {
+  if (kv_dtype == DSA_KV_BF16) return launch_bounds_t<DSA_KV_BF16>(p, sms, stream);
+  if (kv_dtype == DSA_KV_FP16) return launch_bounds_t<DSA_KV_FP16>(p, sms, stream);
+  return launch_bounds_t<DSA_KV_FP8_E4M3>(p, sms, stream);
 }
 
 }  // namespace dsa

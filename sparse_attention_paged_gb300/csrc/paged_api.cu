@@ -11,7 +11,7 @@
 namespace dsa {
 cudaError_t launch_request_slots(const RequestSlotsParams& p, cudaStream_t stream);
 cudaError_t launch_kv_store(const KvStoreParams& p, int kv_dtype, cudaStream_t stream);
-cudaError_t launch_block_bounds(const BlockBoundsParams& p, int kv_dtype, cudaStream_t stream);
+cudaError_t launch_block_bounds(const BlockBoundsParams& p, int kv_dtype, int sms, cudaStream_t stream);
 cudaError_t launch_block_select(const BlockSelectParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedAttnParams& p, int dim, int kv_dtype, const CUtensorMap& kmap,
                                    const CUtensorMap& vmap, int sms, cudaStream_t stream);
@@ -154,7 +154,9 @@ int dsa_block_bounds(const void* k_cache, long long kc_page_stride, long long kc
   if ((double)n_req * pages * Hkv >= (double)k2G) return DSA_ERR_UNSUPPORTED;
   const dsa::BlockBoundsParams p{k_cache, at, k_scale, Hkv, D, num_pages, block_table, bt_stride, W, starts, seqlens,
                                  n_req, pages, reinterpret_cast<int8_t*>(bounds), bound_scale, dev_status};
-  return launched(dsa::launch_block_bounds(p, kv_dtype, static_cast<cudaStream_t>(stream)));
+  const int sms = sm_count();
+  if (sms <= 0) return DSA_ERR_CUDA;
+  return launched(dsa::launch_block_bounds(p, kv_dtype, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int dsa_block_select(const void* q, long long q_row_stride, long long q_head_stride, int rows, int Hq, int Hkv,

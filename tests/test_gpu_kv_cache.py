@@ -229,3 +229,40 @@ def test_boxes_data_errors():
     lib.block_bounds(k, table, None, int32([128, 128, 129]), 128, bounds, unit, dev_status=status)
     assert int(status) == 7
     assert (bounds[:2] == 64).all() and (bounds[2] == 9).all()
+
+
+@pytest.mark.parametrize("kv,dim,hint", [("bf16", 64, 3000), ("fp8", 128, 3000), ("fp16", 128, 1), ("fp8", 64, 100)])
+def test_boxes_of_many_requests(kv, dim, hint):
+    """Few of many places hold a page, a block's list is refilled, and lengths are past the hint."""
+    g, H, R = torch.Generator().manual_seed(hint), 3, 310
+    lens = [[3000, 0, 70, 1, 64, 500][int(x)] for x in torch.randint(0, 6, (R,), generator=g)]
+    starts = [[0, 64, 65, 2999][int(x)] for x in torch.randint(0, 4, (R,), generator=g)]
+    pages = sum(ref.pages_of(n) for n in lens) + 1
+    pools = ref.Pools(pages, H, dim, kv, "head")
+    table = torch.full((R, 47), -1, dtype=torch.int32)
+    perm, at = torch.randperm(pages, generator=g).to(torch.int32), 0
+    for r, n in enumerate(lens):
+        m = ref.pages_of(n)
+        table[r, :m] = perm[at:at + m]
+        at += m
+        t = torch.arange(n)
+        if n:
+            x = torch.randn((n, H, dim), generator=g).to(ref.TYPES["fp16" if kv == "fp16" else "bf16"])
+            pools.put(table[r].long()[t // PAGE], t % PAGE, x, x)
+    bounds, unit = torch.full((pages, H, 2, dim), 77, dtype=torch.int8), torch.full((pages, H), -1.0)
+    got, got_unit, status = bounds.cuda(), unit.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, _, ks, _ = pools.cuda()
+    lib.block_bounds(k, table.cuda(), int32(starts), int32(lens), hint, got, got_unit, k_scale=ks, dev_status=status)
+    touched = torch.zeros(pages, dtype=torch.bool)
+    for r, n in enumerate(lens):
+        for b in range(starts[r] // PAGE, ref.pages_of(n)) if starts[r] < n else ():
+            page = int(table[r, b])
+            touched[page] = True
+            if (r + b) % 9 == 0 or b == ref.pages_of(n) - 1:
+                t = torch.arange(b * PAGE, min(n, (b + 1) * PAGE))
+                keys, _ = pools.get(torch.full_like(t, page), t % PAGE)
+                for h in range(H):
+                    box, scale = ref.box(keys[:, h])
+                    assert torch.equal(got[page, h].cpu(), box) and float(got_unit[page, h]) == float(scale), (r, b, h)
+    assert int(status) == 0
+    assert torch.equal((got_unit.cpu() > 0).all(1), touched) and (got.cpu()[~touched] == 77).all()

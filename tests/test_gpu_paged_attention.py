@@ -301,6 +301,14 @@ def test_same_bits_every_time(kv, dtype, lens):
         assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
 
 
+@pytest.mark.parametrize("kv,dtype", KINDS)
+@pytest.mark.parametrize("lens,heads,W", [([1000], 8, None), ([1000, 0, 70], 70, None), ([30000], 40, None), ([70, 9000, 0, 300] * 9, 24, WIDE)])
+def test_results_in_the_queries_place(kv, dtype, lens, heads, W):
+    c = Case(lens, heads, 2, 64, kv, dtype, seed=len(lens), W=W)
+    q = c.q.cuda()
+    c.run(q=q, out=q).check()
+
+
 def test_no_rows_and_allocated_outputs():
     c = Case([100], 4, 2, 64, "bf16", "bf16", seed=15)
     k, v, _, _ = c.pools.cuda()
