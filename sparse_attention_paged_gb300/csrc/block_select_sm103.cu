@@ -46,8 +46,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBlocksPerSm = 2;
 constexpr int kOrdered = 128;        // rows that are started by their lengths, at most
 constexpr int kWarpPages = 256;      // a row of so many is one warp's to choose from: of 64 pages 5.3 us, 6.4 by the block
-constexpr int kRun = 256;            // pages that a block has before another one joins it
-constexpr int kRunFull = 1024;
+constexpr int kRunFull = 1024;       // pages that a block has before another one joins it, where the GPU is half full
 constexpr int kGridBits = 20;
 constexpr uint32_t kAlways = 0xffffffffu;  // key of a page that is taken whatever its score
 
@@ -371,9 +370,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Pages of each block's run, at least kRun: a row of few pages is one block's.
-__device__ __forceinline__ int run_of(int n, int blocks) { return max((n + blocks - 1) / blocks, min(n, kRun)); }
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     block_select_kernel(const BlockSelectParams p, int blocks, int run_max, bool by_length) {
@@ -408,10 +404,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   if (past && rank == 0 && threadIdx.x == 0) raise_status(p.status, DSA_ERR_BAD_SEQLEN);
   if (threadIdx.x == 0) s.bad = 0, s.count = 0;
   __syncthreads();
-  const int run = run_of(n, blocks), begin = min(rank * run, n), mine = min(run, n - begin);
+  const int run = select_run(n, blocks), begin = min(rank * run, n), mine = min(run, n - begin);
   const bool all = n <= p.k;             // every page is taken: no scores
   if (rank > 0 && mine == 0) return;     // (the cluster's barrier goes by the threads that are there)
-  const int active = max(1, (n + run - 1) / run);
+  const int active = select_active(n, run);
   const int* table = p.block_table + (long long)row * p.bt_stride + begin;
   for (int i = threadIdx.x; i < mine; i += kThreads) {
     int page = __ldg(table + i);
@@ -795,10 +791,10 @@ cudaError_t launch_t(const BlockSelectParams& p, int sms, cudaStream_t stream) {
   // 1,024 pages 16.3 and 14.0, of 4,096 29.7 and 34.6.  A list of many entries leaves no room
   // for all blocks' best ones beside each other.
   int blocks = 1;
-  while (blocks < 8 && 2 * blocks * items <= slots && p.k <= kSelectMaxList && p.W > 2 * kRun &&
-         blocks * (4 * blocks * items > slots ? kRunFull : kRun) < p.W)
+  while (blocks < 8 && 2 * blocks * items <= slots && p.k <= kSelectMaxList && p.W > 2 * kSelectRun &&
+         blocks * (4 * blocks * items > slots ? kRunFull : kSelectRun) < p.W)
     blocks *= 2;
-  const int run = std::max((p.W + blocks - 1) / blocks, std::min(p.W, kRun)), most = std::min(run, p.k);
+  const int run = select_run(p.W, blocks), most = std::min(run, p.k);
   const size_t smem = 4 * (size_t)(blocks > 1 ? run + 2 * most + 2 * blocks * most : run);
   return launch(block_select_kernel<D>, items * blocks, kThreads, smem, blocks, stream, p, blocks, run,
                 items > slots && p.rows <= kOrdered);

@@ -67,6 +67,16 @@ struct BlockBoundsParams {
 // length also the best of several blocks.
 constexpr int kSelectMaxPages = 32768, kSelectMaxList = 1024;
 
+// A row's n pages among the blocks that share it: pages of a block's run, at least
+// kSelectRun where there are as many (a row of few pages is one block's), and blocks that
+// have one.  A row without pages is one block's too: neither is ever 0.
+constexpr int kSelectRun = 256;
+constexpr int select_run(int n, int blocks) {
+  const int even = (n + blocks - 1) / blocks, least = n < kSelectRun ? n : kSelectRun;
+  return even > least ? even : least > 1 ? least : 1;
+}
+constexpr int select_active(int n, int run) { return n > run ? (n + run - 1) / run : 1; }
+
 struct BlockSelectParams {
   const uint16_t* q;           // bf16 or fp16 bits, [rows, Hq, dim] through the strides
   long long q_row, q_head;
