@@ -478,11 +478,12 @@ long long dsa_latent_attention_workspace(void);
  *   used       [1], nullable: pages taken
  * No other entry of the table is written.  Arrays must not overlap.
  * Data errors: a request with a negative length or more than W * 64 tokens
- * (DSA_ERR_BAD_SEQLEN), or for whose pages the free list is too short
- * (DSA_ERR_BAD_PAGE), takes none; its tokens have slot -1 and position 0, its
- * seqlens is 0.  A page whose slots would pass 32 bits, or a negative one,
- * gives slot -1 and DSA_ERR_BAD_PAGE.  More than n tokens: those past n have no
- * row, and a fresh page that begins there is not entered, DSA_ERR_BAD_SEQLEN.
+ * (DSA_ERR_BAD_SEQLEN), or that still needs more pages than the requests before
+ * it have left of the free list (DSA_ERR_BAD_PAGE), takes none and leaves them to
+ * the next; its tokens have slot -1 and position 0, its seqlens is 0.  A page
+ * whose slots would pass 32 bits, or a negative one, gives slot -1 and
+ * DSA_ERR_BAD_PAGE.  More than n tokens: those past n have no row, and a fresh
+ * page that begins there is not entered, DSA_ERR_BAD_SEQLEN.
  * bt_stride may be 0 for one request only.
  */
 int dsa_request_slots(const int* lengths, const int* new_tokens, int n_req,

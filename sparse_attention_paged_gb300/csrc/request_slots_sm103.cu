@@ -1,9 +1,11 @@
 // request_slots_sm103.cu -- block tables and slot maps from the requests'
 // lengths: request b holds c_b tokens and gets n_b new ones, for which it
 // takes the next ceil((c_b + n_b) / 64) - ceil(c_b / 64) pages of the free list,
-// requests in order.
+// requests in order.  One that wants more pages than are left takes none, and
+// those behind it go on from the same place of the list.
 //
-//   pages   o_b = sum of the pages taken before b
+//   pages   o_b = sum of the pages taken before b; while the list is long enough for
+//           all, those wanted, else one thread walks the requests (1,024 at a time)
 //   tokens  cu_b = sum of n before b; token i, cu_b <= i < cu_{b+1}, has position
 //           c_b + i - cu_b and the slot page * 64 + position % 64
 //
@@ -33,7 +35,8 @@ struct Shared {
   long long tokens[kThreads / 32], pages[kThreads / 32];
   long long cu[kChunk + 1];      // tokens before each request
   long long take[kChunk];        // pages before it; -1: it gets none
-  int cached[kChunk];
+  int cached[kChunk], want[kChunk];
+  long long given;               // pages that requests up to the chunk's end got
 };
 
 __global__ void __launch_bounds__(kThreads) request_slots_kernel(const RequestSlotsParams p) {
@@ -44,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) request_slots_kernel(const RequestSl
   const long long t0 = (long long)blockIdx.x * kThreads, t1 = min(t0 + kThreads, (long long)p.n);
   const long long token = t0 + threadIdx.x;
   const bool first = blockIdx.x == 0;
-  long long tokens = 0, pages = 0, taken = 0;  // before the chunk; pages that requests got
+  long long tokens = 0, pages = 0, taken = 0;  // before the chunk; up to the last request that got pages
   bool found = false;
   for (int r0 = 0; r0 < p.n_req; r0 += kChunk) {
     int c[kPer], n[kPer], want[kPer];
@@ -70,6 +73,7 @@ __global__ void __launch_bounds__(kThreads) request_slots_kernel(const RequestSl
       if (lane >= o) a += x, b += y;
     }
     if (lane == 31) s.tokens[warp] = a, s.pages[warp] = b;
+    const long long given = pages;
     a += tokens - my_tokens, b += pages - my_pages;
     __syncthreads();
 #pragma unroll
@@ -77,10 +81,29 @@ __global__ void __launch_bounds__(kThreads) request_slots_kernel(const RequestSl
       if (w < warp) a += s.tokens[w], b += s.pages[w];
       tokens += s.tokens[w], pages += s.pages[w];
     }
+    const bool enough = pages <= p.n_free;      // for all up to the chunk's end
+    if (!enough) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) s.want[threadIdx.x * kPer + j] = want[j];
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        long long at = given;
+        for (int i = 0; i < min(kChunk, p.n_req - r0); ++i) {
+          const int n = s.want[i];
+          const bool fits = n == 0 || (n > 0 && at + n <= p.n_free);
+          s.take[i] = fits ? at : -1;
+          if (fits) at += n;
+        }
+        s.given = at;
+      }
+      __syncthreads();
+      pages = s.given;
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = threadIdx.x * kPer + j, r = r0 + i;
-      const bool got = want[j] >= 0 && (want[j] == 0 || b + want[j] <= p.n_free);
+      if (!enough) b = r < p.n_req ? s.take[i] : 0;
+      const bool got = want[j] >= 0 && b >= 0;
       s.cu[i] = a, s.take[i] = got ? b : -1, s.cached[i] = c[j];
       if (first && r < p.n_req) {
         if (p.seqlens) p.seqlens[r] = got ? c[j] + n[j] : 0;

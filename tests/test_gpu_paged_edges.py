@@ -1,0 +1,64 @@
+"""Edges of the calls on the paged cache of keys and values."""
+import pytest
+import torch
+
+import sparse_attention_paged_gb300 as lib
+from tests import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+PAGE = ref.PAGE
+
+
+def int32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ---- a free list that ends ---------------------------------------------------------------
+
+def slots_by_contract(lengths, new, free, table, n):
+    """Requests in order; one that wants more pages than are left takes none and leaves them to the next."""
+    table, slots, positions, seqlens, cu, at, status = [list(r) for r in table], [], [], [], [0], 0, 0
+    for b, (c, m) in enumerate(zip(lengths, new)):
+        have, want = ref.pages_of(c), ref.pages_of(c + m)
+        good = want == have or want - have <= len(free) - at
+        if not good:
+            status = 6
+        else:
+            table[b][have:want] = free[at:at + want - have]
+            at += want - have
+        for p in range(c, c + m):
+            slots.append(table[b][p // PAGE] * PAGE + p % PAGE if good else -1)
+            positions.append(p if good else 0)
+        seqlens.append(c + m if good else 0)
+        cu.append(cu[-1] + m)
+    rest = n - len(slots)
+    return table, slots + [-1] * rest, positions + [0] * rest, seqlens, cu, at, status
+
+
+def check_slots(lengths, new, free):
+    W, n, at, table = max(1, *(ref.pages_of(c + m) for c, m in zip(lengths, new))), sum(new) + 3, 5000, []
+    for c in lengths:
+        held = ref.pages_of(c)
+        table.append(list(range(at, at + held)) + [-1] * (W - held))
+        at += held
+    there, status = int32(table), int32([0])
+    slots, positions, seqlens, cu, used = lib.request_slots(int32(lengths), int32(new), int32(free), there, n, dev_status=status)
+    got = there.tolist(), slots.tolist(), positions.tolist(), seqlens.tolist(), cu.tolist(), int(used), int(status)
+    assert got == slots_by_contract(lengths, new, free, table, n)
+
+
+@pytest.mark.parametrize("lengths,new,pages", [
+    ([0, 0], [12 * 64, 1], 10), ([0, 60, 64], [700, 10, 1], 10), ([0, 5, 0, 0, 64], [65, 3, 64, 65, 1], 2),
+    ([64, 0, 0, 0, 0], [1, 129, 128, 129, 64], 4), ([0, 0, 0], [64, 65, 64], 0), ([0, 0, 0], [128, 64, 64], 1)])
+def test_slots_behind_a_refused_request(lengths, new, pages):
+    check_slots(lengths, new, [70 + 3 * i for i in range(pages)])
+
+
+@pytest.mark.parametrize("requests,pages,high", [(64, 40, 200), (1024, 900, 150), (1030, 700, 300), (2500, 2400, 200), (3000, 1, 90)])
+def test_slots_behind_many_refused_requests(requests, pages, high):
+    """Free lists that end in the first, a later or no chunk of requests, those that fit between those that do not."""
+    g = torch.Generator().manual_seed(requests)
+    lengths = torch.randint(0, 130, (requests,), generator=g).tolist()
+    new = torch.randint(0, high, (requests,), generator=g).tolist()
+    check_slots(lengths, new, torch.randperm(4000, generator=g)[:pages].tolist())
