@@ -287,8 +287,10 @@ __global__ void __launch_bounds__(kBoxThreads, kBoxBlocks) block_bounds_kernel(c
     const int e = max((int)(bits >> 23) - 133 + ((bits & 0x7fffffu) > 0x7e0000u), -126);
     const float inverse = power(-e);
     if (t < D) {
-      p.bounds[(record * 2 + 0) * D + d] = (int8_t)(int)ceilf(h1 * inverse);
-      p.bounds[(record * 2 + 1) * D + d] = (int8_t)(int)floorf(l1 * inverse);
+      // a quotient below 2^-149 is 0 here, and its key is not: 1 and -1 are the least codes around it
+      const int up = (int)ceilf(h1 * inverse), down = (int)floorf(l1 * inverse);
+      p.bounds[(record * 2 + 0) * D + d] = (int8_t)(h1 > 0.f ? max(up, 1) : up);
+      p.bounds[(record * 2 + 1) * D + d] = (int8_t)(l1 < 0.f ? min(down, -1) : down);
       if (t == 0) p.bound_scale[record] = power(e);
     }
   };

@@ -1,4 +1,6 @@
 """Edges of the calls on the paged cache of keys and values."""
+import math
+
 import pytest
 import torch
 
@@ -62,3 +64,34 @@ def test_slots_behind_many_refused_requests(requests, pages, high):
     lengths = torch.randint(0, 130, (requests,), generator=g).tolist()
     new = torch.randint(0, high, (requests,), generator=g).tolist()
     check_slots(lengths, new, torch.randperm(4000, generator=g)[:pages].tolist())
+
+
+# ---- keys far apart ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_boxes_of_channels_far_apart(kv, dim):
+    """A channel so much smaller than the page's largest that its quotient underflows still lies in the box."""
+    x = torch.randn((4, PAGE, 1, dim), generator=torch.Generator().manual_seed(dim))
+    x[:, :, 0, 1], x[:, :, 0, 2] = x[:, :, 0, 1].abs() + 1, -x[:, :, 0, 2].abs() - 1
+    small = 2.0 ** -60 if kv == "bf16" else 2.0 ** -20
+    x = (x * small).to(ref.TYPES["bf16" if kv == "fp8" else kv])
+    large = float(torch.finfo(x.dtype).max)
+    for page in range(1, 4):                                   # of one token, as it is stored
+        x[page, 7] = 0
+        x[page, 7, 0, 5] = (0, large, -large, math.inf if kv != "fp8" else large / 3)[page]
+    pools = ref.Pools(4, 1, dim, kv)
+    page, slot = torch.arange(4 * PAGE) // PAGE, torch.arange(4 * PAGE) % PAGE
+    pools.put(page, slot, x.flatten(0, 1), x.flatten(0, 1))
+    if kv == "fp8":
+        pools.k_scale[1:, 0, torch.arange(PAGE) != 7] *= 2.0 ** -60
+    k, _, ks, _ = pools.cuda()
+    bounds = torch.zeros((4, 1, 2, dim), dtype=torch.int8, device="cuda")
+    unit = torch.zeros((4, 1), device="cuda")
+    lib.block_bounds(k, torch.arange(4, dtype=torch.int32, device="cuda")[None], None, int32([4 * PAGE]), 4 * PAGE, bounds, unit,
+                     k_scale=ks)
+    for p in range(4):
+        keys, _ = pools.get(torch.full((PAGE,), p), torch.arange(PAGE))
+        want, scale = ref.box(keys[:, 0])
+        assert float(unit[p, 0]) == scale
+        assert torch.equal(bounds[p, 0].cpu(), want), p
