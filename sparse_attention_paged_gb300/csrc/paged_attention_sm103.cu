@@ -477,7 +477,7 @@ struct Consumer {
   float o[kSteps][NT][4];
   // heads 2 t and 2 t + 1 of each column tile: reference of the scores, that of
   // the weights * value scales (fp8), this lane's part of the total, and the
-  // factor from a product to log2 units
+  // factor from a product to log2 units (fp8: the queries' power of two)
   float top[NT][2], ref[NT][2], sum[NT][2], qf[NT][2];
   Waiter wait;
   uint32_t meet_phase, turn, smem;
@@ -553,7 +553,7 @@ struct Consumer {
       // big < 2^x; queries times 2^(14 - x)
       const int x = max((int)(__float_as_uint(big) >> 23) - 126, -100);
       const float up = __uint_as_float((uint32_t)(127 + 14 - x) << 23);
-      const float down = __uint_as_float((uint32_t)(127 - 14 + x) << 23) * p.scale_log2;
+      const float down = __uint_as_float((uint32_t)(127 - 14 + x) << 23);
 #pragma unroll
       for (int c = 0; c < 2; ++c) qf[n][c] = __shfl_sync(kAll, down, (2 * t + c) * 4);  // heads 2t + c
 #pragma unroll
@@ -685,7 +685,12 @@ struct Consumer {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) s[n][2 * h + c] = s[n][2 * h + c] * qf[n][c] * ks;
+          for (int c = 0; c < 2; ++c) {
+            // what makes a product smaller before the key scale, what makes it larger behind it: queries
+            // and keys of any sizes pass no infinity on the way to a score that is none
+            const float small = fminf(qf[n][c], 1.f), large = fmaxf(qf[n][c], 1.f) * p.scale_log2;
+            s[n][2 * h + c] = s[n][2 * h + c] * small * ks * large;
+          }
       }
     } else {
 #pragma unroll

@@ -6,6 +6,7 @@ import torch
 
 import sparse_attention_paged_gb300 as lib
 from tests import paged_ref as ref
+from tests.test_gpu_paged_attention import WIDE, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,25 @@ def test_boxes_of_channels_far_apart(kv, dim):
         want, scale = ref.box(keys[:, 0])
         assert float(unit[p, 0]) == scale
         assert torch.equal(bounds[p, 0].cpu(), want), p
+
+
+# ---- queries and scales at the ends of their range ------------------------------------------
+
+@pytest.mark.parametrize("power", [-110, -60, 60, 100, 120])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_fp8_queries_against_their_keys(power, dim, W):
+    """Queries of 2^power with keys of 2^-power: scores of ordinary size."""
+    c = Case([300, 64], 20, 2, dim, "fp8", "bf16", seed=power + 200, spread=0.5, W=W)
+    c.q = (c.q.double() * 2.0 ** power).to(c.dtype)
+    c.pools.k_scale *= 2.0 ** -power
+    c.run().check()
+
+
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_fp8_smallest_queries(W):
+    """bf16's subnormal numbers keep their bits beside the largest keys."""
+    c = Case([200], 8, 2, 64, "fp8", "bf16", seed=1, spread=0.0, W=W)
+    c.q = (c.q.double() * 2.0 ** -128).to(c.dtype)
+    c.pools.k_scale *= 2.0 ** 124
+    c.run().check()
