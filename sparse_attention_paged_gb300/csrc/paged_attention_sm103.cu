@@ -875,11 +875,15 @@ struct Consumer {
                                                    float big, float high, float total) {
     // no visible token: zeros, -inf
     const float f = total == 0.f ? 0.f : (kFp8 ? kSmallest : 1.f) / total;
-    const float unit = kFp8 ? ex2_small(high - big) : 1.f;  // of the size of the value scales
+    // of the size of the value scales, and 2^8 above them where the references of the scores and
+    // of the weights have been raised apart: past 2^100 a second factor
+    const float apart = high - big;
+    const float unit = kFp8 ? ex2_small(fminf(apart, 100.f)) : 1.f, more = kFp8 ? ex2(fmaxf(apart - 100.f, 0.f)) : 1.f;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = total == 0.f ? 0.f : x[2 * i] * f * unit, b = total == 0.f ? 0.f : x[2 * i + 1] * f * unit;
+      const float a = total == 0.f ? 0.f : x[2 * i] * f * unit * more;
+      const float b = total == 0.f ? 0.f : x[2 * i + 1] * f * unit * more;
       w[i] = p.dtype == DSA_FP16 ? pack2<true>(a, b) : pack2<false>(a, b);
     }
     *reinterpret_cast<uint4*>(p.out + (long long)row * p.out_row + (long long)head * p.out_head + c0) =

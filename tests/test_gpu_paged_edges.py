@@ -118,3 +118,27 @@ def test_fp8_smallest_queries(W):
     c.q = (c.q.double() * 2.0 ** -128).to(c.dtype)
     c.pools.k_scale *= 2.0 ** 124
     c.run().check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,pages,every", [(1, 24, 3), (608, 2, 2)])
+def test_fp8_largest_value_scales(dtype, rows, pages, every):
+    """Small codes under scales near 2^127, on tokens whose scores are a little above those before them,
+    wherever a row's pages are shared out."""
+    n = pages * PAGE
+    c = Case([n] * rows, 8, 1, 64, "fp8", dtype, seed=2, spread=0.0)
+    c.scale = 1.0
+    c.q[:] = 0
+    c.q[..., 0] = 8.0
+    late = torch.arange(n) // PAGE % every == every - 1
+    key = torch.zeros((n, 1, 64))
+    key[late, 0, 0] = 0.6                                       # 7 in log2 units: no reason for a new reference
+    g = torch.Generator().manual_seed(3)
+    top = 126 if dtype == "bf16" else 14                        # results that the type has
+    for r in range(rows):
+        page, slot = c.tokens(r, 0)
+        value = (torch.rand((n, 1, 64), generator=g) + 0.25).to(torch.float8_e4m3fn)
+        c.pools.put(page, slot, key, key)
+        c.pools.v.view(torch.uint8)[page, slot] = value.view(torch.uint8)
+        c.pools.v_scale[page, 0, slot] = torch.where(late, 2.0 ** top, 1.0)
+    c.run().check(rows=range(0, rows, 101))
