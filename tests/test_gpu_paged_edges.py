@@ -6,6 +6,7 @@ import torch
 
 import sparse_attention_paged_gb300 as lib
 from tests import paged_ref as ref
+from tests.test_gpu_block_select import Case as Selection
 from tests.test_gpu_paged_attention import WIDE, Case
 
 pytestmark = pytest.mark.gpu
@@ -142,3 +143,16 @@ def test_fp8_largest_value_scales(dtype, rows, pages, every):
         c.pools.v.view(torch.uint8)[page, slot] = value.view(torch.uint8)
         c.pools.v_scale[page, 0, slot] = torch.where(late, 2.0 ** top, 1.0)
     c.run().check(rows=range(0, rows, 101))
+
+
+# ---- the widest shared table -----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,dim,heads,kv_heads", [("bf16", 64, 4, 2), ("fp16", 128, 8, 1)])
+@pytest.mark.parametrize("k", [5, 700])
+def test_widest_table_that_rows_share(dtype, dim, heads, kv_heads, k):
+    """Exactly the 2,048 pages that a block of 16 rows has room for, the last row's keys before the page ids."""
+    rows = 330
+    lens = list(range(131072 - rows + 1, 131072 + 1))
+    c = Selection(lens, heads, kv_heads, dim, dtype, seed=k, shared=True)
+    assert c.W == 2048
+    c.run(k).check(rows=[0, 1, 14, 15, 16, 200, rows - 2, rows - 1])
