@@ -5,7 +5,7 @@
 // those behind it go on from the same place of the list.
 //
 //   pages   o_b = sum of the pages taken before b; while the list is long enough for
-//           all, those wanted, else one thread walks the requests (1,024 at a time)
+//           all, those wanted; else a warp walks the requests, 32 at a time
 //   tokens  cu_b = sum of n before b; token i, cu_b <= i < cu_{b+1}, has position
 //           c_b + i - cu_b and the slot page * 64 + position % 64
 //
@@ -15,7 +15,8 @@
 // request, from L2) and then looks its tokens' requests up in shared memory.
 // Bound by latency: the lengths, then the table or the free list, then stores.
 // Measured: 3.2 us a call for a decode step of 64 requests, 3.4 for 23 prompts of
-// 23,400 tokens.
+// 23,400 tokens.  Lists that end: 1,024 requests that each want a page, 500 left,
+// 10.3 us (3.5 with enough; 52 with one thread that walks them).
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <stdint.h>
@@ -86,15 +87,35 @@ __global__ void __launch_bounds__(kThreads) request_slots_kernel(const RequestSl
 #pragma unroll
       for (int j = 0; j < kPer; ++j) s.want[threadIdx.x * kPer + j] = want[j];
       __syncthreads();
-      if (threadIdx.x == 0) {
-        long long at = given;
-        for (int i = 0; i < min(kChunk, p.n_req - r0); ++i) {
-          const int n = s.want[i];
-          const bool fits = n == 0 || (n > 0 && at + n <= p.n_free);
-          s.take[i] = fits ? at : -1;
-          if (fits) at += n;
+      if (warp == 0) {
+        int at = (int)given;                    // (at most n_free)
+        for (int i0 = 0; i0 < min(kChunk, p.n_req - r0); i0 += 32) {
+          const int w = s.want[i0 + lane];
+          bool open = w > 0;                    // not decided yet
+          int mine = w == 0 ? at : -1;
+          while (true) {
+            // whoever wants more than is left has lost; among the others, whoever does with
+            // those before it
+            const int left = p.n_free - at;
+            open = open && w <= left;
+            const int v = open ? w : 0;
+            int before = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int x = __shfl_up_sync(0xffffffffu, before, o);
+              if (lane >= o) before += x;
+            }
+            before -= v;
+            const uint32_t over = __ballot_sync(0xffffffffu, open && before + v > left);
+            const int end = over ? __ffs(over) - 1 : 32;
+            if (open && lane < end) mine = at + before;
+            open = open && lane > end;
+            at += __shfl_sync(0xffffffffu, end < 32 ? before : before + v, min(end, 31));
+            if (!over) break;
+          }
+          s.take[i0 + lane] = mine;
         }
-        s.given = at;
+        if (lane == 0) s.given = at;
       }
       __syncthreads();
       pages = s.given;
