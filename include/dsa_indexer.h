@@ -546,10 +546,20 @@ int dsa_block_bounds(const void* k_cache, long long kc_page_stride, long long kc
  * largest product with a key of the page, up to one factor per row and head and
  * the queries' rounding.  It is exact, past the largest float that; NaN queries
  * count as 0, infinities as the largest float.
+ * A bound favours coarse boxes: codes are rounded outwards, by half a step on
+ * average, and a page whose largest key lies just past a power of two times 127
+ * has steps of twice the size.  Pages of one scale are chosen as unrounded boxes
+ * would have them (of the 32 best of 512, normal keys, 97 %); where few pages have
+ * the coarser scale, 79 %, and 52 % where a few channels are 4 times as large and
+ * hold most of a box's range.
+ * A causal row (a token of a prompt) needs last >= 1: the box of its newest page
+ * may hold keys behind it, and only that page's.
  * q: [rows, Hq, D] through its strides, 16-byte aligned; Hq / Hkv <= 1024 and W
  * <= 32768 (DSA_ERR_UNSUPPORTED).
  * Data errors: seqlens[r] > W * 64 (DSA_ERR_BAD_SEQLEN) or a page outside the
- * pool among the row's (DSA_ERR_BAD_PAGE) gives a list of -1.
+ * pool among the row's (DSA_ERR_BAD_PAGE) gives a list of -1, in which
+ * dsa_paged_attention sees no visible token: its zeros are told from a row's
+ * without tokens by the status only.
  */
 int dsa_block_select(const void* q, long long q_row_stride, long long q_head_stride, int rows,
                      int Hq, int Hkv, int D, int dtype, const signed char* bounds,
@@ -567,8 +577,8 @@ int dsa_block_select(const void* q, long long q_row_stride, long long q_head_str
  * blocks_head_stride + j], j < k, names (places in the row's block table; the
  * lists that dsa_block_select writes, or one for all heads with head stride 0).
  * Entries that are negative or past the row's pages are passed over, and a
- * page that is named twice counts twice.  A row without a visible token gives
- * zeros and lse = -inf.
+ * page that is named twice counts twice.  A row without a visible token, or
+ * whose scores are all -inf, gives zeros and lse = -inf.
  *   q, out    [rows, Hq, D] through their strides, 16-byte aligned, of dtype.
  *             out may be q itself, with the same strides.
  *   lse       fp32 [rows, Hq] contiguous, nullable.
@@ -580,8 +590,8 @@ int dsa_block_select(const void* q, long long q_row_stride, long long q_head_str
  *             without an access out of range.
  * Softmax and sums are fp32.  The weights of the value product are rounded to
  * the cache's type.  With an fp8 cache the codes are taken as fp16 (exact); a
- * head's queries as fp16 under a power of two, exact down to 2^-28 of the
- * head's largest and to 2^-39 of it below; weights times the tokens' value
+ * head's queries as fp16 under a power of two, exact down to 2^-27 of the
+ * head's largest and to 2^-38 of it below; weights times the tokens' value
  * scales as fp16, rounded by 2^-11 of themselves and by 2^-31 of the row's
  * largest where they are below 2^-20 of it.  The same call gives the same bits.
  * One kernel launch for few rows of narrow tables or short lists, else two;

@@ -156,3 +156,31 @@ def test_widest_table_that_rows_share(dtype, dim, heads, kv_heads, k):
     c = Selection(lens, heads, kv_heads, dim, dtype, seed=k, shared=True)
     assert c.W == 2048
     c.run(k).check(rows=[0, 1, 14, 15, 16, 200, rows - 2, rows - 1])
+
+
+# ---- what the header says of lists and scores without a finite number ---------------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "fp16"])
+@pytest.mark.parametrize("W", [None, WIDE])
+def test_scores_all_minus_infinity(kv, W):
+    c = Case([130, 300], 8, 2, 64, kv, kv, seed=20, W=W)
+    page, slot = c.tokens(0, 0)
+    c.pools.k[page, slot, 1, 3] = -math.inf
+    c.q[..., 3] = 1.0
+    c.run().check(rows=[1])
+    assert (c.out[0, 4:] == 0).all() and c.lse[0, 4:].isneginf().all()
+    assert c.out[0, :4].isfinite().all() and c.lse[0, :4].isfinite().all()
+
+
+def test_list_of_a_bad_table():
+    """A table with a page outside the pool: -1 from the selection, zeros from the attention, and the status."""
+    c = Case([700, 500], 4, 2, 64, "bf16", "bf16", seed=21)
+    c.table[0, 2] = 10 ** 6
+    pages = c.pools.k.shape[0]
+    bounds = torch.ones((pages, 2, 2, 64), dtype=torch.int8, device="cuda")
+    status = int32([0])
+    c.blocks = lib.block_select(c.q.cuda(), bounds, torch.ones((pages, 2), device="cuda"), c.table.cuda(), c.seqlens.cuda(), 4,
+                                dev_status=status).cpu()
+    assert int(status) == 6 and (c.blocks[0] == -1).all() and (c.blocks[1] >= 0).all()
+    c.run().check()
+    assert (c.out[0] == 0).all() and c.lse[0].isneginf().all()
