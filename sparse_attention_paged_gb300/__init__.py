@@ -465,8 +465,8 @@ def request_slots(lengths, new_tokens, free_pages, block_table, n, *, slots=None
     """Pages for new tokens into the block table, and the tokens' slots, from the requests' lengths.
 
     Request b holds ``lengths[b]`` tokens and gets ``new_tokens[b]``, for which it takes pages of
-    ``free_pages`` in order (int32, ``used`` says how many); ``block_table`` [requests, W] is updated
-    in place.  ``n``: rows of the outputs, at least the new tokens in all; the rest has slot -1.
+    ``free_pages`` in order (int32, ``used`` says how many), or none where fewer are left (slots -1,
+    length 0, a status); ``block_table`` [requests, W] is updated in place.  ``n``: rows of the outputs, at least the new tokens in all; the rest has slot -1.
     Outputs are allocated unless given.  Returns (slots [n], positions [n], seqlens [requests],
     cu_rows [requests + 1], used [1]), int32.  Raises DsaError on a host-side error.
     """
@@ -522,7 +522,8 @@ def block_select(q, bounds, bound_scale, block_table, seqlens, k, *, first=1, la
     queries [rows, Hq, D], the ``first`` and the ``last`` ones always among them.
 
     Returns int32 [rows, Hkv, k]: places in the row's block table, ascending, then -1, as
-    ``paged_attention`` takes them.  ``block_table`` has a row per query row, or one for all.
+    ``paged_attention`` takes them.  A prompt's tokens need ``last`` >= 1: the box of their newest
+    page may hold keys behind them.  ``block_table`` has a row per query row, or one for all.
     Raises DsaError on a host-side error.
     """
     if out is None:

@@ -10,7 +10,8 @@
 //   p = ceil(P / 2^s), n = ceil(N / 2^s), s the smallest with max(P, N) <= 127 * 2^s
 //   score = (sum_d p_d high_d - n_d low_d) * scale        int8 products, below 2^24
 // The score is exact, and with it the order and the choice: the result does
-// not depend on how the work is split.  Scores past the largest float count as
+// not depend on how the work is split.  As a bound it favours boxes of a coarse scale,
+// whose codes are rounded outwards by larger steps.  Scores past the largest float count as
 // that.  NaN queries count as 0, infinities as the largest float.
 //
 // Rows with tables of their own: a cluster of up to eight blocks per row and
@@ -19,12 +20,13 @@
 // run, and the first one the best k of those.  The k-th largest by bins of equal
 // width, the keys of its bin ranked by all pairs.  Bound by latency, and by HBM at
 // long rows, whose later pages are few blocks' work.  Measured: 64 rows
-// of 64 to 2,048 pages, 8 heads of 128, 22.7 us (27.0 out of HBM: 78.6 MB); one row
-// of 64 pages 5.3, of 2,048 11.2.
+// of 64 to 2,048 pages, 8 heads of 128, 22 us with the boxes (78.6 MB) in L2 and 27 with
+// boxes that come from HBM; one row of 64 pages 5.4, of 2,048 10.3.
 //
 // Rows that share a table (a prompt): a block per 16 or 32 rows and key head reads the
 // boxes once, multiplies them on the tensor cores, and a warp selects for a row.
-// Bound by its instructions: 1,024 rows of 352 pages, 8 heads of 128 33 us (38 out of HBM).
+// Bound by its instructions: 1,024 rows of 352 pages, 8 heads of 128 31 us with the boxes
+// (9.2 MB) in L2, some 3 more with an L2 that holds nothing of them.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
