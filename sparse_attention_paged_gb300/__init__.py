@@ -466,9 +466,10 @@ def request_slots(lengths, new_tokens, free_pages, block_table, n, *, slots=None
 
     Request b holds ``lengths[b]`` tokens and gets ``new_tokens[b]``, for which it takes pages of
     ``free_pages`` in order (int32, ``used`` says how many), or none where fewer are left (slots -1,
-    length 0, a status); ``block_table`` [requests, W] is updated in place.  ``n``: rows of the outputs, at least the new tokens in all; the rest has slot -1.
-    Outputs are allocated unless given.  Returns (slots [n], positions [n], seqlens [requests],
-    cu_rows [requests + 1], used [1]), int32.  Raises DsaError on a host-side error.
+    length 0, a status); ``block_table`` [requests, W] is updated in place.  ``n``: rows of the
+    outputs, at least the new tokens in all; the rest has slot -1.  Outputs are allocated unless
+    given.  Returns (slots [n], positions [n], seqlens [requests], cu_rows [requests + 1], used [1]),
+    int32.  Raises DsaError on a host-side error.
     """
     if slots is None or positions is None or seqlens is None or cu_rows is None or used is None:
         requests = lengths.shape[0]
