@@ -35,7 +35,9 @@
 // token's key scale; the weights take its value scale before they are rounded
 // to fp16, under a reference of their own that follows the largest weight *
 // scale: that lies between 2^6 and 2^15, and a token's weight is rounded by
-// 2^-11 of itself down to 2^-20 of it, and by 2^-31 of it below.
+// 2^-11 of itself down to 2^-20 of it, and by 2^-31 of it below.  That reference is
+// held as its distance from the scores': a score past 2^24 has no room for a scale's
+// exponent beside it.
 // 16-bit caches: the weights are rounded to the cache's type (2^-8 of
 // themselves for bf16, 2^-11 for fp16, 2^-25 of the largest where it is below
 // fp16's normal numbers), independently from token to token.
@@ -128,7 +130,7 @@ struct Misc {
   int begin, end, share, total;  // the slice, places per CTA, places in all
   int row, tile, place;          // where it begins, in its row's tile
   int rank;                      // in a cluster
-  // per consumer warp and head: maximum, reference of the sums, total.  Two of
+  // per consumer warp and head: reference of the scores, distance to that of the sums, total.  Two of
   // them in turn: a warp may reach the end of the next row while another still
   // reads those of this one.
   float stat[2][8][16][3];
@@ -156,6 +158,28 @@ __device__ __forceinline__ float ex2_small(float x) {
   float y;
   asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// References before any token: of the scores, and (fp8) the distance to that of the weights *
+// value scales.  fp8's are finite, so that differences of two of them are no NaN.
+template <bool FP8>
+__device__ __forceinline__ float no_top() {
+  return FP8 ? -3e38f : -CUDART_INF_F;
+}
+template <bool FP8>
+__device__ __forceinline__ float no_distance() {
+  return FP8 ? -1e30f : 0.f;
+}
+// A partial result's distance from a reference of the scores above its own, and the factor from
+// its sums to the largest distance of all.
+template <bool FP8>
+__device__ __forceinline__ float distance(float top, float ref, float above) {
+  return FP8 ? (top - above) + ref : 0.f;
+}
+template <bool FP8>
+__device__ __forceinline__ float factor(float top, float ref, float above, float high) {
+  if (FP8) return ex2((top - above) + ref - high);
+  return top == -CUDART_INF_F ? 0.f : ex2(top - above);
 }
 
 template <bool FP16>
@@ -476,8 +500,8 @@ struct Consumer {
   int warp, lane, g, t, slice, mt, heads;             // heads: of this warp's column tiles
   uint32_t qb[NT][kSteps][2];
   float o[kSteps][NT][4];
-  // heads 2 t and 2 t + 1 of each column tile: reference of the scores, that of
-  // the weights * value scales (fp8), this lane's part of the total, and the
+  // heads 2 t and 2 t + 1 of each column tile: reference of the scores, distance to that
+  // of the weights * value scales (fp8), this lane's part of the total, and the
   // factor from a product to log2 units (fp8: the queries' power of two)
   float top[NT][2], ref[NT][2], sum[NT][2], qf[NT][2];
   Waiter wait;
@@ -507,7 +531,7 @@ struct Consumer {
       for (int n = 0; n < NT; ++n) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      top[n][0] = top[n][1] = ref[n][0] = ref[n][1] = -CUDART_INF_F;
+      top[n][0] = top[n][1] = no_top<kFp8>(), ref[n][0] = ref[n][1] = no_distance<kFp8>();
       sum[n][0] = sum[n][1] = 0.f;
     }
   }
@@ -714,7 +738,7 @@ struct Consumer {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         over |= s[n][c] > top[n][c & 1] + kAbove;
-        if (kFp8) over |= s[n][c] + e[c >> 1] > ref[n][c & 1] + kAbove;
+        if (kFp8) over |= s[n][c] - top[n][c & 1] + e[c >> 1] > ref[n][c & 1] + kAbove;
       }
     if (__any_sync(kAll, over)) raise(s, e);
     uint32_t pb[NT][2];
@@ -723,12 +747,13 @@ struct Consumer {
       float x[4];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float base = top[n][c] == -CUDART_INF_F ? 0.f : top[n][c];
-        x[c] = ex2(s[n][c] - base), x[2 + c] = ex2(s[n][2 + c] - base);
+        const float base = !kFp8 && top[n][c] == -CUDART_INF_F ? 0.f : top[n][c];
+        const float y0 = s[n][c] - base, y1 = s[n][2 + c] - base;
+        x[c] = ex2(y0), x[2 + c] = ex2(y1);
         sum[n][c] += x[c] + x[2 + c];
         if (kFp8) {
-          const float from = (ref[n][c] == -CUDART_INF_F ? 0.f : ref[n][c]) - kBelow;
-          x[c] = ex2(s[n][c] + e[0] - from) * f[0], x[2 + c] = ex2(s[n][2 + c] + e[1] - from) * f[1];
+          const float from = ref[n][c] - kBelow;
+          x[c] = ex2(y0 + e[0] - from) * f[0], x[2 + c] = ex2(y1 + e[1] - from) * f[1];
         }
       }
       pb[n][0] = transpose8(pack2<kHalf>(x[0], x[1]));
@@ -753,10 +778,14 @@ struct Consumer {
       for (int c = 0; c < 2; ++c) {
         const float big = over_tokens(fmaxf(s[n][c], s[n][2 + c]));
         float less = 1.f;
-        if (big > top[n][c] + kAbove) less = ex2(top[n][c] - big), top[n][c] = big;
+        if (big > top[n][c] + kAbove) {
+          less = ex2(top[n][c] - big);
+          if (kFp8) ref[n][c] += top[n][c] - big;
+          top[n][c] = big;
+        }
         sum[n][c] *= less;
         if (kFp8) {
-          const float high = over_tokens(fmaxf(s[n][c] + e[0], s[n][2 + c] + e[1]));
+          const float high = over_tokens(fmaxf(s[n][c] - top[n][c] + e[0], s[n][2 + c] - top[n][c] + e[1]));
           less = 1.f;
           if (high > ref[n][c] + kAbove) less = ex2(ref[n][c] - high), ref[n][c] = high;
         }
@@ -781,7 +810,6 @@ struct Consumer {
         sum[n][c] += __shfl_xor_sync(kAll, sum[n][c], 4);
         sum[n][c] += __shfl_xor_sync(kAll, sum[n][c], 8);
         sum[n][c] += __shfl_xor_sync(kAll, sum[n][c], 16);
-        if (!kFp8) ref[n][c] = top[n][c];
         if (g == 0) {
           float* s = stats[warp][8 * n + 2 * t + c];
           s[0] = top[n][c], s[1] = ref[n][c], s[2] = sum[n][c];
@@ -794,10 +822,14 @@ struct Consumer {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float high = -CUDART_INF_F;
+        const int h = 8 * n + 2 * t + c;
+        float big = -CUDART_INF_F, high = -CUDART_INF_F;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) high = fmaxf(high, stats[mt * 4 + w][8 * n + 2 * t + c][1]);
-        const float f = ref[n][c] == -CUDART_INF_F ? 0.f : ex2(ref[n][c] - high);
+        for (int w = 0; w < 4; ++w) big = fmaxf(big, stats[mt * 4 + w][h][0]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          high = fmaxf(high, distance<kFp8>(stats[mt * 4 + w][h][0], stats[mt * 4 + w][h][1], big));
+        const float f = factor<kFp8>(top[n][c], ref[n][c], big, high);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) o[j][n][c] *= f, o[j][n][2 + c] *= f;
       }
@@ -838,7 +870,9 @@ struct Consumer {
         const int h = row % kWarpHeads;
         float big = -CUDART_INF_F, high = -CUDART_INF_F, total = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) big = fmaxf(big, st[w][h][0]), high = fmaxf(high, st[w][h][1]);
+        for (int w = 0; w < 4; ++w) big = fmaxf(big, st[w][h][0]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) high = fmaxf(high, distance<kFp8>(st[w][h][0], st[w][h][1], big));
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const float l = st[w][h][2];
@@ -871,15 +905,14 @@ struct Consumer {
     }
   }
 
-  // Eight values of a head's result: the sums x under `high`, the total under `big`.
+  // Eight values of a head's result: the total under `big`, the sums x under that and `high` above it.
   static __device__ __forceinline__ void write_out(const PagedAttnParams& p, int row, int head, int c0, float (&x)[8],
                                                    float big, float high, float total) {
     // no visible token: zeros, -inf
     const float f = total == 0.f ? 0.f : (kFp8 ? kSmallest : 1.f) / total;
     // of the size of the value scales, and 2^8 above them where the references of the scores and
     // of the weights have been raised apart: past 2^100 a second factor
-    const float apart = high - big;
-    const float unit = kFp8 ? ex2_small(fminf(apart, 100.f)) : 1.f, more = kFp8 ? ex2(fmaxf(apart - 100.f, 0.f)) : 1.f;
+    const float unit = kFp8 ? ex2_small(fminf(high, 100.f)) : 1.f, more = kFp8 ? ex2(fmaxf(high - 100.f, 0.f)) : 1.f;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -1002,13 +1035,16 @@ struct Consumer {
       float big = -CUDART_INF_F, high = -CUDART_INF_F, total = 0.f;
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r < active) big = fmaxf(big, st[r].x), high = fmaxf(high, st[r].y);
+        if (r < active) big = fmaxf(big, st[r].x);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < active) high = fmaxf(high, distance<kFp8>(st[r].x, st[r].y, big));
       float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int r = 0; r < 8; ++r)
         if (r < active) {
           total += st[r].x == -CUDART_INF_F ? st[r].z : st[r].z * ex2(st[r].x - big);
-          const float w = st[r].y == -CUDART_INF_F ? 0.f : ex2(st[r].y - high);
+          const float w = factor<kFp8>(st[r].x, st[r].y, big, high);
           x[0] += w * a[r].x, x[1] += w * a[r].y, x[2] += w * a[r].z, x[3] += w * a[r].w;
           x[4] += w * b[r].x, x[5] += w * b[r].y, x[6] += w * b[r].z, x[7] += w * b[r].w;
         }
@@ -1082,19 +1118,27 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   if (h >= p.group - group0) return;
   const int pieces = last - first + 1;
   auto part = [&](int i) { return p.ws + ((long long)(first + i) * 2 + (i == 0)) * hv * (D + 4); };
-  // the largest maximum and reference
-  float big = -CUDART_INF_F, high = -CUDART_INF_F;
+  // the largest references
+  constexpr bool kFp8 = KV == DSA_KV_FP8_E4M3;
+  float big = no_top<kFp8>(), high = no_distance<kFp8>();
+  auto larger = [&](float top, float ref) {
+    const float above = fmaxf(big, top);
+    high = fmaxf(distance<kFp8>(big, high, above), distance<kFp8>(top, ref, above)), big = above;
+  };
   for (int i = threadIdx.x; i < pieces; i += kJoinThreads) {
     const float4 s = *reinterpret_cast<const float4*>(part(i) + (long long)hv * D + h * 4);
-    big = fmaxf(big, s.x), high = fmaxf(high, s.y);
+    larger(s.x, s.y);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    big = fmaxf(big, __shfl_xor_sync(kAll, big, o)), high = fmaxf(high, __shfl_xor_sync(kAll, high, o));
+  for (int o = 16; o > 0; o >>= 1) {
+    const float x = __shfl_xor_sync(kAll, big, o), y = kFp8 ? __shfl_xor_sync(kAll, high, o) : 0.f;
+    larger(x, y);
+  }
   if (lane == 0) stat[warp] = make_float4(big, high, 0.f, 0.f);
   __syncthreads();
+  big = no_top<kFp8>(), high = no_distance<kFp8>();  // in one order, so that all threads have the same
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) big = fmaxf(big, stat[w].x), high = fmaxf(high, stat[w].y);
+  for (int w = 0; w < kJoinThreads / 32; ++w) larger(stat[w].x, stat[w].y);
   // four columns a thread, several groups of pieces
   const int col = threadIdx.x % kLanes * 4, group = threadIdx.x / kLanes;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1104,7 +1148,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     __syncthreads();
     if (threadIdx.x < n) {
       const float4 s = *reinterpret_cast<const float4*>(part(i0 + threadIdx.x) + (long long)hv * D + h * 4);
-      weight[threadIdx.x] = s.y == -CUDART_INF_F ? 0.f : ex2(s.y - high);
+      weight[threadIdx.x] = factor<kFp8>(s.x, s.y, big, high);
       total += s.x == -CUDART_INF_F ? s.z : s.z * ex2(s.x - big);
     }
     __syncthreads();

@@ -7,7 +7,7 @@ import torch
 import sparse_attention_paged_gb300 as lib
 from tests import paged_ref as ref
 from tests.test_gpu_block_select import Case as Selection
-from tests.test_gpu_paged_attention import WIDE, Case
+from tests.test_gpu_paged_attention import KINDS, WIDE, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -143,6 +143,38 @@ def test_fp8_largest_value_scales(dtype, rows, pages, every):
         c.pools.v.view(torch.uint8)[page, slot] = value.view(torch.uint8)
         c.pools.v_scale[page, 0, slot] = torch.where(late, 2.0 ** top, 1.0)
     c.run().check(rows=range(0, rows, 101))
+
+
+@pytest.mark.parametrize("kv,dtype", KINDS)
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 20, 2.0 ** 26, 2.0 ** 33])
+@pytest.mark.parametrize("lens,W", [([900], None), ([900, 64, 9000], WIDE)])
+def test_one_token_takes_all(kv, dtype, size, lens, W):
+    """Scores far past the steps of 1 that an fp32 has: the token with the largest is the result, whatever
+    the value scales beside it.  Off by two roundings of 16 bits (the result's, the weight's) and, of
+    2^-18 each at most, a few steps of exponents up to 2^7."""
+    c = Case(lens, 8, 2, 64, kv, dtype, seed=30, spread=0.0, W=W)
+    c.scale = size * (1 + 2.0 ** -9 / 3)                        # no power of two
+    c.q[:] = 0
+    c.q[..., 5] = 1.0 + 2.0 ** -7
+    g = torch.Generator().manual_seed(31)
+    for r, n in enumerate(lens):
+        page, slot = c.tokens(r, 0)
+        best = torch.randint(0, n, (1,), generator=g)
+        key = torch.zeros((n, 2, 64))
+        key[:, :, 5] = 0.5 + 0.25 * torch.rand((n, 1), generator=g)
+        key[best, :, 5] = 1.375
+        value = torch.randn((n, 2, 64), generator=g) * torch.exp2(torch.randint(-6, 7, (n, 2, 1), generator=g).float())
+        c.pools.put(page, slot, key.to(c.dtype), value.to(c.dtype))
+        c.best = [*getattr(c, "best", []), (page[best], slot[best])]
+    c.run()
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    step = torch.finfo(c.dtype).eps / 2 + (2.0 ** -8 if kv == "bf16" else 2.0 ** -11) + 2.0 ** -14
+    for r, at in enumerate(c.best):
+        _, value = c.pools.get(*at)
+        want = value[0].repeat_interleave(4, 0)
+        off = (c.out[r].double().cpu() - want).abs()
+        assert (off <= step * want.abs() + 2.0 ** -25).all(), (r, float((off / want.abs()).max()))
 
 
 # ---- the widest shared table -----------------------------------------------------------------
