@@ -52,7 +52,7 @@
 // (6.9 TB/s, a little above the rate of a copy, half of which are writes); one row of
 // 131,072 fp8 tokens, 64 heads, 52 (277 MB: 41 at that rate, start 5, last results and
 // join 6); 64 rows of 32 listed fp8 pages 55; 1,024 prefill rows of 16 listed bf16 pages
-// 140 back to back in a graph, 145 as calls (2.1 GB through L2, 15 TB/s); one row of
+// 141 back to back in a graph, 145 as calls (2.1 GB through L2, 15 TB/s); one row of
 // 1,024 tokens 6.5 (32 heads on 8).
 //
 // Warps: the last one walks the slice (lengths, list, table; 32 pages at a
